@@ -15,7 +15,9 @@ The functions carry the C names:
   gc_all_reduce, gc_reduce_scatter, gc_all_gather, gc_all_to_all,
   gc_all_reduce_scratch_bytes, gc_bucket_plan_create / _query / _destroy,
   gc_bucket_pack, gc_bucket_unpack, gc_bucket_all_reduce, gc_status_string,
-  gc_version, gc_last_hip_error
+  gc_version, gc_last_hip_error; the MoE calls gc_moe_route, gc_moe_dispatch,
+  gc_moe_combine and its gradient, gc_moe_ffn and its backward; gc_rms_norm and
+  its backward; gc_mx8_pack, gc_mx8_unpack
 plus BucketPlan, a small owner of a gc_bucket_plan handle; RankArena, which
 gives each rank its own region of HBM; gc_rank_buffers, which lays N rank
 buffers out in one allocation with a per-rank stagger; and gc_pointers, which
@@ -47,13 +49,13 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 GC_MAX_RANKS = 64
 GC_OK, GC_ERR_INVALID_ARG, GC_ERR_UNSUPPORTED, GC_ERR_HIP, GC_ERR_NO_MEMORY = range(5)
-GC_INT32, GC_FP32, GC_BF16 = 0, 1, 2
+GC_INT32, GC_FP32, GC_BF16, GC_MX8 = 0, 1, 2, 3
 GC_SUM, GC_AVG = 0, 1
 GC_ORDER_RING, GC_ORDER_RANK, GC_ORDER_RING_WIRE = 0, 1, 2
 GC_AR_FUSED, GC_AR_RS_AG = 0, 1
 SIZE_MAX = (1 << 64) - 1
 
-_DTYPE = {"int32": GC_INT32, "fp32": GC_FP32, "bf16": GC_BF16}
+_DTYPE = {"int32": GC_INT32, "fp32": GC_FP32, "bf16": GC_BF16, "mx8": GC_MX8}
 _OP = {"sum": GC_SUM, "avg": GC_AVG}
 _ORDER = {"ring": GC_ORDER_RING, "rank": GC_ORDER_RANK, "ring_wire": GC_ORDER_RING_WIRE}
 _ALGO = {"fused": GC_AR_FUSED, "rs_ag": GC_AR_RS_AG}
@@ -92,6 +94,20 @@ _c_plan_query = _sig("gc_bucket_plan_query", _int, _vp, ctypes.POINTER(_int), ct
 _c_pack = _sig("gc_bucket_pack", _int, _vp, _int, _VPP, _VPP, _int, _vp)
 _c_unpack = _sig("gc_bucket_unpack", _int, _vp, _int, _VPP, _VPP, _int, _vp)
 _c_bucket_ar = _sig("gc_bucket_all_reduce", _int, _vp, _int, _VPP, _int, _int, _int, _vp, _vp)
+_c_moe_combine_bwd = _sig("gc_moe_combine_backward", _int, _VPP, _VPP, _I64P, _VPP, _VPP, _I64P, _int, _int, _sz, _int,
+                          _VPP, _VPP, _vp)
+_c_mx8_row = _sig("gc_mx8_row_bytes", _sz, _sz)
+_c_mx8_pack = _sig("gc_mx8_pack", _int, _VPP, _I64P, _int, _sz, _int, _VPP, _vp)
+_c_mx8_unpack = _sig("gc_mx8_unpack", _int, _VPP, _I64P, _int, _sz, _int, _VPP, _vp)
+_c_norm = _sig("gc_rms_norm", _int, _VPP, _VPP, _VPP, _I64P, _int, _sz, ctypes.c_float, _int, _VPP, _VPP, _int, _VPP, _vp)
+_c_norm_bwd_scratch = _sig("gc_rms_norm_backward_scratch_bytes", _sz, _I64P, _int, _sz)
+_c_norm_bwd = _sig("gc_rms_norm_backward", _int, _VPP, _VPP, _VPP, _VPP, _VPP, _I64P, _int, _sz, _int, _VPP, _VPP, _vp,
+                   _sz, _vp)
+_c_ffn_scratch = _sig("gc_moe_ffn_scratch_bytes", _sz, _I64P, _int, _int, _sz, _sz, _int, _int)
+_c_ffn = _sig("gc_moe_ffn", _int, _VPP, _int, _I64P, _vp, _int, _int, _sz, _sz, _VPP, _VPP, _VPP, _VPP, _int, _VPP, _vp,
+              _sz, _vp)
+_c_ffn_bwd = _sig("gc_moe_ffn_backward", _int, _VPP, _VPP, _int, _VPP, _int, _I64P, _vp, _int, _int, _sz, _sz, _VPP, _VPP,
+                  _VPP, _VPP, _VPP, _VPP, _VPP, _int, _vp, _sz, _vp)
 _c_plan_destroy = _sig("gc_bucket_plan_destroy", None, _vp)
 _c_status = _sig("gc_status_string", ctypes.c_char_p, _int)
 _c_version = _sig("gc_version", _int)
@@ -172,7 +188,7 @@ def _dtype_code(x):
     if isinstance(x, int):
         return x
     import torch
-    return {torch.bfloat16: GC_BF16, torch.float32: GC_FP32, torch.int32: GC_INT32}[x]
+    return {torch.bfloat16: GC_BF16, torch.float32: GC_FP32, torch.int32: GC_INT32, torch.uint8: GC_MX8}[x]
 
 
 def _enum(table, x):
@@ -442,6 +458,145 @@ def gc_moe_combine(expert_out, expert_rows, dest, weights, ntokens, topk, hidden
                           int(topk), int(hidden), t, _bufs(out, n, [max(0, int(x)) * rb for x in ntokens], "out"),
                           _stream(stream, _first(out))), "gc_moe_combine")
     return out
+
+
+def gc_moe_combine_backward(dout, expert_out, expert_rows, dest, weights, ntokens, topk, hidden, dtype, dexpert, dweights,
+                            stream=None):
+    """Gradient of gc_moe_combine: dexpert rows = weights * dout, dweights = the rows' dot products (fp32)."""
+    n, t = len(ntokens), _dtype_code(dtype)
+    rb = max(0, int(hidden)) * _ES.get(t, 0)
+    rows = [max(0, int(r)) * rb for r in expert_rows]
+    _check(_c_moe_combine_bwd(_bufs(dout, n, [max(0, int(x)) * rb for x in ntokens], "dout"),
+                              _bufs(expert_out, n, rows, "expert_out"), _i64_array(expert_rows),
+                              _bufs(dest, n, _per_route(ntokens, topk, 8), "dest"),
+                              _bufs(weights, n, _per_route(ntokens, topk, 4), "weights"), _i64_array(ntokens), n,
+                              int(topk), int(hidden), t, _bufs(dexpert, n, rows, "dexpert"),
+                              _bufs(dweights, n, _per_route(ntokens, topk, 4), "dweights"),
+                              _stream(stream, _first(dexpert))), "gc_moe_combine_backward")
+    return dexpert, dweights
+
+
+# ------------------------------------------------------------------ 8-bit rows and norm
+
+def gc_mx8_row_bytes(n):
+    """Bytes of an 8-bit row of n values: e4m3 codes, a scale byte per 32 values, zeros to a multiple of 16."""
+    return int(_c_mx8_row(max(0, int(n))))
+
+
+def _row_bytes(n, t):
+    return gc_mx8_row_bytes(n) if t == GC_MX8 else max(0, int(n)) * _ES.get(t, 0)
+
+
+def _rows_of(counts, row):
+    return [max(0, int(c)) * row for c in counts]
+
+
+def gc_mx8_pack(x, rows, n, packed, dtype=None, stream=None):
+    """x[r]: rows[r] rows of n bf16 or fp32 values -> packed[r]: as many 8-bit rows (uint8)."""
+    N, t = len(rows), _infer_dtype(x, dtype)
+    _check(_c_mx8_pack(_bufs(x, N, _rows_of(rows, _row_bytes(n, t)), "x"), _i64_array(rows), N, int(n), t,
+                       _bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed"),
+                       _stream(stream, _first(packed))), "gc_mx8_pack")
+    return packed
+
+
+def gc_mx8_unpack(packed, rows, n, out, dtype=None, stream=None):
+    """Inverse of gc_mx8_pack: the values that 8-bit rows stand for, exact in bf16 and fp32."""
+    N, t = len(rows), _infer_dtype(out, dtype)
+    _check(_c_mx8_unpack(_bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed"), _i64_array(rows), N,
+                         int(n), t, _bufs(out, N, _rows_of(rows, _row_bytes(n, t)), "out"),
+                         _stream(stream, _first(out))), "gc_mx8_unpack")
+    return out
+
+
+def gc_rms_norm(x, weight, ntokens, hidden, y, residual=None, sum_out=None, rstd=None, eps=1e-6, dtype=None,
+                y_dtype=None, stream=None):
+    """s = x + residual; y = s / sqrt(mean(s^2) + eps) * weight, per row.  y: rows of x's type, or uint8 buffers
+    for 8-bit rows.  sum_out (may be x or residual) takes s, rstd [ntokens] fp32 what the backward needs."""
+    N, t = len(ntokens), _infer_dtype(x, dtype)
+    yt = _infer_dtype(y, y_dtype)
+    full = _rows_of(ntokens, _row_bytes(hidden, t))
+    one = [_row_bytes(hidden, t) if int(c) > 0 else 0 for c in ntokens]
+    _check(_c_norm(_bufs(x, N, full, "x"), _bufs(residual, N, full, "residual"), _bufs(weight, N, one, "weight"),
+                   _i64_array(ntokens), N, int(hidden), float(eps), t, _bufs(sum_out, N, full, "sum_out"),
+                   _bufs(y, N, _rows_of(ntokens, _row_bytes(hidden, yt)), "y"), yt,
+                   _bufs(rstd, N, _rows_of(ntokens, 4), "rstd"), _stream(stream, _first(y))), "gc_rms_norm")
+    return y
+
+
+def gc_rms_norm_backward_scratch_bytes(ntokens, hidden):
+    """Scratch bytes gc_rms_norm_backward needs (0 if the sizes are invalid)."""
+    return int(_c_norm_bwd_scratch(_i64_array(ntokens), len(ntokens), max(0, int(hidden))))
+
+
+def gc_rms_norm_backward(dy, sum, weight, rstd, ntokens, hidden, dx, dweight, scratch, dsum=None, scratch_bytes=None,
+                         dtype=None, stream=None):
+    """dx (of x and residual alike; may be dy or dsum) and dweight[r] (fp32 [hidden], one per rank) from dy and,
+    optionally, dsum, the gradient arriving at the forward's sum_out."""
+    N, t = len(ntokens), _infer_dtype(dy, dtype)
+    if scratch_bytes is None:
+        scratch_bytes = scratch.numel() * scratch.element_size()
+    full = _rows_of(ntokens, _row_bytes(hidden, t))
+    one = [_row_bytes(hidden, t) if int(c) > 0 else 0 for c in ntokens]
+    _check(_c_norm_bwd(_bufs(dy, N, full, "dy"), _bufs(dsum, N, full, "dsum"), _bufs(sum, N, full, "sum"),
+                       _bufs(weight, N, one, "weight"), _bufs(rstd, N, _rows_of(ntokens, 4), "rstd"),
+                       _i64_array(ntokens), N, int(hidden), t, _bufs(dx, N, full, "dx"),
+                       _bufs(dweight, N, max(0, int(hidden)) * 4, "dweight"),
+                       _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes), _stream(stream, _first(dx))),
+           "gc_rms_norm_backward")
+    return dx, dweight
+
+
+# ------------------------------------------------------------------ experts
+
+def gc_moe_ffn_scratch_bytes(rows, experts_per_rank, hidden, inter, x_dtype="bf16", backward=False):
+    """Scratch bytes gc_moe_ffn (or gc_moe_ffn_backward) needs for these row counts (0 if the sizes are invalid)."""
+    return int(_c_ffn_scratch(_i64_array(rows), len(rows), int(experts_per_rank), max(0, int(hidden)),
+                              max(0, int(inter)), _dtype_code(x_dtype), int(bool(backward))))
+
+
+def _ffn_common(rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_down, scratch, scratch_bytes):
+    N, E = len(rows), max(0, int(experts_per_rank))
+    w = E * max(0, int(hidden)) * max(0, int(inter))
+    if scratch_bytes is None:
+        scratch_bytes = scratch.numel() * scratch.element_size()
+    return (N, w, _buf(splits, N * N * E * 8, "splits"),
+            [_bufs(p, N, 2 * w, k) for p, k in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))],
+            _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes))
+
+
+def gc_moe_ffn(x, rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_down, y, scratch, saved=None,
+               x_dtype=None, saved_dtype=None, scratch_bytes=None, stream=None):
+    """The experts' gated feed-forward on the receive layout: y = (silu(x Wg^T) * (x Wu^T)) Wd^T per expert block.
+    x[d], y[d]: rows[d] rows of hidden (x: bf16, or uint8 8-bit rows); splits: the device table of gc_moe_route;
+    w_gate[d], w_up[d] [E][inter][hidden] and w_down[d] [E][hidden][inter] bf16; saved[d]: rows of 2 * inter values
+    (gate then up, bf16 or 8-bit rows) for the backward, or None."""
+    N, _w, sp, ws, sc, scb = _ffn_common(rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_down, scratch,
+                                         scratch_bytes)
+    xt = _infer_dtype(x, x_dtype)
+    st = GC_BF16 if saved is None else _infer_dtype(saved, saved_dtype)
+    _check(_c_ffn(_bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x"), xt, _i64_array(rows), sp, N,
+                  int(experts_per_rank), int(hidden), int(inter), *ws,
+                  _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved"), st,
+                  _bufs(y, N, _rows_of(rows, 2 * max(0, int(hidden))), "y"), sc, scb, _stream(stream, _first(y))),
+           "gc_moe_ffn")
+    return y
+
+
+def gc_moe_ffn_backward(dy, x, saved, rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_down, dx, dw_gate,
+                        dw_up, dw_down, scratch, x_dtype=None, saved_dtype=None, dw_dtype=None, scratch_bytes=None,
+                        stream=None):
+    """Backward of gc_moe_ffn from its checkpoints: dx rows and the three weight gradients (bf16 or fp32)."""
+    N, w, sp, ws, sc, scb = _ffn_common(rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_down, scratch,
+                                        scratch_bytes)
+    xt, st, wt = _infer_dtype(x, x_dtype), _infer_dtype(saved, saved_dtype), _infer_dtype(dw_gate, dw_dtype)
+    row = _rows_of(rows, 2 * max(0, int(hidden)))
+    dws = [_bufs(p, N, w * _ES.get(wt, 0), k) for p, k in ((dw_gate, "dw_gate"), (dw_up, "dw_up"), (dw_down, "dw_down"))]
+    _check(_c_ffn_bwd(_bufs(dy, N, row, "dy"), _bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x"), xt,
+                      _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved"), st, _i64_array(rows), sp,
+                      N, int(experts_per_rank), int(hidden), int(inter), *ws, _bufs(dx, N, row, "dx"), *dws, wt, sc, scb,
+                      _stream(stream, _first(dx))), "gc_moe_ffn_backward")
+    return dx, dw_gate, dw_up, dw_down
 
 
 # ------------------------------------------------------------------ HBM layout

@@ -152,4 +152,132 @@ gc_status moe_route_static_scratch(hipStream_t stream, void** ptr);
 gc_status launch_moe_dispatch(const MoeMoveCall& call);
 gc_status launch_moe_combine(const MoeMoveCall& call);
 
+// ---- operators of the layer around the experts (norm.hip, mx8.hip, moe_grad.hip, ffn.hip)
+
+// Bytes of an 8-bit row of n values: codes, a scale per 32 values, zeros to a multiple of 16.
+inline uint64_t mx8_row_bytes(uint64_t n) { return (n + (n + 31) / 32 + 15) / 16 * 16; }
+
+// Token rows of every rank (see gc_rms_norm); res, sum and rstd may be null.
+struct NormCall {
+  const void* const* x;
+  const void* const* res;
+  const void* const* w;
+  const int64_t* tokens;
+  int nranks;
+  uint64_t hidden;
+  float eps;
+  gc_dtype t;
+  void* const* sum;
+  void* const* y;
+  gc_dtype y_t;
+  float* const* rstd;
+  hipStream_t stream;
+};
+gc_status launch_rms_norm(const NormCall& call);
+
+struct NormBackwardCall {
+  const void* const* dy;
+  const void* const* dsum;
+  const void* const* sum;
+  const void* const* w;
+  const float* const* rstd;
+  const int64_t* tokens;
+  int nranks;
+  uint64_t hidden;
+  gc_dtype t;
+  void* const* dx;
+  float* const* dw;
+  float* partial;         // [blocks][hidden] partial weight gradients
+  int64_t rows_per_block; // consecutive rows of one rank that one block sums
+  hipStream_t stream;
+};
+gc_status launch_rms_norm_backward(const NormBackwardCall& call);
+
+// Rows of n values of type t to 8-bit rows (unpack == false) or back.
+struct Mx8Call {
+  const void* const* src;
+  void* const* dst;
+  const int64_t* rows;
+  int nranks;
+  uint64_t n;
+  gc_dtype t;
+  bool unpack;
+  hipStream_t stream;
+};
+gc_status launch_mx8(const Mx8Call& call);
+
+struct MoeCombineBackwardCall {
+  const void* const* dout;
+  const void* const* y;
+  const int64_t* y_rows;
+  const int32_t* const* dest;
+  const float* const* weights;
+  const int64_t* tokens;
+  int nranks;
+  int topk;
+  uint64_t hidden;
+  gc_dtype t;
+  void* const* dy;
+  float* const* dweights;
+  hipStream_t stream;
+};
+gc_status launch_moe_combine_backward(const MoeCombineBackwardCall& call);
+
+// Experts (see gc_moe_ffn).  Every per-rank pointer list may be null where a
+// direction does not use it.
+struct FfnCall {
+  const void* const* x;
+  gc_dtype x_t;
+  const int64_t* rows;
+  const int64_t* splits;
+  int nranks;
+  int experts_per_rank;
+  uint64_t hidden;
+  uint64_t inter;
+  const void* const* w_gate;
+  const void* const* w_up;
+  const void* const* w_down;
+  void* const* saved;        // written by the forward, read by the backward
+  gc_dtype saved_t;
+  void* const* y;            // forward: output rows; backward: dx rows
+  const void* const* dy;     // backward only, as the rest
+  void* const* dw_gate;
+  void* const* dw_up;
+  void* const* dw_down;
+  gc_dtype dw_t;
+  void* scratch;
+  hipStream_t stream;
+};
+
+// One expert's block of rows, as the plan kernel leaves it for the products.
+struct FfnSeg {
+  const char* x;             // first row of each buffer's block
+  const char* dy;
+  char* saved;
+  char* y;
+  const char* w_gate;        // this expert's weights and their gradients
+  const char* w_up;
+  const char* w_down;
+  char* dw_gate;
+  char* dw_up;
+  char* dw_down;
+  int64_t row;               // first row in the scratch matrices (all ranks' rows in order)
+  int32_t rows;
+  int32_t tile0;             // first row tile
+};
+
+// Row tiles and the scratch areas of a call, from its sizes alone.
+struct FfnGeom {
+  int64_t rows = 0;          // of all ranks
+  int32_t segs = 0;          // experts of all ranks
+  int32_t tile_rows = 0;     // rows per tile of the row products
+  int64_t tiles = 0;         // most row tiles the experts' blocks can make
+  uint64_t map = 0, x = 0, h = 0, g = 0, bytes = 0;  // offsets (segment table at 0) and total
+};
+FfnGeom ffn_geom(const int64_t* rows, int nranks, int experts_per_rank, uint64_t hidden, uint64_t inter, gc_dtype x_t,
+                 bool backward);
+
+gc_status launch_moe_ffn(const FfnCall& call);
+gc_status launch_moe_ffn_backward(const FfnCall& call);
+
 }  // namespace gci

@@ -82,7 +82,12 @@ typedef enum {
   GC_ERR_NO_MEMORY = 4      /* host allocation failed (bucket plan)                           */
 } gc_status;
 
-typedef enum { GC_INT32 = 0, GC_FP32 = 1, GC_BF16 = 2 } gc_dtype;
+typedef enum {
+  GC_INT32 = 0,
+  GC_FP32 = 1,
+  GC_BF16 = 2,
+  GC_MX8 = 3                /* 8-bit rows with scales (see gc_mx8_row_bytes); not for collectives */
+} gc_dtype;
 typedef enum { GC_SUM = 0, GC_AVG = 1 } gc_op;                 /* GC_AVG: floating types only */
 typedef enum { GC_ORDER_RING = 0, GC_ORDER_RANK = 1, GC_ORDER_RING_WIRE = 2 } gc_order;
 typedef enum { GC_AR_FUSED = 0, GC_AR_RS_AG = 1 } gc_ar_algo;
@@ -226,7 +231,8 @@ gc_status gc_fsdp2_all_gather(const void* const* shards, void* const* params, co
  * rank and dispatched with All-to-AllV, the local experts run, a second
  * All-to-AllV brings the results back and the token order is restored).
  * Ranks hold E = experts_per_rank experts each; global expert g lives on rank
- * g / E as local expert g % E.  The router and the experts are the caller's.
+ * g / E as local expert g % E.  The router is the caller's; the experts may be
+ * gc_moe_ffn or the caller's.
  *
  * A route is one (token, k) pair of a source rank, numbered t * topk + k.
  * Its destination row in rank d's receive buffer follows gc_all_to_all's
@@ -317,6 +323,149 @@ gc_status gc_moe_dispatch(const void* const* tokens, const int64_t* ntokens, con
 gc_status gc_moe_combine(const void* const* expert_out, const int64_t* expert_rows, const int32_t* const* dest,
                          const float* const* weights, const int64_t* ntokens, int nranks, int topk,
                          size_t hidden, gc_dtype t, void* const* out, hipStream_t stream);
+
+/*
+ * Gradient of gc_moe_combine (its arguments, with dout the gradient of out):
+ *   dexpert[d][r]            = weights[s][t * topk + k] * dout[s][t], rounded once to t,
+ *   dweights[s][t * topk + k] = sum over the row of dout[s][t] * expert_out[d][r] (fp32),
+ *   (d, r) = dest[s][t * topk + k].
+ * Entries of dest outside the expert buffers get a zero dweights entry and
+ * write no row; rows of dexpert that no route names keep what they held.  A
+ * plan of gc_moe_route names each row once.  The gradient of gc_moe_dispatch
+ * is gc_moe_combine of the rows' gradients with every weight 1.
+ *   dexpert[d]   DEVICE [expert_rows[d]] rows of type t.
+ *   dweights[s]  DEVICE fp32 [ntokens[s] * topk].
+ * t is GC_BF16 or GC_FP32.  Output buffers must not overlap anything else.
+ */
+gc_status gc_moe_combine_backward(const void* const* dout, const void* const* expert_out, const int64_t* expert_rows,
+                                  const int32_t* const* dest, const float* const* weights, const int64_t* ntokens,
+                                  int nranks, int topk, size_t hidden, gc_dtype t, void* const* dexpert,
+                                  float* const* dweights, hipStream_t stream);
+
+/*
+ * 8-bit rows (GC_MX8).  A row of n values is n e4m3 bytes, one scale byte per
+ * 32 values (the last block may be short), then zero bytes up to a multiple of
+ * 16: gc_mx8_row_bytes(n) in all, so a row moves through gc_moe_dispatch and
+ * gc_all_to_all as row_bytes of plain bytes.  Value i stands for
+ * e4m3(byte i) * 2^(scale byte(i / 32) - 127).  The encoder takes, per block,
+ * a = the largest finite magnitude and e = the smallest integer with
+ * a <= 448 * 2^e, clamped to [-117, 120], stores e + 127, and rounds each
+ * value * 2^-e to e4m3 (nearest, ties to even): at most 2^-4 of the value off,
+ * or 2^(e-10) where it is below 2^(e-6).  Every finite code is exact in bf16,
+ * except that a value within half a step of 2^128 rounds up to it and decodes
+ * as infinity.  Infinities and NaN become NaN and leave the rest of their
+ * block unaffected.  Buffers of 8-bit rows are 16-byte aligned.
+ */
+size_t gc_mx8_row_bytes(size_t n);
+
+/*
+ * Activation checkpoints in 8 bits: rows[r] rows of n values of type t
+ * (GC_BF16 or GC_FP32) on every rank, to 8-bit rows and back.  Unpacked values
+ * are exact in either type.  Source and destination must not overlap.
+ *   x[r], out[r]  DEVICE [rows[r]] rows of n elements of t, stored densely.
+ *   packed[r]     DEVICE [rows[r]] rows of gc_mx8_row_bytes(n) bytes.
+ *   rows          HOST int64 [nranks].  Rows of all ranks below 2^31.
+ */
+gc_status gc_mx8_pack(const void* const* x, const int64_t* rows, int nranks, size_t n, gc_dtype t,
+                      void* const* packed, hipStream_t stream);
+
+gc_status gc_mx8_unpack(const void* const* packed, const int64_t* rows, int nranks, size_t n, gc_dtype t,
+                        void* const* out, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of token rows with the residual's addition.  Per row,
+ *   s = x + residual, rounded to t (x itself where residual is NULL),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),   y = s * rstd * weight.
+ * s is normed as it is stored, so that the backward pass sees what was normed;
+ * sums and rstd are fp32, y is rounded once.
+ *   x[r], residual[r]  DEVICE [ntokens[r]] rows of hidden elements of t
+ *                      (GC_BF16 or GC_FP32); residual may be NULL.
+ *   weight[r]          DEVICE [hidden] of t; ranks may share one buffer.
+ *   sum_out[r]         s, rows of t; NULL: not written.  May be x[r] or
+ *                      residual[r] itself.
+ *   y[r]               rows of y_t: t, or GC_MX8 (8-bit rows, from y in fp32).
+ *   rstd[r]            DEVICE fp32 [ntokens[r]], for the backward; may be NULL.
+ * Rows of all ranks below 2^31.  A zero row gives zeros.  Other overlaps of
+ * outputs with anything are refused.
+ */
+gc_status gc_rms_norm(const void* const* x, const void* const* residual, const void* const* weight,
+                      const int64_t* ntokens, int nranks, size_t hidden, float eps, gc_dtype t,
+                      void* const* sum_out, void* const* y, gc_dtype y_t, float* const* rstd, hipStream_t stream);
+
+/* Scratch bytes gc_rms_norm_backward needs (0 if the sizes are invalid). */
+size_t gc_rms_norm_backward_scratch_bytes(const int64_t* ntokens, int nranks, size_t hidden);
+
+/*
+ * Backward of gc_rms_norm.  With n = s * rstd and d = dy * weight, per row
+ *   dx = rstd * (d - n * mean(d * n)) + dsum, rounded once to t: the gradient
+ *        of x and of residual alike, and
+ *   dweight[r] = sum over rank r's rows of dy * n, fp32: one gradient per
+ *        rank, for the data-parallel all-reduce.
+ * The sums' order is fixed by the sizes alone, so runs repeat bit for bit.
+ *   dy[r], sum[r]  rows of t; sum is the forward's sum_out (x without residual).
+ *   dsum[r]        rows of t: what arrives at sum_out from later layers; may be NULL.
+ *   dx[r]          rows of t; may be dy[r] or dsum[r] itself.
+ *   dweight[r]     DEVICE fp32 [hidden]; zeros for a rank without tokens.
+ *   scratch        DEVICE, 256-byte aligned, gc_rms_norm_backward_scratch_bytes().
+ */
+gc_status gc_rms_norm_backward(const void* const* dy, const void* const* dsum, const void* const* sum,
+                               const void* const* weight, const float* const* rstd, const int64_t* ntokens,
+                               int nranks, size_t hidden, gc_dtype t, void* const* dx, float* const* dweight,
+                               void* scratch, size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * The experts: a gated feed-forward block on the receive layout (rows by local
+ * expert, then source), so it takes what gc_moe_dispatch wrote and leaves what
+ * gc_moe_combine reads.  For each row of local expert e of rank d,
+ *   gate = x Wg^T,  up = x Wu^T,  h = silu(gate) * up,  y = h Wd^T.
+ *   x[d]       DEVICE [rows[d]] rows of hidden values: GC_BF16, or GC_MX8 as
+ *              the norm or gc_mx8_pack wrote them and dispatch moved them.
+ *   rows       HOST int64 [nranks]: rows of rank d's buffers.
+ *   splits     DEVICE int64 [nranks][nranks][E], as gc_moe_route writes it; it
+ *              is read on the device.  Rank d's expert e takes the next
+ *              (sum over s of splits[s][d][e]) rows; negative entries count as
+ *              0 and blocks end at rows[d].
+ *   w_gate[d], w_up[d]  DEVICE bf16 [E][inter][hidden];  w_down[d] [E][hidden][inter].
+ *   saved[d]   the checkpoint for the backward: rows of 2 * inter values, gate
+ *              then up, as GC_BF16 or GC_MX8 rows; NULL (saved_t ignored):
+ *              nothing is kept (serving).
+ *   y[d]       DEVICE bf16 [rows[d]] rows of hidden.
+ *   scratch    DEVICE, 256-byte aligned, gc_moe_ffn_scratch_bytes() bytes;
+ *              calls that may run at once need one each.
+ * Sums are fp32; h is rounded to bf16 (it feeds the second product), gate and
+ * up only where they are saved.  Rows of y and saved that no expert takes keep
+ * what they held.  hidden is a multiple of 8, inter of 8 (of 32 with GC_MX8
+ * checkpoints), both at most 2^20; nranks * E <= 8192; rows of all ranks below
+ * 2^31 (GC_ERR_UNSUPPORTED beyond).  All buffers are 16-byte aligned; outputs
+ * and scratch must not overlap anything else.
+ */
+size_t gc_moe_ffn_scratch_bytes(const int64_t* rows, int nranks, int experts_per_rank, size_t hidden, size_t inter,
+                                gc_dtype x_t, int backward);
+
+gc_status gc_moe_ffn(const void* const* x, gc_dtype x_t, const int64_t* rows, const int64_t* splits, int nranks,
+                     int experts_per_rank, size_t hidden, size_t inter, const void* const* w_gate,
+                     const void* const* w_up, const void* const* w_down, void* const* saved, gc_dtype saved_t,
+                     void* const* y, void* scratch, size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Backward of gc_moe_ffn from its checkpoints (x and saved in the types they
+ * were kept in; the gradient is that of the values they stand for):
+ *   dh = dy Wd,  dgate = dh * up * silu'(gate),  dup = dh * silu(gate),
+ *   dx = dgate Wg + dup Wu,
+ *   dWg = dgate^T x,  dWu = dup^T x,  dWd = dy^T h   per expert.
+ * dgate, dup and h are rounded to bf16 between the products; sums are fp32.
+ *   dx[d]                   DEVICE bf16 rows of hidden; rows that no expert takes keep
+ *                           what they held.
+ *   dw_gate, dw_up, dw_down  shaped as the weights, of type dw_t (GC_BF16 or
+ *                           GC_FP32), overwritten; zeros for an expert without rows.
+ * Limits, alignment, scratch (backward = 1) and overlaps as gc_moe_ffn.
+ */
+gc_status gc_moe_ffn_backward(const void* const* dy, const void* const* x, gc_dtype x_t, const void* const* saved,
+                              gc_dtype saved_t, const int64_t* rows, const int64_t* splits, int nranks,
+                              int experts_per_rank, size_t hidden, size_t inter, const void* const* w_gate,
+                              const void* const* w_up, const void* const* w_down, void* const* dx,
+                              void* const* dw_gate, void* const* dw_up, void* const* dw_down, gc_dtype dw_t,
+                              void* scratch, size_t scratch_bytes, hipStream_t stream);
 
 /*
  * Bucket plan: DDP gradient buckets (AIG6 §6.2.4; NXMR §5.1) and the FSDP
