@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "rows.h"
 
@@ -162,11 +163,11 @@ struct GemmArgs {
   const int32_t* map;
   char* h;                 // scratch [rows][F] bf16
   char* g;                 // scratch [rows][2F] bf16: dgate then dup
-  int64_t mtiles;          // row tiles (row products) or output row tiles of one expert (weight gradients)
-  int64_t ntiles;
+  uint32_t mtiles;         // row tiles (row products) or output row tiles of one expert (weight gradients)
+  uint32_t ntiles;
   uint64_t H, F;
   uint64_t saved_row;
-  int32_t segs_n;
+  uint32_t segs_n;
 };
 
 // Where one operand's tile comes from.  kc: the summed index is contiguous in
@@ -176,6 +177,25 @@ struct Side {
   const char* p2;          // second half: of the tile's rows (kc) or of the summed index
   uint64_t ld;             // bytes per stored row
   int32_t rows;            // valid rows of the tile (kc), or valid values of a row (else)
+};
+
+// The plan's tables were written by an earlier kernel and do not change here:
+// read through the constant address space they come by scalar loads and stay
+// in scalar registers, where the operands' buffer descriptors need them (the
+// compiler cannot tell by itself, because the kernel also writes memory).
+typedef const __attribute__((address_space(4))) Seg ConstSeg;
+__device__ __forceinline__ ConstSeg* as_constant(const Seg* p) { return (ConstSeg*)(uintptr_t)p; }
+__device__ __forceinline__ const __attribute__((address_space(4))) int32_t* as_constant(const int32_t* p) {
+  return (const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// One tile of a product: its operands, the summed length, where it goes.
+struct Tile {
+  ConstSeg* sg;
+  Side A, B;
+  uint32_t K;              // below 2^31
+  int64_t m0, n0;
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor's range: the load gives zeros
@@ -192,7 +212,7 @@ __device__ __forceinline__ void lds_load(const char* base, char* dst, uint32_t o
 // c ^ ((r >> 1) & 7) of the row's 128 bytes, so that 16 lanes reading one
 // chunk of 16 rows touch all 64 banks.  A wavefront's load covers eight rows.
 template <int ROWS, bool HALVES>
-__device__ __forceinline__ void load_kc(char* dst, const Side& s, int64_t k0, int64_t K, int w, int lane) {
+__device__ __forceinline__ void load_kc(char* dst, const Side& s, uint32_t k0, uint32_t K, int w, int lane) {
   constexpr int L = ROWS / 64;  // loads per wavefront
 #pragma unroll
   for (int i = 0; i < L; ++i) {
@@ -202,19 +222,19 @@ __device__ __forceinline__ void load_kc(char* dst, const Side& s, int64_t k0, in
     const int rr = second ? r - ROWS / 2 : r;
     const bool ok = rr < s.rows && k0 + c * 8 < K;
     const uint32_t off = static_cast<uint32_t>(rr * s.ld) + c * 16;
-    lds_load((second ? s.p2 : s.p) + k0 * 2, dst + q * 1024, ok ? off : kOutside);
+    lds_load((second ? s.p2 : s.p) + static_cast<uint64_t>(k0) * 2, dst + q * 1024, ok ? off : kOutside);
   }
 }
 
 // Tile of 64 summed indices x 256 values: 512-byte rows whose 32-byte unit u
 // sits at u ^ 2 (k & 3), so that the four rows a transposing read takes
 // together lie in different banks.  A wavefront's load covers two rows.
-__device__ __forceinline__ void load_ks(char* dst, const Side& s, int64_t k0, int64_t K, int64_t K1, int w, int lane) {
+__device__ __forceinline__ void load_ks(char* dst, const Side& s, uint32_t k0, uint32_t K, uint32_t K1, int w, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int q = w * 4 + i, kr = q * 2 + (lane >> 5);
     const int c = (lane & 31) ^ (4 * (kr & 3));
-    const int64_t k = k0 + q * 2;  // even, as is K1: a pair of rows lies in one half
+    const uint32_t k = k0 + q * 2;  // even, as is K1: a pair of rows lies in one half
     const char* base = k < K1 ? s.p + k * s.ld : s.p2 + (k - K1) * s.ld;
     const bool ok = k0 + kr < K && c * 8 < s.rows;
     const uint32_t off = static_cast<uint32_t>((lane >> 5) * s.ld) + c * 16;
@@ -324,13 +344,29 @@ __device__ __forceinline__ void load_block8(const char* row, uint64_t n, uint64_
 
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
+// Instruction classes of the scheduling barriers.
+constexpr int kMfma = 0x8, kDsRead = 0x100;
+
+// One matrix instruction, then N LDS reads.
+template <int N>
+__device__ __forceinline__ void group_pair() {
+  __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+  if constexpr (N > 0) __builtin_amdgcn_sched_group_barrier(kDsRead, N, 0);
+}
+
+// READS reads spread evenly behind the MM matrix instructions.
+template <int READS, int MM, int... M>
+__device__ __forceinline__ void group_pairs(std::integer_sequence<int, M...>) {
+  (group_pair<(READS * (M + 1)) / MM - (READS * M) / MM>(), ...);
+}
+
 enum SavedKind { kNoSaved, kSaved16, kSaved8 };
 
 // One tile of one product.  MB: 32-row blocks per wavefront (two wavefronts
 // along the rows, four along the 256 columns, two blocks of columns each).
 // SAVED: the checkpoint's type (kGateUp, kDh).  F32OUT: fp32 weight gradients.
 template <int KIND, int MB, int SAVED, bool F32OUT>
-__global__ void __launch_bounds__(kGemmThreads, 2) ffn_gemm_kernel(const GemmArgs a) {
+__global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel(const GemmArgs a) {
   constexpr int TM = 64 * MB;
   constexpr bool WGRAD = KIND == kDwDown || KIND == kDwGateUp;
   constexpr bool A_KC = !WGRAD;
@@ -345,189 +381,227 @@ __global__ void __launch_bounds__(kGemmThreads, 2) ffn_gemm_kernel(const GemmArg
   const int wm = w >> 2, wn = w & 3;
   const uint64_t H = a.H, F = a.F;
 
-  // Consecutive tiles on one XCD share operands: the grid's blocks go round
-  // the XCDs, so each XCD gets a contiguous range, ordered four row tiles deep.
-  const int64_t total = WGRAD ? a.mtiles * a.ntiles * a.segs_n : a.mtiles * a.ntiles;
-  const int64_t chunk = gridDim.x / kXcds;
-  const int64_t t = static_cast<int64_t>(blockIdx.x % kXcds) * chunk + blockIdx.x / kXcds;
-  if (t >= total) return;
-  int64_t mt, nt;
-  int seg;
-  {
-    constexpr int64_t GM = 4;
-    const int64_t per = WGRAD ? a.mtiles * a.ntiles : total;
-    const int64_t tt = t % per;
-    const int64_t grp = tt / (GM * a.ntiles), in = tt - grp * GM * a.ntiles;
-    const int64_t depth = min(GM, a.mtiles - grp * GM);
-    mt = grp * GM + in % depth;
-    nt = in / depth;
-    seg = WGRAD ? static_cast<int>(t / per) : a.map[mt];
-  }
-  if (seg < 0) return;
-  const Seg& sg = a.segs[seg];
-  const int64_t m0 = (WGRAD ? mt : mt - sg.tile0) * TM;
-  const int64_t n0 = nt * (KIND == kGateUp ? kTileN / 2 : kTileN);
+  const uint32_t total = a.mtiles * a.ntiles * (WGRAD ? a.segs_n : 1u);  // below 2^31, checked on the host
 
-  Side A, B;
-  int64_t K, K1 = INT64_MAX;
-  if constexpr (KIND == kGateUp) {
-    K = H;
-    A = {sg.x + m0 * H * 2, nullptr, H * 2, static_cast<int32_t>(std::min<int64_t>(TM, sg.rows - m0))};
-    B = {sg.w_gate + n0 * H * 2, sg.w_up + n0 * H * 2, H * 2, static_cast<int32_t>(std::min<int64_t>(kTileN / 2, F - n0))};
-  } else if constexpr (KIND == kDown) {
-    K = F;
-    A = {a.h + (sg.row + m0) * F * 2, nullptr, F * 2, static_cast<int32_t>(std::min<int64_t>(TM, sg.rows - m0))};
-    B = {sg.w_down + n0 * F * 2, nullptr, F * 2, static_cast<int32_t>(std::min<int64_t>(kTileN, H - n0))};
-  } else if constexpr (KIND == kDh) {
-    K = H;
-    A = {sg.dy + m0 * H * 2, nullptr, H * 2, static_cast<int32_t>(std::min<int64_t>(TM, sg.rows - m0))};
-    B = {sg.w_down + n0 * 2, nullptr, F * 2, static_cast<int32_t>(std::min<int64_t>(kTileN, F - n0))};
-  } else if constexpr (KIND == kDx) {
-    K = 2 * F;
-    K1 = F;
-    A = {a.g + (sg.row + m0) * F * 4, nullptr, F * 4, static_cast<int32_t>(std::min<int64_t>(TM, sg.rows - m0))};
-    B = {sg.w_gate + n0 * 2, sg.w_up + n0 * 2, H * 2, static_cast<int32_t>(std::min<int64_t>(kTileN, H - n0))};
-  } else if constexpr (KIND == kDwDown) {
-    K = sg.rows;
-    A = {sg.dy + m0 * 2, nullptr, H * 2, static_cast<int32_t>(std::min<int64_t>(TM, H - m0))};
-    B = {a.h + (sg.row * F + n0) * 2, nullptr, F * 2, static_cast<int32_t>(std::min<int64_t>(kTileN, F - n0))};
-  } else {
-    K = sg.rows;
-    A = {a.g + (sg.row * 2 * F + m0) * 2, nullptr, F * 4, static_cast<int32_t>(std::min<int64_t>(TM, 2 * F - m0))};
-    B = {sg.x + n0 * 2, nullptr, H * 2, static_cast<int32_t>(std::min<int64_t>(kTileN, H - n0))};
-  }
+  // Tile t of the product.  Tiles are numbered four row tiles deep, so that
+  // the ones that run together on an XCD share operands in its L2.  False for a
+  // row tile past the blocks' last.
+  auto find = [&](uint32_t t, Tile& r) -> bool {
+    constexpr uint32_t GM = 4;
+    const uint32_t per = a.mtiles * a.ntiles;
+    const uint32_t s = WGRAD ? uniform(t / per) : 0;
+    const uint32_t tt = t - s * per;
+    const uint32_t grp = uniform(tt / (GM * a.ntiles)), in = tt - grp * GM * a.ntiles;
+    const uint32_t depth = std::min(GM, a.mtiles - grp * GM);
+    const uint32_t nt = depth == GM ? in / GM : uniform(in / depth), mt = grp * GM + in - nt * depth;
+    const int32_t seg = WGRAD ? static_cast<int32_t>(s) : as_constant(a.map)[mt];
+    if (seg < 0) return false;
+    const ConstSeg& sg = as_constant(a.segs)[seg];
+    r.sg = &sg;
+    const int64_t m0 = r.m0 = static_cast<int64_t>(WGRAD ? mt : mt - sg.tile0) * TM;
+    const int64_t n0 = r.n0 = static_cast<int64_t>(nt) * (KIND == kGateUp ? kTileN / 2 : kTileN);
+    Side &A = r.A, &B = r.B;
+    const auto left = [](int64_t most, uint64_t n) { return static_cast<int32_t>(std::min<int64_t>(most, n)); };
+    if constexpr (KIND == kGateUp) {
+      r.K = H;
+      A = {sg.x + m0 * H * 2, nullptr, H * 2, left(TM, sg.rows - m0)};
+      B = {sg.w_gate + n0 * H * 2, sg.w_up + n0 * H * 2, H * 2, left(kTileN / 2, F - n0)};
+    } else if constexpr (KIND == kDown) {
+      r.K = F;
+      A = {a.h + (sg.row + m0) * F * 2, nullptr, F * 2, left(TM, sg.rows - m0)};
+      B = {sg.w_down + n0 * F * 2, nullptr, F * 2, left(kTileN, H - n0)};
+    } else if constexpr (KIND == kDh) {
+      r.K = H;
+      A = {sg.dy + m0 * H * 2, nullptr, H * 2, left(TM, sg.rows - m0)};
+      B = {sg.w_down + n0 * 2, nullptr, F * 2, left(kTileN, F - n0)};
+    } else if constexpr (KIND == kDx) {
+      r.K = 2 * F;
+      A = {a.g + (sg.row + m0) * F * 4, nullptr, F * 4, left(TM, sg.rows - m0)};
+      B = {sg.w_gate + n0 * 2, sg.w_up + n0 * 2, H * 2, left(kTileN, H - n0)};
+    } else if constexpr (KIND == kDwDown) {
+      r.K = sg.rows;
+      A = {sg.dy + m0 * 2, nullptr, H * 2, left(TM, H - m0)};
+      B = {a.h + (sg.row * F + n0) * 2, nullptr, F * 2, left(kTileN, F - n0)};
+    } else {
+      r.K = sg.rows;
+      A = {a.g + (sg.row * 2 * F + m0) * 2, nullptr, F * 4, left(TM, 2 * F - m0)};
+      B = {sg.x + n0 * 2, nullptr, H * 2, left(kTileN, H - n0)};
+    }
+    return true;
+  };
+  // The workgroup's tiles: every gridDim.x-th, the ones of one round next to
+  // each other on each XCD (blocks go round the XCDs).
+  uint32_t next = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  auto advance = [&](Tile& r) -> bool {
+    for (; next < total; next += gridDim.x)
+      if (find(next, r)) {
+        next += gridDim.x;
+        return true;
+      }
+    return false;
+  };
 
   f32x16 acc[MB][2];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-
-  auto load = [&](char* da, char* db, int64_t k0) {
-    if constexpr (A_KC) load_kc<TM, false>(da, A, k0, K, w, lane);
-    else load_ks(da, A, k0, K, INT64_MAX, w, lane);
-    if constexpr (B_KC) load_kc<kTileN, KIND == kGateUp>(db, B, k0, K, w, lane);
-    else load_ks(db, B, k0, K, K1, w, lane);
+  auto load = [&](char* da, char* db, const Tile& r, uint32_t k0) {
+    if constexpr (A_KC) load_kc<TM, false>(da, r.A, k0, r.K, w, lane);
+    else load_ks(da, r.A, k0, r.K, ~0u, w, lane);
+    if constexpr (B_KC) load_kc<kTileN, KIND == kGateUp>(db, r.B, k0, r.K, w, lane);
+    else load_ks(db, r.B, k0, r.K, KIND == kDx ? static_cast<uint32_t>(F) : ~0u, w, lane);
   };
+  // One step of 64 summed values: the fragments of each 16 are read while the
+  // matrix cores work on the 16 before.  The group barriers pin that order; left
+  // alone, the compiler reads each fragment just before its use, to save
+  // registers, and every read's latency shows.
   auto compute = [&](const char* ta, const char* tb) {
-#pragma unroll
-    for (int kk = 0; kk < kTileK / 16; ++kk) {
-      bf16x8 fa[MB], fb[2];
+    constexpr int STEPS = kTileK / 16, MM = 2 * MB;
+    constexpr int READS = MB * (A_KC ? 1 : 2) + 2 * (B_KC ? 1 : 2);
+    bf16x8 fa[2][MB], fb[2][2];
+    auto fragments = [&](int s, int kk) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int b = KIND == kGateUp ? wn + 4 * j : wn * 2 + j;  // 32-column block
-        if constexpr (B_KC) fb[j] = frag_kc(tb, b * 32, kk, lane);
-        else fb[j] = frag_ks(tb, b, kk, lane);
+        if constexpr (B_KC) fb[s][j] = frag_kc(tb, b * 32, kk, lane);
+        else fb[s][j] = frag_ks(tb, b, kk, lane);
       }
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
-        if constexpr (A_KC) fa[i] = frag_kc(ta, (wm * MB + i) * 32, kk, lane);
-        else fa[i] = frag_ks(ta, wm * MB + i, kk, lane);
+        if constexpr (A_KC) fa[s][i] = frag_kc(ta, (wm * MB + i) * 32, kk, lane);
+        else fa[s][i] = frag_ks(ta, wm * MB + i, kk, lane);
       }
+    };
+    fragments(0, 0);
+    __builtin_amdgcn_sched_group_barrier(kDsRead, READS, 0);
+#pragma unroll
+    for (int kk = 0; kk < STEPS; ++kk) {
+      if (kk + 1 < STEPS) fragments((kk + 1) & 1, kk + 1);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
+      if (kk + 1 < STEPS) {
+        group_pairs<READS, MM>(std::make_integer_sequence<int, MM>{});
+      } else {
+        __builtin_amdgcn_sched_group_barrier(kMfma, MM, 0);
+      }
     }
   };
 
-  if (K > 0) {
-    load(A0, B0, 0);
-    __syncthreads();
-    for (int64_t k0 = 0; k0 < K; k0 += 2 * kTileK) {
-      if (k0 + kTileK < K) load(A1, B1, k0 + kTileK);
+  Tile cur;
+  bool more = advance(cur);
+  if (!more) return;
+  load(A0, B0, cur, 0);
+  __syncthreads();
+  while (more) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+    Tile then;
+    more = advance(then);
+    // Two steps a turn, so that each buffer is known at compile time (the
+    // compiler then lets reads of one pass loads into the other).  The last
+    // turn already loads the next tile's first step, which the epilogue hides.
+    const uint32_t K = cur.K;
+    uint32_t k0 = 0;
+    do {
+      if (k0 + kTileK < K) load(A1, B1, cur, k0 + kTileK);
       compute(A0, B0);
       __syncthreads();
-      if (k0 + kTileK >= K) break;
-      if (k0 + 2 * kTileK < K) load(A0, B0, k0 + 2 * kTileK);
-      compute(A1, B1);
+      const bool last = k0 + 2 * kTileK >= K;
+      if (!last) load(A0, B0, cur, k0 + 2 * kTileK);
+      else if (more) load(A0, B0, then, 0);
+      if (k0 + kTileK < K) compute(A1, B1);
       __syncthreads();
-    }
-  }
-
+      k0 += 2 * kTileK;
+    } while (k0 < K);
+    ConstSeg& sg = *cur.sg;
+    const int64_t m0 = cur.m0, n0 = cur.n0;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t m = m0 + (wm * MB + i) * 32 + (lane & 31);
-    if constexpr (KIND == kGateUp) {
-      const bool row = m < sg.rows;
-      const uint64_t n = n0 + wn * 32;
-      f32x16 hv;
+    for (int i = 0; i < MB; ++i) {
+      const int64_t m = m0 + (wm * MB + i) * 32 + (lane & 31);
+      if constexpr (KIND == kGateUp) {
+        const bool row = m < sg.rows;
+        const uint64_t n = n0 + wn * 32;
+        f32x16 hv;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) hv[e] = acc[i][0][e] * sigmoid(acc[i][0][e]) * acc[i][1][e];
-      store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
-      if constexpr (SAVED == kSaved16) {
-        store_block(sg.saved + m * a.saved_row, n, F, row, lane, acc[i][0]);
-        store_block(sg.saved + m * a.saved_row + F * 2, n, F, row, lane, acc[i][1]);
-      } else if constexpr (SAVED == kSaved8) {
-        char* const out = sg.saved + m * a.saved_row;
-        store_block8(out, 2 * F, n, row && n < F, lane, acc[i][0]);
-        store_block8(out, 2 * F, F + n, row && n < F, lane, acc[i][1]);
-        if (row && n == 0 && lane < 32)  // zeros behind the scales
-          for (uint64_t p = 2 * F + 2 * F / 32; p < a.saved_row; ++p) out[p] = 0;
-      }
-    } else if constexpr (KIND == kDh) {
-      const bool row = m < sg.rows;
-      const char* in = sg.saved + static_cast<uint64_t>(std::min<int64_t>(m, sg.rows - 1)) * a.saved_row;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint64_t n = n0 + wn * 64 + j * 32;
-        if (n >= F) continue;
-        float gate[16], up[16];
-        if constexpr (SAVED == kSaved16) {
-          u32x4 gv[2], uv[2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint64_t c = std::min<uint64_t>(n + 8 * (2 * p + (lane >> 5)), F - 8);
-            gv[p] = *reinterpret_cast<const u32x4*>(in + c * 2);
-            uv[p] = *reinterpret_cast<const u32x4*>(in + (F + c) * 2);
-          }
-          unpack_block(gv, gate);
-          unpack_block(uv, up);
-        } else {
-          load_block8(in, 2 * F, n, lane, gate);
-          load_block8(in, 2 * F, F + n, lane, up);
-        }
-        f32x16 hv, dg, du;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float g = gate[e], u = up[e], d = acc[i][j][e];
-          const float s = sigmoid(g), act = g * s;
-          hv[e] = act * u;
-          dg[e] = d * u * (s * (1.0f + g * (1.0f - s)));
-          du[e] = d * act;
-        }
+        for (int e = 0; e < 16; ++e) hv[e] = acc[i][0][e] * sigmoid(acc[i][0][e]) * acc[i][1][e];
         store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
-        store_block(a.g + (sg.row + m) * F * 4, n, F, row, lane, dg);
-        store_block(a.g + (sg.row + m) * F * 4 + F * 2, n, F, row, lane, du);
-      }
-    } else if constexpr (!WGRAD) {
+        if constexpr (SAVED == kSaved16) {
+          store_block(sg.saved + m * a.saved_row, n, F, row, lane, acc[i][0]);
+          store_block(sg.saved + m * a.saved_row + F * 2, n, F, row, lane, acc[i][1]);
+        } else if constexpr (SAVED == kSaved8) {
+          char* const out = sg.saved + m * a.saved_row;
+          store_block8(out, 2 * F, n, row && n < F, lane, acc[i][0]);
+          store_block8(out, 2 * F, F + n, row && n < F, lane, acc[i][1]);
+          if (row && n == 0 && lane < 32)  // zeros behind the scales
+            for (uint64_t p = 2 * F + 2 * F / 32; p < a.saved_row; ++p) out[p] = 0;
+        }
+      } else if constexpr (KIND == kDh) {
+        const bool row = m < sg.rows;
+        const char* in = sg.saved + static_cast<uint64_t>(std::min<int64_t>(m, sg.rows - 1)) * a.saved_row;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        store_block(sg.y + m * H * 2, n0 + wn * 64 + j * 32, H, m < sg.rows, lane, acc[i][j]);
-    } else {
-      constexpr int ES = F32OUT ? 4 : 2;
-      const uint64_t M = KIND == kDwDown ? H : 2 * F, N = KIND == kDwDown ? F : H;
-      const bool row = static_cast<uint64_t>(m) < M;
-      char* out;
-      if constexpr (KIND == kDwDown) out = sg.dw_down + m * N * ES;
-      else out = static_cast<uint64_t>(m) < F ? sg.dw_gate + m * N * ES : sg.dw_up + (m - static_cast<int64_t>(F)) * N * ES;
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t n = n0 + wn * 64 + j * 32;
+          if (n >= F) continue;
+          float gate[16], up[16];
+          if constexpr (SAVED == kSaved16) {
+            u32x4 gv[2], uv[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint64_t n = n0 + wn * 64 + j * 32;
-        if constexpr (F32OUT) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint64_t c = n + 8 * q + 4 * (lane >> 5);
-            if (row && c < N)
-              *reinterpret_cast<u32x4*>(out + c * 4) =
-                  u32x4{__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
-                        __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])};
+            for (int p = 0; p < 2; ++p) {
+              const uint64_t c = std::min<uint64_t>(n + 8 * (2 * p + (lane >> 5)), F - 8);
+              gv[p] = *reinterpret_cast<const u32x4*>(in + c * 2);
+              uv[p] = *reinterpret_cast<const u32x4*>(in + (F + c) * 2);
+            }
+            unpack_block(gv, gate);
+            unpack_block(uv, up);
+          } else {
+            load_block8(in, 2 * F, n, lane, gate);
+            load_block8(in, 2 * F, F + n, lane, up);
           }
-        } else {
-          store_block(out, n, N, row, lane, acc[i][j]);
+          f32x16 hv, dg, du;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float g = gate[e], u = up[e], d = acc[i][j][e];
+            const float s = sigmoid(g), act = g * s;
+            hv[e] = act * u;
+            dg[e] = d * u * (s * (1.0f + g * (1.0f - s)));
+            du[e] = d * act;
+          }
+          store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
+          store_block(a.g + (sg.row + m) * F * 4, n, F, row, lane, dg);
+          store_block(a.g + (sg.row + m) * F * 4 + F * 2, n, F, row, lane, du);
+        }
+      } else if constexpr (!WGRAD) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          store_block(sg.y + m * H * 2, n0 + wn * 64 + j * 32, H, m < sg.rows, lane, acc[i][j]);
+      } else {
+        constexpr int ES = F32OUT ? 4 : 2;
+        const uint64_t M = KIND == kDwDown ? H : 2 * F, N = KIND == kDwDown ? F : H;
+        const bool row = static_cast<uint64_t>(m) < M;
+        char* out;
+        if constexpr (KIND == kDwDown) out = sg.dw_down + m * N * ES;
+        else out = static_cast<uint64_t>(m) < F ? sg.dw_gate + m * N * ES : sg.dw_up + (m - static_cast<int64_t>(F)) * N * ES;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint64_t n = n0 + wn * 64 + j * 32;
+          if constexpr (F32OUT) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t c = n + 8 * q + 4 * (lane >> 5);
+              if (row && c < N)
+                *reinterpret_cast<u32x4*>(out + c * 4) =
+                    u32x4{__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
+                          __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])};
+            }
+          } else {
+            store_block(out, n, N, row, lane, acc[i][j]);
+          }
         }
       }
     }
+    cur = then;
   }
 }
 
@@ -542,8 +616,11 @@ gc_status launch(Kern kernel, const A& args, uint64_t grid, uint32_t threads, hi
                                          dim3(threads), params, 0, stream));
 }
 
-// Blocks of a product's grid: its tiles, rounded up to a whole number per XCD.
-uint64_t grid_for(int64_t tiles) { return static_cast<uint64_t>((tiles + kXcds - 1) / kXcds) * kXcds; }
+// Workgroups of a product: as many as run at once (`per_cu` on each of the 256
+// CUs), or one per tile where there are fewer, a whole number per XCD.
+uint64_t grid_for(int64_t tiles, int per_cu) {
+  return static_cast<uint64_t>(std::min<int64_t>((tiles + kXcds - 1) / kXcds * kXcds, 256 * per_cu));
+}
 
 int64_t ceil_div(uint64_t a, uint64_t b) { return static_cast<int64_t>((a + b - 1) / b); }
 
@@ -618,7 +695,7 @@ template <int KIND, int SAVED>
 gc_status row_product(GemmArgs a, const gci::FfnGeom& g, int64_t ntiles, hipStream_t stream) {
   a.mtiles = g.tiles;
   a.ntiles = ntiles;
-  const uint64_t grid = grid_for(a.mtiles * a.ntiles);
+  const uint64_t grid = grid_for(a.mtiles * a.ntiles, g.tile_rows == 64 ? 2 : 1);
   if (g.tile_rows == 256) return launch(ffn_gemm_kernel<KIND, 4, SAVED, false>, a, grid, kGemmThreads, stream);
   if (g.tile_rows == 128) return launch(ffn_gemm_kernel<KIND, 2, SAVED, false>, a, grid, kGemmThreads, stream);
   return launch(ffn_gemm_kernel<KIND, 1, SAVED, false>, a, grid, kGemmThreads, stream);
@@ -628,7 +705,7 @@ template <int KIND>
 gc_status weight_product(GemmArgs a, uint64_t M, uint64_t N, bool f32, hipStream_t stream) {
   a.mtiles = ceil_div(M, 256);
   a.ntiles = ceil_div(N, kTileN);
-  const uint64_t grid = grid_for(a.mtiles * a.ntiles * a.segs_n);
+  const uint64_t grid = grid_for(a.mtiles * a.ntiles * a.segs_n, 1);
   if (f32) return launch(ffn_gemm_kernel<KIND, 4, kNoSaved, true>, a, grid, kGemmThreads, stream);
   return launch(ffn_gemm_kernel<KIND, 4, kNoSaved, false>, a, grid, kGemmThreads, stream);
 }
