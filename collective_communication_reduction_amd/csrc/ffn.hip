@@ -7,7 +7,7 @@
 //             dx = [dgate dup] [Wg; Wu],  dWd = dy^T h,  [dWg; dWu] = [dgate dup]^T x
 //
 // Every product is one kernel template over bf16 operands with fp32 MFMA
-// accumulators: a workgroup of eight wavefronts owns a tile of TM x 256 outputs
+// accumulators: a workgroup owns tiles of TM x 256 outputs
 // and walks the summed index in steps of 64 through double-buffered LDS, filled
 // by direct global-to-LDS loads.  An operand is stored either with the summed
 // index contiguous (rows of 64 values, 128 bytes) or across rows (rows of 256
@@ -33,8 +33,8 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef gci::FfnSeg Seg;
 
-constexpr int kGemmThreads = 512;
 constexpr int kTileN = 256;
+constexpr int kWaves = 8;
 constexpr int kTileK = 64;
 constexpr int kXcds = 8;
 
@@ -170,15 +170,6 @@ struct GemmArgs {
   uint32_t segs_n;
 };
 
-// Where one operand's tile comes from.  kc: the summed index is contiguous in
-// memory (rows x K); else each row holds one summed index.
-struct Side {
-  const char* p;
-  const char* p2;          // second half: of the tile's rows (kc) or of the summed index
-  uint64_t ld;             // bytes per stored row
-  int32_t rows;            // valid rows of the tile (kc), or valid values of a row (else)
-};
-
 // The plan's tables were written by an earlier kernel and do not change here:
 // read through the constant address space they come by scalar loads and stay
 // in scalar registers, where the operands' buffer descriptors need them (the
@@ -190,6 +181,14 @@ __device__ __forceinline__ const __attribute__((address_space(4))) int32_t* as_c
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// Where one operand's tile comes from.  kc: the summed index is contiguous in
+// memory (rows x K); else each stored row holds one summed index.
+struct Side {
+  const char* p;
+  const char* p2;          // second half: of the tile's rows (kc) or of the summed index
+  int32_t n;               // valid rows of the tile (kc), or valid values of a stored row (else)
+};
+
 // One tile of a product: its operands, the summed length, where it goes.
 struct Tile {
   ConstSeg* sg;
@@ -198,68 +197,114 @@ struct Tile {
   int64_t m0, n0;
 };
 
-constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor's range: the load gives zeros
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, 0x7FFFFFFF, 0x00020000);
+// x's operands if c, else y's; field by field, so that they stay in registers.
+__device__ __forceinline__ Side pick(bool c, const Side& x, const Side& y) {
+  return {c ? x.p : y.p, c ? x.p2 : y.p2, c ? x.n : y.n};
 }
 
-__device__ __forceinline__ void lds_load(const char* base, char* dst, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base), (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
-}
+// One step's loads: summed indices from k0 of K.
+struct Load {
+  Side a, b;
+  uint32_t k0, K;
+};
 
-// Tile of ROWS rows x 64 summed values: 16-byte chunk c of row r sits at chunk
-// c ^ ((r >> 1) & 7) of the row's 128 bytes, so that 16 lanes reading one
-// chunk of 16 rows touch all 64 banks.  A wavefront's load covers eight rows.
-template <int ROWS, bool HALVES>
-__device__ __forceinline__ void load_kc(char* dst, const Side& s, uint32_t k0, uint32_t K, int w, int lane) {
-  constexpr int L = ROWS / 64;  // loads per wavefront
+constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor's range, whatever is added: the load gives zeros
+
+// Loads of one operand's tile by eight wavefronts, straight from memory into LDS
+// (1 KiB per wavefront and instruction, 16 bytes per lane).  Rows, columns and
+// summed indices outside the operand come as zeros: the buffer descriptor ends
+// behind the last valid row, and a lane outside its row gets an offset past it.
+//
+// kc: ROWS rows x 64 summed values; chunk c (16 bytes) of row r sits at chunk
+// c ^ ((r >> 1) & 7) of the row's 128 bytes, so that 16 lanes reading one chunk
+// of 16 rows touch all 64 banks.  An instruction covers eight rows.
+// else: 64 summed indices x 256 values; the 32-byte unit u of row k sits at
+// u ^ 2 (k & 3), so that the four rows a transposing read takes together lie in
+// different banks.  An instruction covers two rows.
+//
+// Either way an instruction's lanes differ between tiles only by a multiple of
+// the rows skipped and by the parity of its number, so two lane offsets serve all.
+template <bool KC, int ROWS, bool HALVES>
+struct Loader {
+  static constexpr int L = KC ? ROWS / 8 / kWaves : 32 / kWaves;  // instructions per wavefront
+  uint32_t ld;      // bytes per stored row
+  uint32_t off[2];  // lane offset by parity
+  uint32_t c8[2];   // the lane's first value in its stored row's part
+  int q0;           // first instruction
+
+  __device__ __forceinline__ Loader(uint64_t stored, int w, int lane) : ld(static_cast<uint32_t>(stored)), q0(w * L) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int q = w * L + i, r = q * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ ((r >> 1) & 7);
-    const bool second = HALVES && q * 8 >= ROWS / 2;
-    const int rr = second ? r - ROWS / 2 : r;
-    const bool ok = rr < s.rows && k0 + c * 8 < K;
-    const uint32_t off = static_cast<uint32_t>(rr * s.ld) + c * 16;
-    lds_load((second ? s.p2 : s.p) + static_cast<uint64_t>(k0) * 2, dst + q * 1024, ok ? off : kOutside);
+    for (int e = 0; e < 2; ++e) {
+      const int q = q0 + e, r = KC ? lane >> 3 : lane >> 5;
+      const int c = KC ? (lane & 7) ^ (((q * 8 + r) >> 1) & 7) : (lane & 31) ^ (4 * ((q * 2 + r) & 3));
+      off[e] = r * ld + c * 16;
+      c8[e] = c * 8;
+    }
   }
-}
 
-// Tile of 64 summed indices x 256 values: 512-byte rows whose 32-byte unit u
-// sits at u ^ 2 (k & 3), so that the four rows a transposing read takes
-// together lie in different banks.  A wavefront's load covers two rows.
-__device__ __forceinline__ void load_ks(char* dst, const Side& s, uint32_t k0, uint32_t K, uint32_t K1, int w, int lane) {
+  // The step's summed indices start at k0 of K; for !KC those from K1 on come from p2.
+  // Instructions [I0, I1) of it.
+  template <int I0 = 0, int I1 = L>
+  __device__ __forceinline__ void run(char* dst, const Side& s, uint32_t k0, uint32_t K, uint32_t K1) const {
+    const uint32_t left = uniform(K > k0 ? K - k0 : 0);  // a saturating subtraction is a vector instruction
+    const uint32_t inside = KC ? left : static_cast<uint32_t>(s.n);
+    uint32_t lane_off[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = w * 4 + i, kr = q * 2 + (lane >> 5);
-    const int c = (lane & 31) ^ (4 * (kr & 3));
-    const uint32_t k = k0 + q * 2;  // even, as is K1: a pair of rows lies in one half
-    const char* base = k < K1 ? s.p + k * s.ld : s.p2 + (k - K1) * s.ld;
-    const bool ok = k0 + kr < K && c * 8 < s.rows;
-    const uint32_t off = static_cast<uint32_t>((lane >> 5) * s.ld) + c * 16;
-    lds_load(base, dst + q * 1024, ok ? off : kOutside);
+    for (int e = 0; e < 2; ++e) lane_off[e] = c8[e] < inside ? off[e] : kOutside;
+#pragma unroll
+    for (int i = I0; i < I1; ++i) {
+      const uint32_t q = q0 + i;
+      const char* base;
+      uint32_t bytes, skip = 0;
+      if constexpr (KC) {
+        const bool second = HALVES && q * 8 >= ROWS / 2;
+        base = (second ? s.p2 : s.p) + static_cast<uint64_t>(k0) * 2;
+        bytes = left ? static_cast<uint32_t>(s.n) * ld - k0 * 2 : 0;
+        skip = (q * 8 - (second ? ROWS / 2 : 0)) * ld;
+      } else {
+        const uint32_t k = k0 + q * 2;  // even, as is K1: both rows lie in one half
+        base = k < K1 ? s.p + static_cast<uint64_t>(k) * ld : s.p2 + static_cast<uint64_t>(k - K1) * ld;
+        bytes = (left > q * 2 ? std::min(left - q * 2, 2u) : 0) * ld;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000),
+                                               (__attribute__((address_space(3))) void*)(dst + q * 1024), 16,
+                                               lane_off[i & 1] + skip, 0, 0, 0);
+    }
   }
-}
+};
 
-// A lane's eight summed values (16 kk + 8 (lane / 32) ..) of row r0 + lane % 32.
-__device__ __forceinline__ bf16x8 frag_kc(const char* t, int r0, int kk, int lane) {
-  const int r = r0 + (lane & 31);
-  return *reinterpret_cast<const bf16x8*>(t + r * 128 + (((kk * 2 + (lane >> 5)) ^ ((r >> 1) & 7)) * 16));
-}
+// Fragments: a lane's eight summed values (16 kk + 8 (lane / 32) ..) of row
+// lane % 32 of a 32-row block.  The lane's offsets within the tile are kept in
+// four registers, everything else is a constant of the read: by kk for kc (the
+// chunk swizzle), by block for the other kind (the unit swizzle), whose groups of
+// 16 lanes read 4 rows x 16 values each and receive them transposed.
+template <bool KC>
+struct Reader {
+  uint32_t off[4];
 
-// The same from a tile stored across rows, block of 32 values at 32 b: each
-// group of 16 lanes reads 4 rows x 16 values and receives them transposed.
-__device__ __forceinline__ bf16x8 frag_ks(const char* t, int b, int kk, int lane) {
-  typedef __attribute__((address_space(3))) bf16x4 L;
-  const int i = lane & 15, q = lane >> 4;
-  const int k = kk * 16 + (q >> 1) * 8 + (i >> 2);
-  const int u = (2 * b + (q & 1)) ^ (2 * (i >> 2));
-  const char* p = t + k * 512 + u * 32 + (i & 3) * 8;
-  const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((L*)p);
-  const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((L*)(p + 4 * 512));
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
+  // block0: the wavefront's first block (a multiple of 4, or of the blocks it has).
+  __device__ __forceinline__ Reader(int block0, int lane) {
+    const int i = lane & 15, q = lane >> 4, r = lane & 31;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (KC) off[e] = (block0 * 32 + r) * 128 + (((e * 2 + (lane >> 5)) ^ ((r >> 1) & 7)) * 16);
+      else off[e] = ((q >> 1) * 8 + (i >> 2)) * 512 + ((2 * ((block0 + e) ^ (i >> 2)) + (q & 1)) * 32) + (i & 3) * 8;
+    }
+  }
+
+  // skip: blocks between the wavefront's first and this one beyond its number j (gate and up).
+  __device__ __forceinline__ bf16x8 operator()(const char* t, int j, int kk, int skip = 0) const {
+    if constexpr (KC) {
+      return *reinterpret_cast<const bf16x8*>(t + off[kk] + (j + skip) * 4096);
+    } else {
+      typedef __attribute__((address_space(3))) bf16x4 V;
+      const char* p = t + off[j] + kk * 8192;
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((V*)p);
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((V*)(p + 2048));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
 
 // A 32 x 32 block of results: lane l holds output row l % 32 and, of its 32
 // columns, 8 j + 4 (l / 32) + i as v[4 j + i].  For wide stores the two halves
@@ -271,41 +316,38 @@ __device__ __forceinline__ void swap_halves(uint32_t& x, uint32_t& y) {
   y = r[1];
 }
 
-__device__ __forceinline__ void pack_block(const f32x16& v, u32x4 (&o)[2]) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    uint32_t a0 = bf16_bits(v[8 * p]) | (bf16_bits(v[8 * p + 1]) << 16);
-    uint32_t a1 = bf16_bits(v[8 * p + 2]) | (bf16_bits(v[8 * p + 3]) << 16);
-    uint32_t b0 = bf16_bits(v[8 * p + 4]) | (bf16_bits(v[8 * p + 5]) << 16);
-    uint32_t b1 = bf16_bits(v[8 * p + 6]) | (bf16_bits(v[8 * p + 7]) << 16);
-    swap_halves(a0, b0);
-    swap_halves(a1, b1);
-    o[p] = u32x4{a0, a1, b0, b1};
-  }
+// Half p of a block: its values 8 p .. 8 p + 7 of every lane, as the vector above.
+__device__ __forceinline__ u32x4 pack_half(const float (&v)[8]) {
+  uint32_t a0 = bf16_bits(v[0]) | (bf16_bits(v[1]) << 16);
+  uint32_t a1 = bf16_bits(v[2]) | (bf16_bits(v[3]) << 16);
+  uint32_t b0 = bf16_bits(v[4]) | (bf16_bits(v[5]) << 16);
+  uint32_t b1 = bf16_bits(v[6]) | (bf16_bits(v[7]) << 16);
+  swap_halves(a0, b0);
+  swap_halves(a1, b1);
+  return u32x4{a0, a1, b0, b1};
 }
 
-__device__ __forceinline__ void unpack_block(const u32x4 (&o)[2], float (&v)[16]) {
+__device__ __forceinline__ void unpack_half(const u32x4& o, float (&v)[8]) {
+  uint32_t w[4] = {o[0], o[1], o[2], o[3]};
+  swap_halves(w[0], w[2]);
+  swap_halves(w[1], w[3]);
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    uint32_t w[4] = {o[p][0], o[p][1], o[p][2], o[p][3]};
-    swap_halves(w[0], w[2]);
-    swap_halves(w[1], w[3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[8 * p + 2 * i] = __uint_as_float(w[i] << 16);
-      v[8 * p + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 
 // bf16 store of a block: columns n0 .. n0 + 31 of the lane's row (ok: the row exists).
 __device__ __forceinline__ void store_block(char* row, uint64_t n0, uint64_t N, bool ok, int lane, const f32x16& v) {
-  u32x4 o[2];
-  pack_block(v, o);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = v[8 * p + e];
+    const u32x4 o = pack_half(h);
     const uint64_t n = n0 + 8 * (2 * p + (lane >> 5));
-    if (ok && n < N) *reinterpret_cast<u32x4*>(row + n * 2) = o[p];
+    if (ok && n < N) *reinterpret_cast<u32x4*>(row + n * 2) = o;
   }
 }
 
@@ -331,12 +373,13 @@ __device__ __forceinline__ void store_block8(char* row, uint64_t n, uint64_t c0,
   if (lane < 32) row[n + c0 / 32] = static_cast<char>(e + 127);
 }
 
-__device__ __forceinline__ void load_block8(const char* row, uint64_t n, uint64_t c0, int lane, float (&v)[16]) {
+// Half p of an 8-bit block, in the same places.
+__device__ __forceinline__ void load_half8(const char* row, uint64_t n, uint64_t c0, int p, int lane, float (&v)[8]) {
   const float s = mx8_scale(*reinterpret_cast<const uint8_t*>(row + n + c0 / 32));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     float f[4];
-    mx8_values(*reinterpret_cast<const uint32_t*>(row + c0 + 8 * j + 4 * (lane >> 5)), s, f);
+    mx8_values(*reinterpret_cast<const uint32_t*>(row + c0 + 16 * p + 8 * j + 4 * (lane >> 5)), s, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[4 * j + i] = f[i];
   }
@@ -345,42 +388,55 @@ __device__ __forceinline__ void load_block8(const char* row, uint64_t n, uint64_
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // Instruction classes of the scheduling barriers.
-constexpr int kMfma = 0x8, kDsRead = 0x100;
+constexpr int kMfma = 0x8, kVmemRead = 0x20, kDsRead = 0x100;
 
-// One matrix instruction, then N LDS reads.
-template <int N>
-__device__ __forceinline__ void group_pair() {
+// One matrix instruction, then R LDS reads and L loads.
+template <int R, int L>
+__device__ __forceinline__ void group_one() {
   __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-  if constexpr (N > 0) __builtin_amdgcn_sched_group_barrier(kDsRead, N, 0);
+  if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(kDsRead, R, 0);
+  if constexpr (L > 0) __builtin_amdgcn_sched_group_barrier(kVmemRead, L, 0);
 }
 
-// READS reads spread evenly behind the MM matrix instructions.
-template <int READS, int MM, int... M>
-__device__ __forceinline__ void group_pairs(std::integer_sequence<int, M...>) {
-  (group_pair<(READS * (M + 1)) / MM - (READS * M) / MM>(), ...);
+// READS reads and LOADS loads spread evenly behind MM matrix instructions.
+template <int READS, int LOADS, int MM, int... M>
+__device__ __forceinline__ void group_all(std::integer_sequence<int, M...>) {
+  (group_one<(READS * (M + 1)) / MM - (READS * M) / MM, (LOADS * (M + 1)) / MM - (LOADS * M) / MM>(), ...);
+}
+
+// Barrier of the workgroup that also waits for this wavefront's loads into LDS:
+// behind it every wavefront's have arrived.  (A fence alone orders LDS accesses,
+// and the loads count as memory accesses.)
+constexpr int kLoadsDone = 0x0F70;  // vmcnt(0), the other counters free
+__device__ __forceinline__ void loads_barrier() {
+  __builtin_amdgcn_s_waitcnt(kLoadsDone);
+  __syncthreads();
 }
 
 enum SavedKind { kNoSaved, kSaved16, kSaved8 };
 
-// One tile of one product.  MB: 32-row blocks per wavefront (two wavefronts
-// along the rows, four along the 256 columns, two blocks of columns each).
+// A product's tiles of TM x 256 outputs, by eight wavefronts: two along the
+// rows, four along the columns, each with MB x 2 blocks of 32 x 32.
 // SAVED: the checkpoint's type (kGateUp, kDh).  F32OUT: fp32 weight gradients.
-template <int KIND, int MB, int SAVED, bool F32OUT>
-__global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel(const GemmArgs a) {
-  constexpr int TM = 64 * MB;
+template <int KIND, int TM, int SAVED, bool F32OUT>
+__global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel(const GemmArgs a) {
+  constexpr int WM = 2, WN = kWaves / WM;
+  constexpr int MB = TM / WM / 32, NB = kTileN / WN / 32;
   constexpr bool WGRAD = KIND == kDwDown || KIND == kDwGateUp;
   constexpr bool A_KC = !WGRAD;
   constexpr bool B_KC = KIND == kGateUp || KIND == kDown;
-  static_assert(!WGRAD || MB == 4, "tiles across rows are 256 wide");
+  static_assert(!WGRAD || TM == 256, "tiles across rows are 256 wide");
   __shared__ __align__(1024) char A0[TM * 128];
   __shared__ __align__(1024) char A1[TM * 128];
   __shared__ __align__(1024) char B0[kTileN * 128];
   __shared__ __align__(1024) char B1[kTileN * 128];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = w >> 2, wn = w & 3;
+  const int wm = w / WN, wn = w % WN;
   const uint64_t H = a.H, F = a.F;
-
+  constexpr bool A_WIDE = KIND == kDx || KIND == kDwGateUp;  // rows of 2F values
+  const Loader<A_KC, TM, false> load_a(KIND == kGateUp || KIND == kDh || KIND == kDwDown ? H * 2 : A_WIDE ? F * 4 : F * 2, w, lane);
+  const Loader<B_KC, kTileN, KIND == kGateUp> load_b(KIND == kGateUp || KIND == kDx || KIND == kDwGateUp ? H * 2 : F * 2, w, lane);
   const uint32_t total = a.mtiles * a.ntiles * (WGRAD ? a.segs_n : 1u);  // below 2^31, checked on the host
 
   // Tile t of the product.  Tiles are numbered four row tiles deep, so that
@@ -404,28 +460,28 @@ __global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel
     const auto left = [](int64_t most, uint64_t n) { return static_cast<int32_t>(std::min<int64_t>(most, n)); };
     if constexpr (KIND == kGateUp) {
       r.K = H;
-      A = {sg.x + m0 * H * 2, nullptr, H * 2, left(TM, sg.rows - m0)};
-      B = {sg.w_gate + n0 * H * 2, sg.w_up + n0 * H * 2, H * 2, left(kTileN / 2, F - n0)};
+      A = {sg.x + m0 * H * 2, nullptr, left(TM, sg.rows - m0)};
+      B = {sg.w_gate + n0 * H * 2, sg.w_up + n0 * H * 2, left(kTileN / 2, F - n0)};
     } else if constexpr (KIND == kDown) {
       r.K = F;
-      A = {a.h + (sg.row + m0) * F * 2, nullptr, F * 2, left(TM, sg.rows - m0)};
-      B = {sg.w_down + n0 * F * 2, nullptr, F * 2, left(kTileN, H - n0)};
+      A = {a.h + (sg.row + m0) * F * 2, nullptr, left(TM, sg.rows - m0)};
+      B = {sg.w_down + n0 * F * 2, nullptr, left(kTileN, H - n0)};
     } else if constexpr (KIND == kDh) {
       r.K = H;
-      A = {sg.dy + m0 * H * 2, nullptr, H * 2, left(TM, sg.rows - m0)};
-      B = {sg.w_down + n0 * 2, nullptr, F * 2, left(kTileN, F - n0)};
+      A = {sg.dy + m0 * H * 2, nullptr, left(TM, sg.rows - m0)};
+      B = {sg.w_down + n0 * 2, nullptr, left(kTileN, F - n0)};
     } else if constexpr (KIND == kDx) {
       r.K = 2 * F;
-      A = {a.g + (sg.row + m0) * F * 4, nullptr, F * 4, left(TM, sg.rows - m0)};
-      B = {sg.w_gate + n0 * 2, sg.w_up + n0 * 2, H * 2, left(kTileN, H - n0)};
+      A = {a.g + (sg.row + m0) * F * 4, nullptr, left(TM, sg.rows - m0)};
+      B = {sg.w_gate + n0 * 2, sg.w_up + n0 * 2, left(kTileN, H - n0)};
     } else if constexpr (KIND == kDwDown) {
       r.K = sg.rows;
-      A = {sg.dy + m0 * 2, nullptr, H * 2, left(TM, H - m0)};
-      B = {a.h + (sg.row * F + n0) * 2, nullptr, F * 2, left(kTileN, F - n0)};
+      A = {sg.dy + m0 * 2, nullptr, left(TM, H - m0)};
+      B = {a.h + (sg.row * F + n0) * 2, nullptr, left(kTileN, F - n0)};
     } else {
       r.K = sg.rows;
-      A = {a.g + (sg.row * 2 * F + m0) * 2, nullptr, F * 4, left(TM, 2 * F - m0)};
-      B = {sg.x + n0 * 2, nullptr, H * 2, left(kTileN, H - n0)};
+      A = {a.g + (sg.row * 2 * F + m0) * 2, nullptr, left(TM, 2 * F - m0)};
+      B = {sg.x + n0 * 2, nullptr, left(kTileN, H - n0)};
     }
     return true;
   };
@@ -441,80 +497,116 @@ __global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel
     return false;
   };
 
-  f32x16 acc[MB][2];
-  auto load = [&](char* da, char* db, const Tile& r, uint32_t k0) {
-    if constexpr (A_KC) load_kc<TM, false>(da, r.A, k0, r.K, w, lane);
-    else load_ks(da, r.A, k0, r.K, ~0u, w, lane);
-    if constexpr (B_KC) load_kc<kTileN, KIND == kGateUp>(db, r.B, k0, r.K, w, lane);
-    else load_ks(db, r.B, k0, r.K, KIND == kDx ? static_cast<uint32_t>(F) : ~0u, w, lane);
+  f32x16 acc[MB][NB];
+  bf16x8 fa[2][MB], fb[2][NB];  // fragments of 16 summed values: those in use, and the next
+  constexpr int STEPS = kTileK / 16, MM = MB * NB;
+  constexpr int READS = MB * (A_KC ? 1 : 2) + NB * (B_KC ? 1 : 2);
+  const Reader<A_KC> read_a(wm * MB, lane);
+  const Reader<B_KC> read_b(wn * (KIND == kGateUp ? NB / 2 : NB), lane);
+  auto read = [&](const char* ta, const char* tb, int kk) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j)  // kGateUp: gate blocks, then the up blocks of the same columns
+      fb[kk & 1][j] = read_b(tb, j, kk, KIND == kGateUp && j >= NB / 2 ? 4 - NB / 2 : 0);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fa[kk & 1][i] = read_a(ta, i, kk);
   };
-  // One step of 64 summed values: the fragments of each 16 are read while the
-  // matrix cores work on the 16 before.  The group barriers pin that order; left
-  // alone, the compiler reads each fragment just before its use, to save
-  // registers, and every read's latency shows.
-  auto compute = [&](const char* ta, const char* tb) {
-    constexpr int STEPS = kTileK / 16, MM = 2 * MB;
-    constexpr int READS = MB * (A_KC ? 1 : 2) + 2 * (B_KC ? 1 : 2);
-    bf16x8 fa[2][MB], fb[2][2];
-    auto fragments = [&](int s, int kk) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = KIND == kGateUp ? wn + 4 * j : wn * 2 + j;  // 32-column block
-        if constexpr (B_KC) fb[s][j] = frag_kc(tb, b * 32, kk, lane);
-        else fb[s][j] = frag_ks(tb, b, kk, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        if constexpr (A_KC) fa[s][i] = frag_kc(ta, (wm * MB + i) * 32, kk, lane);
-        else fa[s][i] = frag_ks(ta, wm * MB + i, kk, lane);
-      }
-    };
-    fragments(0, 0);
-    __builtin_amdgcn_sched_group_barrier(kDsRead, READS, 0);
-#pragma unroll
-    for (int kk = 0; kk < STEPS; ++kk) {
-      if (kk + 1 < STEPS) fragments((kk + 1) & 1, kk + 1);
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
-      if (kk + 1 < STEPS) {
-        group_pairs<READS, MM>(std::make_integer_sequence<int, MM>{});
-      } else {
-        __builtin_amdgcn_sched_group_barrier(kMfma, MM, 0);
-      }
-    }
-  };
-
-  Tile cur;
-  bool more = advance(cur);
-  if (!more) return;
-  load(A0, B0, cur, 0);
-  __syncthreads();
-  while (more) {
+  auto multiply = [&](int kk) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-    Tile then;
-    more = advance(then);
-    // Two steps a turn, so that each buffer is known at compile time (the
-    // compiler then lets reads of one pass loads into the other).  The last
-    // turn already loads the next tile's first step, which the epilogue hides.
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[kk & 1][j], fa[kk & 1][i], acc[i][j], 0, 0, 0);
+  };
+  constexpr uint32_t NO_K1 = ~0u;
+  const uint32_t K1 = KIND == kDx ? static_cast<uint32_t>(F) : NO_K1;
+  constexpr int LA = decltype(load_a)::L, LB = decltype(load_b)::L;
+  // Loads of one step that run behind the barrier (the first SPLIT_A and SPLIT_B
+  // instructions of each operand) and the rest, in the step that follows.
+  constexpr int SPLIT_A = LA * 2 / 4, SPLIT_B = LB * 2 / 4;
+  auto load_first = [&](char* ta, char* tb, const Load& l) {
+    load_a.template run<0, SPLIT_A>(ta, l.a, l.k0, l.K, NO_K1);
+    load_b.template run<0, SPLIT_B>(tb, l.b, l.k0, l.K, K1);
+  };
+  auto load_rest = [&](char* ta, char* tb, const Load& l) {
+    load_a.template run<SPLIT_A, LA>(ta, l.a, l.k0, l.K, NO_K1);
+    load_b.template run<SPLIT_B, LB>(tb, l.b, l.k0, l.K, K1);
+  };
+  // One step of 64 summed values from buffer (ta, tb), whose first fragments are
+  // read already.  Fragments are read 16 summed values ahead of the matrix
+  // instructions, across the barrier too: behind it the buffer is free, the
+  // step after next is loaded into it from `src`, and the last instructions run
+  // beside the other buffer's first reads.  The group barriers pin that order;
+  // left alone, the compiler reads each fragment just before its use, to save
+  // registers, and every read's latency shows.
+  auto step = [&](char* ta, char* tb, char* na, char* nb, const Load& here, const Load& other) {
+    load_rest(na, nb, other);
+    read(ta, tb, 1);
+    multiply(0);
+    group_all<READS, LA - SPLIT_A + LB - SPLIT_B, MM>(std::make_integer_sequence<int, MM>{});
+#pragma unroll
+    for (int kk = 1; kk + 1 < STEPS; ++kk) {
+      read(ta, tb, kk + 1);
+      multiply(kk);
+      group_all<READS, 0, MM>(std::make_integer_sequence<int, MM>{});
+    }
+    loads_barrier();
+    load_first(ta, tb, here);
+    read(na, nb, 0);
+    multiply(STEPS - 1);
+    group_all<READS, SPLIT_A + SPLIT_B, MM>(std::make_integer_sequence<int, MM>{});
+  };
+
+  Tile cur;
+  if (!advance(cur)) return;
+  Load to0{cur.A, cur.B, 0, cur.K}, to1{cur.A, cur.B, kTileK, cur.K};  // what each buffer is filled from
+  load_first(A0, B0, to0);
+  load_rest(A0, B0, to0);
+  load_first(A1, B1, to1);
+  loads_barrier();
+  read(A0, B0, 0);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
+    Tile then = cur;
+    const bool more = advance(then);
+    const uint32_t then_K = more ? then.K : 0;
+    // Two steps a turn, one from each buffer: with the buffers known at compile
+    // time the reads of one need not wait for the loads into the other.  A
+    // tile starts in buffer 0; its last steps already load the next tile's first
+    // two, which the epilogue then hides.
     const uint32_t K = cur.K;
     uint32_t k0 = 0;
-    do {
-      if (k0 + kTileK < K) load(A1, B1, cur, k0 + kTileK);
-      compute(A0, B0);
-      __syncthreads();
-      const bool last = k0 + 2 * kTileK >= K;
-      if (!last) load(A0, B0, cur, k0 + 2 * kTileK);
-      else if (more) load(A0, B0, then, 0);
-      if (k0 + kTileK < K) compute(A1, B1);
-      __syncthreads();
-      k0 += 2 * kTileK;
-    } while (k0 < K);
+    for (; k0 + kTileK < K; k0 += 2 * kTileK) {
+      const bool in0 = k0 + 2 * kTileK < K, in1 = k0 + 3 * kTileK < K;
+      to0 = {pick(in0, cur.A, then.A), pick(in0, cur.B, then.B), in0 ? k0 + 2 * kTileK : 0, in0 ? K : then_K};
+      step(A0, B0, A1, B1, to0, to1);
+      to1 = {pick(in1, cur.A, then.A), pick(in1, cur.B, then.B), in1 ? k0 + 3 * kTileK : kTileK, in1 ? K : then_K};
+      step(A1, B1, A0, B0, to1, to0);
+    }
+    const bool odd = k0 < K || K == 0;
+    if (odd) {  // one more step, from buffer 0; the next tile's fragments are read after the epilogue
+      if (K <= kTileK) {
+        __builtin_amdgcn_s_waitcnt(kLoadsDone);  // of what was loaded into buffer 1 for this tile: nothing, as zeros
+        to1 = {then.A, then.B, kTileK, then_K};
+        load_first(A1, B1, to1);
+      }
+#pragma unroll
+      for (int kk = 0; kk + 1 < STEPS; ++kk) {
+        read(A0, B0, kk + 1);
+        multiply(kk);
+      }
+      multiply(STEPS - 1);
+      loads_barrier();
+      to0 = {then.A, then.B, 0, then_K};
+      load_first(A0, B0, to0);
+      load_rest(A0, B0, to0);
+    }
+    // The epilogue's addresses are made here: computed before the loop, as the
+    // compiler would, they take the registers that the loop's own need.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     ConstSeg& sg = *cur.sg;
     const int64_t m0 = cur.m0, n0 = cur.n0;
 #pragma unroll
@@ -522,60 +614,75 @@ __global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel
       const int64_t m = m0 + (wm * MB + i) * 32 + (lane & 31);
       if constexpr (KIND == kGateUp) {
         const bool row = m < sg.rows;
-        const uint64_t n = n0 + wn * 32;
-        f32x16 hv;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) hv[e] = acc[i][0][e] * sigmoid(acc[i][0][e]) * acc[i][1][e];
-        store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
-        if constexpr (SAVED == kSaved16) {
-          store_block(sg.saved + m * a.saved_row, n, F, row, lane, acc[i][0]);
-          store_block(sg.saved + m * a.saved_row + F * 2, n, F, row, lane, acc[i][1]);
-        } else if constexpr (SAVED == kSaved8) {
-          char* const out = sg.saved + m * a.saved_row;
-          store_block8(out, 2 * F, n, row && n < F, lane, acc[i][0]);
-          store_block8(out, 2 * F, F + n, row && n < F, lane, acc[i][1]);
-          if (row && n == 0 && lane < 32)  // zeros behind the scales
-            for (uint64_t p = 2 * F + 2 * F / 32; p < a.saved_row; ++p) out[p] = 0;
+        for (int j = 0; j < NB / 2; ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+          const uint64_t n = n0 + (wn * (NB / 2) + j) * 32;
+          const f32x16 &gate = acc[i][j], &up = acc[i][NB / 2 + j];
+          f32x16 hv;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) hv[e] = gate[e] * sigmoid(gate[e]) * up[e];
+          store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
+          if constexpr (SAVED == kSaved16) {
+            store_block(sg.saved + m * a.saved_row, n, F, row, lane, gate);
+            store_block(sg.saved + m * a.saved_row + F * 2, n, F, row, lane, up);
+          } else if constexpr (SAVED == kSaved8) {
+            char* const out = sg.saved + m * a.saved_row;
+            store_block8(out, 2 * F, n, row && n < F, lane, gate);
+            store_block8(out, 2 * F, F + n, row && n < F, lane, up);
+            if (row && n == 0 && lane < 32)  // zeros behind the scales
+              for (uint64_t p = 2 * F + 2 * F / 32; p < a.saved_row; ++p) out[p] = 0;
+          }
         }
       } else if constexpr (KIND == kDh) {
         const bool row = m < sg.rows;
         const char* in = sg.saved + static_cast<uint64_t>(std::min<int64_t>(m, sg.rows - 1)) * a.saved_row;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint64_t n = n0 + wn * 64 + j * 32;
+        for (int j = 0; j < NB; ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+          const uint64_t n = n0 + (wn * NB + j) * 32;
           if (n >= F) continue;
-          float gate[16], up[16];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // half a block at a time, to hold few registers
+          const uint64_t c = n + 8 * (2 * p + (lane >> 5));
+          float gate[8], up[8], sig[8], r[8];
           if constexpr (SAVED == kSaved16) {
-            u32x4 gv[2], uv[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint64_t c = std::min<uint64_t>(n + 8 * (2 * p + (lane >> 5)), F - 8);
-              gv[p] = *reinterpret_cast<const u32x4*>(in + c * 2);
-              uv[p] = *reinterpret_cast<const u32x4*>(in + (F + c) * 2);
-            }
-            unpack_block(gv, gate);
-            unpack_block(uv, up);
+            const uint64_t in_c = std::min<uint64_t>(c, F - 8);
+            unpack_half(*reinterpret_cast<const u32x4*>(in + in_c * 2), gate);
+            unpack_half(*reinterpret_cast<const u32x4*>(in + (F + in_c) * 2), up);
           } else {
-            load_block8(in, 2 * F, n, lane, gate);
-            load_block8(in, 2 * F, F + n, lane, up);
+            load_half8(in, 2 * F, n, p, lane, gate);
+            load_half8(in, 2 * F, F + n, p, lane, up);
           }
-          f32x16 hv, dg, du;
+          const bool ok = row && c < F;
+          char* const out_h = a.h + (sg.row + m) * F * 2 + c * 2;
+          char* const out_g = a.g + (sg.row + m) * F * 4 + c * 2;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float g = gate[e], u = up[e], d = acc[i][j][e];
-            const float s = sigmoid(g), act = g * s;
-            hv[e] = act * u;
-            dg[e] = d * u * (s * (1.0f + g * (1.0f - s)));
-            du[e] = d * act;
+          for (int e = 0; e < 8; ++e) {
+            sig[e] = sigmoid(gate[e]);
+            r[e] = gate[e] * sig[e] * up[e];
           }
-          store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
-          store_block(a.g + (sg.row + m) * F * 4, n, F, row, lane, dg);
-          store_block(a.g + (sg.row + m) * F * 4 + F * 2, n, F, row, lane, du);
+          const u32x4 hv = pack_half(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            r[e] = acc[i][j][8 * p + e] * up[e] * (sig[e] * (1.0f + gate[e] * (1.0f - sig[e])));
+          const u32x4 dg = pack_half(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[e] = acc[i][j][8 * p + e] * (gate[e] * sig[e]);
+          const u32x4 du = pack_half(r);
+          if (ok) {
+            *reinterpret_cast<u32x4*>(out_h) = hv;
+            *reinterpret_cast<u32x4*>(out_g) = dg;
+            *reinterpret_cast<u32x4*>(out_g + F * 2) = du;
+          }
         }
-      } else if constexpr (!WGRAD) {
+      }
+    } else if constexpr (!WGRAD) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          store_block(sg.y + m * H * 2, n0 + wn * 64 + j * 32, H, m < sg.rows, lane, acc[i][j]);
+        for (int j = 0; j < NB; ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+          store_block(sg.y + m * H * 2, n0 + (wn * NB + j) * 32, H, m < sg.rows, lane, acc[i][j]);
+        }
       } else {
         constexpr int ES = F32OUT ? 4 : 2;
         const uint64_t M = KIND == kDwDown ? H : 2 * F, N = KIND == kDwDown ? F : H;
@@ -584,8 +691,9 @@ __global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel
         if constexpr (KIND == kDwDown) out = sg.dw_down + m * N * ES;
         else out = static_cast<uint64_t>(m) < F ? sg.dw_gate + m * N * ES : sg.dw_up + (m - static_cast<int64_t>(F)) * N * ES;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint64_t n = n0 + wn * 64 + j * 32;
+        for (int j = 0; j < NB; ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+          const uint64_t n = n0 + (wn * NB + j) * 32;
           if constexpr (F32OUT) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -600,6 +708,11 @@ __global__ void __launch_bounds__(kGemmThreads, MB == 1 ? 4 : 2) ffn_gemm_kernel
           }
         }
       }
+    }
+    if (!more) break;
+    if (odd) {
+      loads_barrier();
+      read(A0, B0, 0);
     }
     cur = then;
   }
@@ -696,9 +809,9 @@ gc_status row_product(GemmArgs a, const gci::FfnGeom& g, int64_t ntiles, hipStre
   a.mtiles = g.tiles;
   a.ntiles = ntiles;
   const uint64_t grid = grid_for(a.mtiles * a.ntiles, g.tile_rows == 64 ? 2 : 1);
-  if (g.tile_rows == 256) return launch(ffn_gemm_kernel<KIND, 4, SAVED, false>, a, grid, kGemmThreads, stream);
-  if (g.tile_rows == 128) return launch(ffn_gemm_kernel<KIND, 2, SAVED, false>, a, grid, kGemmThreads, stream);
-  return launch(ffn_gemm_kernel<KIND, 1, SAVED, false>, a, grid, kGemmThreads, stream);
+  if (g.tile_rows == 256) return launch(ffn_gemm_kernel<KIND, 256, SAVED, false>, a, grid, 64 * kWaves, stream);
+  if (g.tile_rows == 128) return launch(ffn_gemm_kernel<KIND, 128, SAVED, false>, a, grid, 64 * kWaves, stream);
+  return launch(ffn_gemm_kernel<KIND, 64, SAVED, false>, a, grid, 64 * kWaves, stream);
 }
 
 template <int KIND>
@@ -706,8 +819,8 @@ gc_status weight_product(GemmArgs a, uint64_t M, uint64_t N, bool f32, hipStream
   a.mtiles = ceil_div(M, 256);
   a.ntiles = ceil_div(N, kTileN);
   const uint64_t grid = grid_for(a.mtiles * a.ntiles * a.segs_n, 1);
-  if (f32) return launch(ffn_gemm_kernel<KIND, 4, kNoSaved, true>, a, grid, kGemmThreads, stream);
-  return launch(ffn_gemm_kernel<KIND, 4, kNoSaved, false>, a, grid, kGemmThreads, stream);
+  if (f32) return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, true>, a, grid, 64 * kWaves, stream);
+  return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, false>, a, grid, 64 * kWaves, stream);
 }
 
 }  // namespace
