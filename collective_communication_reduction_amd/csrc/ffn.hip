@@ -103,9 +103,13 @@ __global__ void __launch_bounds__(kPlanThreads) ffn_plan_kernel(const PlanArgs a
   for (int i = lo; i < hi; ++i) {
     const int d = i / a.E, e = i - d * a.E;
     int64_t c = 0;  // saturates at the rank's rows, so no sum of entries overflows
-    for (int s = 0; s < a.N; ++s) {
-      const int64_t v = a.splits[(static_cast<int64_t>(s) * a.N + d) * a.E + e];
-      c = min(c + min(max(v, int64_t(0)), a.rows[d]), a.rows[d]);
+    for (int s0 = 0; s0 < a.N; s0 += 8) {  // eight loads in flight
+      int64_t v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = a.splits[(static_cast<int64_t>(min(s0 + q, a.N - 1)) * a.N + d) * a.E + e];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (s0 + q < a.N) c = min(c + min(max(v[q], int64_t(0)), a.rows[d]), a.rows[d]);
     }
     pre[i] = c;
     sum += c;
@@ -718,6 +722,118 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
   }
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Serving: a handful of rows per expert, where a product is one pass over the
+// weights.  A wavefront owns 16 output columns of one expert (of both matrices
+// for gate and up) and a share of the summed index: it streams the weights
+// straight into the matrix instructions' registers (16 rows x 32 summed values
+// each, 64 bytes a row and instruction, kFewLoads KiB in flight).  The
+// workgroup's eight wavefronts are `shares` shares of 8 / shares column groups;
+// shares are added through LDS in a fixed order.  The expert's rows are found
+// from the split table by the workgroup itself, so the whole forward is two
+// launches.
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kFewWaves = 8;
+constexpr int kFewLoads = 8;  // weight vectors in flight per lane
+
+template <int P>
+struct FewArgs {
+  const char* x[P];        // rows that gate and up multiply
+  const char* wa[P];
+  const char* wb[P];       // up; unused by down
+  char* y[P];
+  int64_t rows[P];
+  int64_t base[P];         // rows of the ranks before
+  const int64_t* splits;
+  char* h;
+  uint64_t K, n;           // summed values, output columns
+  uint32_t N, E, tiles;    // column tiles per expert
+  uint32_t shares;         // of the summed index: 1, 2, 4 or 8
+};
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t x) {
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+template <bool GATE_UP, int P>
+__global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P> a) {
+  constexpr int U = GATE_UP ? kFewLoads / 2 : kFewLoads;
+  __shared__ f32x4 part[kFewWaves][GATE_UP ? 2 : 1][kWave];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint32_t share = w % a.shares, group = w / a.shares, groups = kFewWaves / a.shares;
+  const uint32_t seg = blockIdx.x / a.tiles;
+  const uint32_t d = seg / a.E, e = seg - d * a.E;
+  int64_t before = 0, count = 0;
+  for (uint32_t i = lane; i < (e + 1) * a.N; i += kWave) {
+    const uint32_t q = i / a.N, s = i - q * a.N;
+    const int64_t v = a.splits[(static_cast<uint64_t>(s) * a.N + d) * a.E + q];
+    const int64_t c = min(max(v, int64_t(0)), a.rows[d]);
+    if (q < e) before += c;
+    else count += c;
+  }
+  before = wave_sum64(before);
+  count = wave_sum64(count);
+  const int64_t start = min(before, a.rows[d]);
+  const int64_t rows = min(before + count, a.rows[d]) - start;
+  const uint64_t n0 = static_cast<uint64_t>((blockIdx.x - seg * a.tiles) * groups + group) * 16;
+  const uint64_t col = min(n0 + (lane & 15), a.n - 1);  // past the last: the last again, not stored
+  const uint64_t w0 = (static_cast<uint64_t>(e) * a.n + col) * a.K * 2;
+  const char* const wa = a.wa[d] + w0;
+  const char* const wb = GATE_UP ? a.wb[d] + w0 : nullptr;
+  for (int64_t m0 = 0; m0 < rows; m0 += 16) {
+    const int64_t m = min(m0 + (lane & 15), rows - 1);
+    const char* const x = GATE_UP ? a.x[d] + (start + m) * a.K * 2 : a.h + (a.base[d] + start + m) * a.K * 2;
+    f32x4 ga{}, ua{};
+    for (uint64_t k0 = static_cast<uint64_t>(share) * 32 * U; k0 < a.K; k0 += 32 * U * a.shares) {
+      u32x4 va[U], vb[U], vx[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint64_t k = k0 + i * 32 + (lane >> 4) * 8;
+        const uint64_t c = k < a.K ? k * 2 : 0;  // clamped: no exec-masked load
+        va[i] = ld16(wa + c);
+        if constexpr (GATE_UP) vb[i] = ld16(wb + c);
+        vx[i] = *reinterpret_cast<const u32x4*>(x + c);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (k0 + i * 32 + (lane >> 4) * 8 >= a.K) {  // past the end: zeros on both sides
+          va[i] = u32x4{};
+          if constexpr (GATE_UP) vb[i] = u32x4{};
+          vx[i] = u32x4{};
+        }
+        ga = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, va[i]), __builtin_bit_cast(bf16x8, vx[i]), ga, 0, 0, 0);
+        if constexpr (GATE_UP)
+          ua = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vb[i]), __builtin_bit_cast(bf16x8, vx[i]), ua, 0, 0, 0);
+      }
+    }
+    part[w][0][lane] = ga;
+    if constexpr (GATE_UP) part[w][1][lane] = ua;
+    __syncthreads();
+    if (share == 0) {
+      for (uint32_t q = 1; q < a.shares; ++q) {
+        ga += part[w + q][0][lane];
+        if constexpr (GATE_UP) ua += part[w + q][1][lane];
+      }
+      // lane l: row m0 + l % 16, columns n0 + 4 (l / 16) .. + 3
+      const uint64_t n = n0 + 4 * (lane >> 4);
+      if (m0 + (lane & 15) < rows && n < a.n) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = GATE_UP ? ga[i] * sigmoid(ga[i]) * ua[i] : ga[i];
+        char* const out = GATE_UP ? a.h + (a.base[d] + start + m) * a.n * 2 : a.y[d] + (start + m) * a.n * 2;
+        *reinterpret_cast<u32x2*>(out + n * 2) =
+            u32x2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------ host side
 
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
@@ -823,6 +939,46 @@ gc_status weight_product(GemmArgs a, uint64_t M, uint64_t N, bool f32, hipStream
   return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, false>, a, grid, 64 * kWaves, stream);
 }
 
+// Shares of the summed index: about four turns of a wavefront's loads each, so
+// that short ones do not leave a workgroup less work than finding its rows, and
+// long ones are spread over all of its wavefronts.
+template <class A>
+void split_few(A& a, int unroll) {
+  a.shares = 1;
+  while (a.shares < kFewWaves && a.K > static_cast<uint64_t>(32 * unroll * 4) * a.shares) a.shares *= 2;
+  a.tiles = static_cast<uint32_t>(ceil_div(a.n, 16 * (kFewWaves / a.shares)));
+}
+
+template <int P>
+gc_status forward_few(const gci::FfnCall& c, const gci::FfnGeom& g) {
+  FewArgs<P> a{};
+  char* const base = static_cast<char*>(c.scratch);
+  int64_t run = 0;
+  for (int d = 0; d < c.nranks; ++d) {
+    a.x[d] = c.x_t == GC_MX8 ? base + g.x + run * c.hidden * 2 : static_cast<const char*>(c.x[d]);
+    a.wa[d] = static_cast<const char*>(c.w_gate[d]);
+    a.wb[d] = static_cast<const char*>(c.w_up[d]);
+    a.y[d] = static_cast<char*>(c.y[d]);
+    a.rows[d] = c.rows[d];
+    a.base[d] = run;
+    run += c.rows[d];
+  }
+  a.splits = c.splits;
+  a.h = base + g.h;
+  a.K = c.hidden;
+  a.n = c.inter;
+  a.N = c.nranks;
+  a.E = c.experts_per_rank;
+  split_few(a, kFewLoads / 2);
+  const gc_status st = launch(ffn_few_kernel<true, P>, a, static_cast<uint64_t>(g.segs) * a.tiles, 64 * kFewWaves, c.stream);
+  if (st != GC_OK) return st;
+  for (int d = 0; d < c.nranks; ++d) a.wa[d] = static_cast<const char*>(c.w_down[d]);
+  a.K = c.inter;
+  a.n = c.hidden;
+  split_few(a, kFewLoads);
+  return launch(ffn_few_kernel<false, P>, a, static_cast<uint64_t>(g.segs) * a.tiles, 64 * kFewWaves, c.stream);
+}
+
 }  // namespace
 
 namespace gci {
@@ -830,6 +986,11 @@ namespace gci {
 gc_status launch_moe_ffn(const FfnCall& c) {
   const FfnGeom g = ffn_geom(c.rows, c.nranks, c.experts_per_rank, c.hidden, c.inter, c.x_t, false);
   if (g.rows == 0) return GC_OK;
+  if (!c.saved && g.few) {
+    const gc_status st = decode_x(c, g);
+    if (st != GC_OK) return st;
+    return c.nranks <= 8 ? forward_few<8>(c, g) : forward_few<64>(c, g);
+  }
   gc_status st = plan(c, g);
   if (st == GC_OK) st = decode_x(c, g);
   if (st != GC_OK) return st;
