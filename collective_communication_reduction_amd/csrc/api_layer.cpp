@@ -247,14 +247,15 @@ uint64_t up256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 // expert a serving forward streams the weights instead: 16 rows over 8 experts
 // of 4096 x 11008 take 336 us so and 483 in tiles, 64 over 16 of 2048 x 1024
 // 49 and 76; at 16 rows per expert the tiles win everywhere (309 us against
-// 568 for 64 experts of 4096 x 1024).
+// 568 for 64 experts of 4096 x 1024).  Each of its workgroups adds up its rank's
+// table up to its expert, which past 1024 experts would take as long.
 gci::FfnGeom gci::ffn_geom(const int64_t* rows, int nranks, int E, uint64_t hidden, uint64_t inter, gc_dtype x_t, bool backward) {
   gci::FfnGeom g;
   for (int d = 0; d < nranks; ++d) g.rows += rows[d];
   g.segs = nranks * E;
   const int64_t avg = g.rows / g.segs;
   g.tile_rows = avg >= 192 ? 256 : avg >= 96 ? 128 : 64;
-  g.few = avg < 8;
+  g.few = avg < 8 && g.segs <= 1024;
   for (int d = 0; d < nranks; ++d) g.tiles += rows[d] / g.tile_rows + std::min<int64_t>(E, rows[d]);
   g.map = up256(static_cast<uint64_t>(g.segs) * sizeof(gci::FfnSeg));
   g.x = g.map + up256(static_cast<uint64_t>(g.tiles) * 4);
