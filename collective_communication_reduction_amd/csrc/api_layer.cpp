@@ -151,12 +151,12 @@ extern "C" gc_status gc_rms_norm(const void* const* x, const void* const* residu
 namespace {
 
 // Consecutive rows of one rank per block of the backward: about a thousand
-// blocks over all ranks (four per CU), at least eight rows each, so that the
+// blocks over all ranks (four per CU), at least four rows each, so that the
 // partial weight gradients stay a small part of the rows' own bytes.
 int64_t norm_rows_per_block(const int64_t* ntokens, int nranks) {
   int64_t total = 0;
   for (int r = 0; r < nranks; ++r) total += ntokens[r];
-  return std::max<int64_t>(8, (total + 1023) / 1024);
+  return std::max<int64_t>(4, (total + 1023) / 1024);
 }
 
 uint64_t norm_partial_bytes(const int64_t* ntokens, int nranks, size_t hidden) {

@@ -13,7 +13,7 @@ namespace {
 
 using namespace gcdev;
 
-constexpr int kGradU = 4;      // units per lane per step
+constexpr int kGradU = 8;      // units per lane per step: a 4096-wide bf16 row at once (958 us against 1013 with 4, 8 x 16384 tokens)
 constexpr int kMaxTopk = 8;
 
 template <int P>

@@ -5,10 +5,11 @@
 //   backward  n = s rstd, d = dy w:  dx = rstd (d - n mean(d n)) + dsum,  dw = sum_t dy n
 //
 // Both read every input and write every output once: a row stays in registers
-// between its sum and its outputs, so HBM bytes bound them.  Rows up to
-// 64 x 8 units take one wavefront each (no barrier), longer ones a workgroup,
-// and rows past a workgroup's registers are read a second time (from the
-// caches, mostly).
+// between its sum and its outputs, so HBM bytes bound them.  Forward rows up to
+// 64 x 2 units take one wavefront each (no barrier), longer ones a workgroup
+// (4096 bf16, 512 units: 630 us with a workgroup's 2 units per lane, 641 with a
+// wavefront's 8, for 8 x 16384 rows), and rows past a workgroup's registers are
+// read a second time (from the caches, mostly).
 
 #include <algorithm>
 #include <type_traits>
@@ -176,42 +177,62 @@ struct NormBackwardArgs {
 
 // One workgroup takes consecutive rows of one rank; each lane keeps the weight
 // gradient of its own columns in registers over them and stores it once.
-template <class In, bool VEC, int NV, int P>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBackwardArgs<P> a) {
+// Longer rows take more lanes rather than more units per lane: 20 units each
+// left one wavefront per SIMD.
+template <class In, bool VEC, int NV, int LANES, int P>
+__global__ void __launch_bounds__(LANES) norm_backward_kernel(const NormBackwardArgs<P> a) {
   typedef RowUnit<In, VEC> U;
   typedef typename U::T T;
   constexpr int VE = U::VE;
-  __shared__ float lds[kThreads / kWave];
+  __shared__ float lds[LANES / kWave];
   const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
   const int64_t first = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * a.rows_per_block;
   const int64_t last = min(first + a.rows_per_block, a.tok[rank]);
   const uint64_t units = a.H / VE;
-  uint64_t c[NV];
+  uint32_t c[NV];  // the lane's units; past the row's end its last unit again
   bool ok[NV];
   T wv[NV];
   float dw[NV][VE];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const uint64_t u = threadIdx.x + j * kThreads;
+    const uint32_t u = threadIdx.x + j * LANES;
     ok[j] = u < units;
-    c[j] = ok[j] ? u : units - 1;
+    c[j] = min(u, static_cast<uint32_t>(units - 1));
     wv[j] = U::load_kept(reinterpret_cast<const T*>(a.w[rank]) + c[j]);
 #pragma unroll
     for (int e = 0; e < VE; ++e) dw[j][e] = 0.0f;
   }
+  const T* const dy = reinterpret_cast<const T*>(a.dy[rank]);
+  const T* const ds = reinterpret_cast<const T*>(a.dsum[rank]);
+  const T* const sm = reinterpret_cast<const T*>(a.sum[rank]);
+  // With few units per lane the next row's loads are in flight while this one's
+  // sum goes round the workgroup (8 x 16384 x 4096 bf16: 792 against 817 us).
+  constexpr bool AHEAD = NV <= (LANES == 256 ? 2 : 1);  // else its registers would cost wavefronts
+  T yn[NV], sn[NV], dn[NV];
+  float rn = 0.0f;
+  auto fetch = [&](int64_t row) {
+    const T *const dy_row = dy + row * units, *const sm_row = sm + row * units, *const ds_row = ds + row * units;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      yn[j] = U::load(dy_row + c[j]);
+      sn[j] = U::load(sm_row + c[j]);
+      if (a.has_dsum) dn[j] = U::load(ds_row + c[j]);
+    }
+    rn = a.rstd[rank][row];
+  };
+  if (AHEAD && first < last) fetch(first);
   for (int64_t row = first; row < last; ++row) {
-    const T* dy = reinterpret_cast<const T*>(a.dy[rank]) + row * units;
-    const T* ds = reinterpret_cast<const T*>(a.dsum[rank]) + row * units;
-    const T* s = reinterpret_cast<const T*>(a.sum[rank]) + row * units;
     T* dx = reinterpret_cast<T*>(a.dx[rank]) + row * units;
+    if constexpr (!AHEAD) fetch(row);
     T yv[NV], sv[NV], dv[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      yv[j] = U::load(dy + c[j]);
-      sv[j] = U::load(s + c[j]);
-      if (a.has_dsum) dv[j] = U::load(ds + c[j]);
+      yv[j] = yn[j];
+      sv[j] = sn[j];
+      dv[j] = dn[j];
     }
-    const float rs = a.rstd[rank][row];
+    const float rs = rn;
+    if (AHEAD && row + 1 < last) fetch(row + 1);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -226,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBackw
         dot = fmaf(ok[j] ? g : 0.0f, w[e], dot);
       }
     }
-    const float mean = lanes_sum<kThreads>(dot, lds) / static_cast<float>(a.H);
+    const float mean = lanes_sum<LANES>(dot, lds) / static_cast<float>(a.H);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float y[VE], n[VE], w[VE], d[VE];
@@ -247,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBackw
   for (int j = 0; j < NV; ++j)
     if (ok[j])
 #pragma unroll
-      for (int e = 0; e < VE; ++e) part[c[j] * VE + e] = dw[j][e];
+      for (int e = 0; e < VE; ++e) part[static_cast<uint64_t>(c[j]) * VE + e] = dw[j][e];
 }
 
 // Rows past a workgroup's registers: partial sums of the weight gradient live
@@ -330,9 +351,9 @@ __global__ void __launch_bounds__(kThreads) norm_weight_kernel(const NormBackwar
 // ------------------------------------------------------------- host side
 
 template <class Kern, class A>
-gc_status launch(Kern kernel, const A& args, dim3 grid, hipStream_t stream) {
+gc_status launch(Kern kernel, const A& args, dim3 grid, hipStream_t stream, int threads = kThreads) {
   void* params[] = {const_cast<A*>(&args)};
-  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreads), params, 0, stream));
+  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), params, 0, stream));
 }
 
 uint64_t addr(const void* p) { return reinterpret_cast<uint64_t>(p); }
@@ -352,14 +373,14 @@ int32_t fill_tiles(int32_t (&tile0)[P + 1], int64_t (&tok)[P], const int64_t* to
 template <class In, bool VEC, bool MX, int P>
 gc_status norm_impl(const gci::NormCall& c, NormArgs<P>& a) {
   const uint64_t units = c.hidden / RowUnit<In, VEC>::VE;
-  const int64_t per = units <= 8 * kWave ? kThreads / kWave : 1;
+  const int64_t per = units <= 2 * kWave ? kThreads / kWave : 1;
   const int32_t grid = fill_tiles<P>(a.tile0, a.tok, c.tokens, c.nranks, per);
   if (!grid) return GC_OK;
   const dim3 g(grid);
   if (units <= 1 * kWave) return launch(norm_kernel<In, VEC, MX, 1, kWave, P>, a, g, c.stream);
   if (units <= 2 * kWave) return launch(norm_kernel<In, VEC, MX, 2, kWave, P>, a, g, c.stream);
-  if (units <= 4 * kWave) return launch(norm_kernel<In, VEC, MX, 4, kWave, P>, a, g, c.stream);
-  if (units <= 8 * kWave) return launch(norm_kernel<In, VEC, MX, 8, kWave, P>, a, g, c.stream);
+  if (units <= 1 * kThreads) return launch(norm_kernel<In, VEC, MX, 1, kThreads, P>, a, g, c.stream);
+  if (units <= 2 * kThreads) return launch(norm_kernel<In, VEC, MX, 2, kThreads, P>, a, g, c.stream);
   if (units <= 4 * kThreads) return launch(norm_kernel<In, VEC, MX, 4, kThreads, P>, a, g, c.stream);
   if (units <= 8 * kThreads) return launch(norm_kernel<In, VEC, MX, 8, kThreads, P>, a, g, c.stream);
   if constexpr (!VEC)
@@ -399,10 +420,11 @@ gc_status norm_backward_impl(const gci::NormBackwardCall& c, const NormBackwardA
   if (blocks) {
     const dim3 g(blocks);
     gc_status st;
-    if (units <= 1 * kThreads) st = launch(norm_backward_kernel<In, VEC, 1, P>, a, g, c.stream);
-    else if (units <= 2 * kThreads) st = launch(norm_backward_kernel<In, VEC, 2, P>, a, g, c.stream);
-    else if (units <= 4 * kThreads) st = launch(norm_backward_kernel<In, VEC, 4, P>, a, g, c.stream);
-    else if (!VEC && units <= 20 * kThreads) st = launch(norm_backward_kernel<In, VEC, VEC ? 1 : 20, P>, a, g, c.stream);
+    if (units <= 256) st = launch(norm_backward_kernel<In, VEC, 1, 256, P>, a, g, c.stream, 256);
+    else if (units <= 512) st = launch(norm_backward_kernel<In, VEC, 2, 256, P>, a, g, c.stream, 256);
+    else if (units <= 1024) st = launch(norm_backward_kernel<In, VEC, 1, 1024, P>, a, g, c.stream, 1024);
+    else if (units <= 2048) st = launch(norm_backward_kernel<In, VEC, 2, 1024, P>, a, g, c.stream, 1024);
+    else if (!VEC && units <= 5 * 1024) st = launch(norm_backward_kernel<In, VEC, VEC ? 1 : 5, 1024, P>, a, g, c.stream, 1024);
     else st = launch(norm_backward_long_kernel<In, VEC, P>, a, g, c.stream);
     if (st != GC_OK) return st;
   }

@@ -29,7 +29,7 @@ struct RowUnit<In, true> {
   typedef typename std::conditional<In::ES == 2, OutBf16, OutF32>::type Out;
   __device__ static __forceinline__ T load(const T* p) { return ld16(p); }
   __device__ static __forceinline__ T load_kept(const T* p) { return *p; }  // read again soon: may stay in the caches
-  __device__ static __forceinline__ void store(T* p, T v) { st16(p, v); }
+  __device__ static __forceinline__ void store(T* p, T v) { st16p<gci::kStoreDevNT>(p, v); }
   __device__ static __forceinline__ void widen(const T& v, float (&x)[VE]) { unpack<In>(v, x); }
   __device__ static __forceinline__ T narrow(const float (&x)[VE]) {
     const Words<Out, VE> r = pack<Out, VE>(x);
