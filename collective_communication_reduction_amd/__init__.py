@@ -25,6 +25,7 @@ marshals a pointer array once for buffers synchronised every step.
 """
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -171,15 +172,36 @@ def _bufs(xs, n, nbytes, what):
     entries; None passes as NULL (the library rejects it)."""
     if xs is None:
         return None
-    if len(xs) < n:
-        raise ValueError(f"{what}: {len(xs)} buffers, the call needs {n}")
+    m = len(xs)
+    if m < n:
+        raise ValueError(f"{what}: {m} buffers, the call needs {n}")
     if isinstance(xs, ctypes.Array):
         return xs
-    arr = (ctypes.c_void_p * max(1, len(xs)))()
+    arr = _ptr_array(m)()
+    same = nbytes if isinstance(nbytes, int) else None
     for i, x in enumerate(xs):
-        need = nbytes if isinstance(nbytes, int) else (int(nbytes[i]) if i < n else 0)
-        arr[i] = _buf(x, need if i < n else 0, f"{what}[{i}]")
+        need = 0 if i >= n else same if same is not None else nbytes[i]
+        # the checks of _buf in line: this loop is most of a short call's time on the host
+        if x is None or type(x) is int:
+            arr[i] = x
+        elif x.is_cuda and x.is_contiguous() and x.numel() * x.element_size() >= need:
+            arr[i] = x.data_ptr()
+        else:
+            arr[i] = _buf(x, need, f"{what}[{i}]")
     return arr
+
+
+@functools.lru_cache(maxsize=None)
+def _ptr_array(n):
+    return ctypes.c_void_p * max(1, n)
+
+
+@functools.lru_cache(maxsize=None)
+def _int64_array(n):
+    return ctypes.c_int64 * max(1, n)
+
+
+_TORCH_DTYPE = {}
 
 
 def _dtype_code(x):
@@ -187,8 +209,10 @@ def _dtype_code(x):
         return _DTYPE[x]
     if isinstance(x, int):
         return x
-    import torch
-    return {torch.bfloat16: GC_BF16, torch.float32: GC_FP32, torch.int32: GC_INT32, torch.uint8: GC_MX8}[x]
+    if not _TORCH_DTYPE:
+        import torch
+        _TORCH_DTYPE.update({torch.bfloat16: GC_BF16, torch.float32: GC_FP32, torch.int32: GC_INT32, torch.uint8: GC_MX8})
+    return _TORCH_DTYPE[x]
 
 
 def _enum(table, x):
@@ -207,13 +231,18 @@ def gc_pointers(tensors):
     return _bufs(xs, len(xs), 0, "gc_pointers")
 
 
+# The current stream's handle without building a Stream object (2 us of a call).
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, like=None):
     """HIP stream handle: an explicit int / torch stream, else torch's current stream on like's device."""
     if stream is None:
-        import torch
         dev = like.device if hasattr(like, "device") and like.device.type == "cuda" else None
-        if dev is None and not torch.cuda.is_available():
-            return None
+        if dev is None:
+            return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if _raw_stream is not None and dev.index is not None:
+            return _raw_stream(dev.index)
         return torch.cuda.current_stream(dev).cuda_stream
     if isinstance(stream, int):
         return stream
@@ -389,7 +418,7 @@ def gc_fsdp2_all_gather(shards, params, rows, cols, nranks, dtype, stream=None):
 
 def _i64_array(xs):
     xs = [int(x) for x in xs]
-    return (ctypes.c_int64 * max(1, len(xs)))(*xs)
+    return _int64_array(len(xs))(*xs)
 
 
 def gc_moe_route_scratch_bytes(ntokens, topk, experts_per_rank):
