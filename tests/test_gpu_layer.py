@@ -1,0 +1,372 @@
+"""The layer's operators as a training step uses them together, captured in graphs,
+on several streams, over many tiles and past 4 GiB."""
+
+import numpy as np
+import pytest
+import torch
+
+import collective_communication_reduction_amd as gc
+from gen.workloads import route_tokens
+from oracle import layer as L
+from tests import test_gpu_ffn as F
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+U, HALF = 2.0 ** -24, 2.0 ** -8
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _rel(a, b):
+    return np.linalg.norm(a - b) / max(np.linalg.norm(b), 1e-300)
+
+
+class Layer:
+    """norm (+ residual) -> 8-bit rows -> route, dispatch -> experts -> combine, and the way back."""
+
+    def __init__(self, N, E, K, T, H, I, seed):
+        rng = np.random.default_rng(seed)
+        self.N, self.E, self.K, self.T, self.H, self.I = N, E, K, T, H, I
+        bf = lambda shape, s: F._bf16(rng, shape, s).to(DEV)  # noqa: E731
+        self.x = [bf((t, H), 0.5) for t in T]
+        self.res = [bf((t, H), 2.0) for t in T]
+        self.w = [bf((H,), 1.0) for _ in T]
+        self.weights = {"w_gate": [bf((E, I, H), H ** -0.5) for _ in T], "w_up": [bf((E, I, H), H ** -0.5) for _ in T],
+                        "w_down": [bf((E, H, I), I ** -0.5) for _ in T]}
+        self.gate = [torch.from_numpy(rng.random((t, K)).astype(np.float32)).to(DEV) for t in T]
+        self.dout = [bf((t, H), 1.0) for t in T]
+        self.dres = [bf((t, H), 1.0) for t in T]
+        self.experts = [torch.zeros(t, K, dtype=torch.int32, device=DEV) for t in T]
+        self.set_routing(seed)
+        e = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+        self.cap = [sum(T) * K] * N                                  # any routing fits
+        rb, sb = gc.gc_mx8_row_bytes(H), gc.gc_mx8_row_bytes(2 * I)
+        self.rb = rb
+        self.sum, self.y8 = [e(t, H) for t in T], [e(t, rb, dt=torch.uint8) for t in T]
+        self.rstd = [e(t, dt=torch.float32) for t in T]
+        self.splits = e(N * N * E, dt=torch.int64)
+        self.dest = [e(t * K, 2, dt=torch.int32) for t in T]
+        self.rscratch = e(max(256, gc.gc_moe_route_scratch_bytes(T, K, E)), dt=torch.uint8)
+        self.recv = [e(c, rb, dt=torch.uint8) for c in self.cap]
+        self.saved = [e(c, sb, dt=torch.uint8) for c in self.cap]
+        self.yexp, self.dyexp, self.dxexp = ([e(c, H) for c in self.cap] for _ in range(3))
+        self.scratch = e(gc.gc_moe_ffn_scratch_bytes(self.cap, E, H, I, x_dtype="mx8", backward=True), dt=torch.uint8)
+        self.out, self.dn, self.dx = ([e(t, H) for t in T] for _ in range(3))
+        self.dgate = [e(t, K, dt=torch.float32) for t in T]
+        self.dw = {k: [torch.zeros_like(t) for t in v] for k, v in self.weights.items()}
+        self.dnorm = [e(H, dt=torch.float32) for _ in T]
+        self.nscratch = e(gc.gc_rms_norm_backward_scratch_bytes(T, H), dt=torch.uint8)
+        self.ones = [torch.ones(t, K, device=DEV) for t in T]
+
+    def set_routing(self, seed):
+        for s, t in enumerate(self.T):
+            if t:
+                r = route_tokens(seed, s, t, self.N * self.E, self.K, 1.1)
+                self.experts[s].copy_(torch.from_numpy(r.astype(np.int32)))
+
+    def step(self):
+        T, H, I, K, E, W = self.T, self.H, self.I, self.K, self.E, self.weights
+        gc.gc_rms_norm(self.x, self.w, T, H, self.y8, residual=self.res, sum_out=self.sum, rstd=self.rstd)
+        gc.gc_moe_route(self.experts, T, K, E, self.splits, self.dest, self.rscratch)
+        gc.gc_moe_dispatch(self.y8, T, self.dest, K, self.rb, self.recv, self.cap)
+        gc.gc_moe_ffn(self.recv, self.cap, self.splits, E, H, I, W["w_gate"], W["w_up"], W["w_down"], self.yexp,
+                      self.scratch, saved=self.saved)
+        gc.gc_moe_combine(self.yexp, self.cap, self.dest, self.gate, T, K, H, "bf16", self.out)
+        gc.gc_moe_combine_backward(self.dout, self.yexp, self.cap, self.dest, self.gate, T, K, H, "bf16", self.dyexp,
+                                   self.dgate)
+        gc.gc_moe_ffn_backward(self.dyexp, self.recv, self.saved, self.cap, self.splits, E, H, I, W["w_gate"], W["w_up"],
+                               W["w_down"], self.dxexp, self.dw["w_gate"], self.dw["w_up"], self.dw["w_down"], self.scratch)
+        gc.gc_moe_combine(self.dxexp, self.cap, self.dest, self.ones, T, K, H, "bf16", self.dn)   # gradient of dispatch
+        gc.gc_rms_norm_backward(self.dn, self.sum, self.w, self.rstd, T, H, self.dx, self.dnorm, self.nscratch,
+                                dsum=self.dres)
+
+    def outputs(self):
+        flat = lambda d: [t for k in sorted(d) for t in d[k]]  # noqa: E731
+        return [*self.out, *self.dgate, *flat(self.dw), *self.dx, *self.dnorm]
+
+    def reference(self):
+        """The step in 64 bits on the values the 8-bit rows stand for; gradients pass the quantisation unchanged."""
+        N, E, K, H = self.N, self.E, self.K, self.H
+        w = {k: [_f64(t) for t in v] for k, v in self.weights.items()}
+        n8 = [L.unpack8(t.cpu().numpy(), H) for t in self.y8]
+        out, dgate, dw, dx, dnorm = [], [], {k: [np.zeros(t.shape) for t in v] for k, v in self.weights.items()}, [], []
+        for s in range(N):
+            T = self.T[s]
+            sm = _f64((self.x[s].float() + self.res[s].float()).bfloat16())
+            ex, g, do = self.experts[s].cpu().numpy(), _f64(self.gate[s]), _f64(self.dout[s])
+            o, dg, dn = np.zeros((T, H)), np.zeros((T, K)), np.zeros((T, H))
+            for e in range(N * E):
+                t, k = np.nonzero(ex == e)
+                if not len(t):
+                    continue
+                r, j = divmod(e, E)
+                wg, wu, wd = (w[q][r][j] for q in ("w_gate", "w_up", "w_down"))
+                ga, up, _, y = L.ffn(n8[s][t], wg, wu, wd)
+                np.add.at(o, t, g[t, k][:, None] * y)
+                dg[t, k] = (do[t] * y).sum(1)
+                b = L.ffn_backward(g[t, k][:, None] * do[t], n8[s][t], ga, up, wg, wu, wd)
+                np.add.at(dn, t, b["dx"])
+                for q, v in (("w_gate", "dwg"), ("w_up", "dwu"), ("w_down", "dwd")):
+                    dw[q][r][j] += b[v]
+            _, rs = L.rms_norm(sm, _f64(self.w[s])[None], 1e-6)
+            a, b = L.rms_norm_backward(dn, sm, _f64(self.w[s])[None], rs, _f64(self.dres[s]))
+            out.append(o), dgate.append(dg), dx.append(a), dnorm.append(b)
+        return [*out, *dgate, *[t for k in sorted(dw) for t in dw[k]], *dx, *dnorm]
+
+
+def check_layer(layer):
+    """Against 64 bits in the 2-norm.  Outputs are a chain of independent roundings, each within half a step of its value:
+    out and the gate gradients pass h, y and out in bf16 (3 half steps); the gradients pass the 8-bit checkpoints
+    (2^-4 of each value), whose effect on silu and silu' of order-1 arguments is at most about twice that."""
+    got, want = layer.outputs(), layer.reference()
+    n = layer.N
+    for i, (a, b) in enumerate(zip(got, want)):
+        if not b.size:
+            continue
+        limit = 4 * HALF if i < 2 * n else 2 * 2.0 ** -4
+        assert _rel(_f64(a), b) <= limit, (i, _rel(_f64(a), b))
+
+
+def test_layer_step():
+    layer = Layer(4, 2, 2, [70, 0, 33, 129], 128, 96, 3)
+    layer.step()
+    torch.cuda.synchronize()
+    check_layer(layer)
+
+
+def test_layer_step_replayed_from_a_graph():
+    """One training step of the layer in a HIP graph, replayed with new tokens and routing and eager work in between."""
+    layer = Layer(2, 3, 2, [65, 40], 64, 64, 5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer.step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.step()
+    rng = np.random.default_rng(8)
+    for rep in range(4):
+        layer.set_routing(20 + rep)
+        for t in (*layer.x, *layer.dout):
+            t.copy_(F._bf16(rng, tuple(t.shape)))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in layer.outputs()]
+        check_layer(layer)
+        layer.step()                                      # the eager result of the same inputs, bit for bit
+        torch.cuda.synchronize()
+        for a, b in zip(replayed, layer.outputs()):
+            assert torch.equal(a, b), f"replay {rep}"
+
+
+def test_two_layers_on_two_streams_at_once():
+    a, b = Layer(2, 2, 2, [90, 31], 128, 64, 1), Layer(2, 2, 2, [17, 80], 128, 64, 2)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(sa):
+            a.step()
+        with torch.cuda.stream(sb):
+            b.step()
+    torch.cuda.synchronize()
+    check_layer(a)
+    check_layer(b)
+
+
+def test_explicit_stream():
+    """A call given a stream runs there, not on the current one: it waits for that stream's earlier work."""
+    x = torch.zeros(300, 4096, dtype=torch.bfloat16, device=DEV)
+    w, y = torch.ones(4096, dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+    big = torch.empty(1 << 28, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        big.normal_()
+        x.fill_(2.0)
+    gc.gc_rms_norm([x], [w], [300], 4096, [y], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, torch.ones_like(y))
+
+
+# ------------------------------------------------------------------ many tiles
+
+def test_many_tiles_forward():
+    """More tiles than workgroups, in every tile height: each workgroup goes through several, with partial last ones."""
+    rng = np.random.default_rng(0)
+    for counts, H, I in (([[230 + 13 * (e % 5) for e in range(8)], [200, 500, 0, 257, 256, 255, 1, 300]], 192, 2304),
+                         ([[100 + e for e in range(16)]], 640, 1088), ([[20 + (e * 7) % 60 for e in range(24)]], 1032, 1056)):
+        st = F.make(rng, counts, H, I)
+        xv, y, saved = F.run_forward(st, "bf16", "mx8")
+        F.check_forward(st, xv, y, saved, "mx8")
+
+
+def test_many_tiles_backward():
+    """Weight products whose tiles sum 0, 1, 63, 64, 65, ... rows one after the other in one workgroup, and
+    row products over several tiles a workgroup."""
+    rng = np.random.default_rng(1)
+    edges = [0, 1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 0, 300, 2, 64, 64, 320, 63, 0, 0, 256, 130, 7, 66]
+    for counts, H, I in (([edges], 776, 544), ([[210 + 9 * (e % 7) for e in range(6)], [250] * 6], 2056, 264)):
+        st = F.make(rng, counts, H, I)
+        gate_up = [F._bf16(rng, (r, 2 * I), 1.5) for r in st["rows"]]
+        dy = [F._bf16(rng, (r, H)) for r in st["rows"]]
+        xv, sv, dx, dw = F.run_backward(st, "bf16", "bf16", "bf16", gate_up, dy)
+        F.check_backward(st, xv, sv, dy, dx, dw, "bf16")
+
+
+def test_results_do_not_depend_on_other_work():
+    """The same call twice, and beside a copy on another stream: bit for bit the same (no unordered sums)."""
+    rng = np.random.default_rng(2)
+    st = F.make(rng, [[130, 300, 5, 64]], 512, 384)
+    gate_up = [F._bf16(rng, (r, 768), 1.0) for r in st["rows"]]
+    dy = [F._bf16(rng, (r, 512)) for r in st["rows"]]
+    first = F.run_backward(st, "bf16", "mx8", "fp32", gate_up, dy)
+    s = torch.cuda.Stream()
+    a = torch.empty(1 << 27, device=DEV)
+    with torch.cuda.stream(s):
+        for _ in range(4):
+            a.mul_(1.0)
+    second = F.run_backward(st, "bf16", "mx8", "fp32", gate_up, dy)
+    torch.cuda.synchronize()
+    for k in first[3]:
+        for p, q in zip(first[3][k], second[3][k]):
+            assert torch.equal(p, q)
+    for p, q in zip(first[2], second[2]):
+        assert torch.equal(p, q)
+
+
+# ------------------------------------------------------------------ serving
+
+@pytest.mark.parametrize("counts,H,I", [
+    ([[40, 0, 0, 0, 0, 0, 1, 0]], 4104, 1032),             # an expert's rows in several turns, sums with a tail
+    ([[0, 17, 0, 0, 16], [15, 0, 1, 3, 0]], 520, 2056), ([[7] * 8], 1024, 264),
+    ([[1, 0, 2] for _ in range(9)], 264, 4096), ([[1]], 8200, 8)])
+@pytest.mark.parametrize("x_t", ["bf16", "mx8"])
+def test_few_rows_per_expert(counts, H, I, x_t):
+    st = F.make(np.random.default_rng(H), counts, H, I)
+    xv, y, saved = F.run_forward(st, x_t, None)
+    F.check_forward(st, xv, y, saved, None)
+
+
+def test_serving_step_replayed_from_a_graph():
+    """One token through norm and experts in a graph; its routing and values change between the replays."""
+    rng = np.random.default_rng(6)
+    st = F.make(rng, [[1, 0, 0, 1]], 512, 256, spare=0)
+    w = F.dev(st["w_gate"]), F.dev(st["w_up"]), F.dev(st["w_down"])
+    x, norm_w = torch.zeros(2, 512, dtype=torch.bfloat16, device=DEV), torch.ones(512, dtype=torch.bfloat16, device=DEV)
+    n, y = torch.empty_like(x), torch.empty_like(x)
+    splits = st["splits_dev"]
+    _, scratch = F.scratch_for(st, "bf16", False)
+
+    def step():
+        gc.gc_rms_norm([x], [norm_w], [2], 512, [n])
+        gc.gc_moe_ffn([n], [2], splits, 4, 512, 256, *w, [y], scratch)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for counts in ([2, 0, 0, 0], [0, 1, 1, 0], [0, 0, 0, 2], [1, 0, 1, 0]):
+        x.copy_(F._bf16(rng, (2, 512)))
+        splits.copy_(torch.tensor(counts))
+        y.fill_(F.FILL)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for e, c in enumerate(counts):
+            want = L.ffn(_f64(n[at:at + c]), *(_f64(t[0][e]) for t in w))[3]
+            assert not c or _rel(_f64(y[at:at + c]), want) <= 2 * HALF      # h and y are rounded to bf16
+            at += c
+
+
+# ------------------------------------------------------------------ past 4 GiB
+
+ROWS, H4 = 600_000, 4096                                   # 4.9 GB of bf16
+
+
+def _some_rows(n):
+    return torch.tensor([0, 1, 524_287, 524_288, 524_289, n - 2, n - 1], device=DEV)
+
+
+def test_norm_and_rows_past_4_gib():
+    x = torch.empty(ROWS, H4, dtype=torch.bfloat16, device=DEV).normal_()
+    w = torch.ones(H4, dtype=torch.bfloat16, device=DEV)
+    y8 = torch.empty(ROWS, gc.gc_mx8_row_bytes(H4), dtype=torch.uint8, device=DEV)
+    rstd = torch.empty(ROWS, device=DEV)
+    gc.gc_rms_norm([x], [w], [ROWS], H4, [y8], rstd=[rstd])
+    back = torch.empty_like(x)
+    gc.gc_mx8_unpack([y8], [ROWS], H4, [back])
+    at = _some_rows(ROWS)
+    from tests.test_gpu_norm import _sum_error, check_rows8
+    want, _ = L.rms_norm(_f64(x[at]), np.ones((1, H4)), 1e-6)
+    check_rows8(y8[at].cpu().numpy(), want, _sum_error(H4) / 2 + 6 * U)
+    assert np.array_equal(_f64(back[at]), L.unpack8(y8[at].cpu().numpy(), H4))
+    again = torch.empty_like(y8)
+    gc.gc_mx8_pack([back], [ROWS], H4, [again])            # an 8-bit row's values are kept by another round trip; its codes
+    twice = torch.empty_like(back)                         # need not be: an amax rounded down to 224*2^e takes the scale e-1,
+    gc.gc_mx8_unpack([again], [ROWS], H4, [twice])         # under which every value of the block is still representable
+    assert torch.equal(twice, back)
+    del again, twice
+    dx, dw = torch.empty_like(x), torch.empty(H4, device=DEV)
+    scratch = torch.empty(gc.gc_rms_norm_backward_scratch_bytes([ROWS], H4), dtype=torch.uint8, device=DEV)
+    gc.gc_rms_norm_backward([back], [x], [w], [rstd], [ROWS], H4, [dx], [dw], scratch)
+    torch.cuda.synchronize()
+    a, _ = L.rms_norm_backward(_f64(back[at]), _f64(x[at]), np.ones((1, H4)), _f64(rstd[at]))
+    assert np.all(np.abs(_f64(dx[at]) - a) <= HALF * np.abs(a) + 1e-4)
+    ref = torch.zeros(H4, dtype=torch.float64, device=DEV)
+    mag = torch.zeros(H4, dtype=torch.float64, device=DEV)
+    for i in range(0, ROWS, 50_000):
+        p = back[i:i + 50_000].double() * x[i:i + 50_000].double() * rstd[i:i + 50_000, None].double()
+        ref += p.sum(0)
+        mag += p.abs().sum(0)
+    assert bool(((dw.double() - ref).abs() <= (ROWS / 1024 + 1024 + 8) * U * mag).all())
+
+
+def test_experts_past_4_gib():
+    E, I = 2, 64
+    counts = [350_001, ROWS - 350_001]
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rnd = lambda *s, sc=1.0: torch.empty(*s, dtype=torch.bfloat16, device=DEV).normal_(0, sc, generator=g)  # noqa: E731
+    x, dy = rnd(ROWS, H4), rnd(ROWS, H4)
+    wg, wu, wd = rnd(E, I, H4, sc=H4 ** -0.5), rnd(E, I, H4, sc=H4 ** -0.5), rnd(E, H4, I, sc=I ** -0.5)
+    splits = torch.tensor(counts, dtype=torch.int64, device=DEV)
+    y, saved = torch.empty_like(x), torch.empty(ROWS, 2 * I, dtype=torch.bfloat16, device=DEV)
+    scratch = torch.empty(gc.gc_moe_ffn_scratch_bytes([ROWS], E, H4, I, backward=True), dtype=torch.uint8, device=DEV)
+    gc.gc_moe_ffn([x], [ROWS], splits, E, H4, I, [wg], [wu], [wd], [y], scratch, saved=[saved])
+    dx = torch.empty_like(x)
+    dwg, dwu, dwd = torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
+    gc.gc_moe_ffn_backward([dy], [x], [saved], [ROWS], splits, E, H4, I, [wg], [wu], [wd], [dx], [dwg], [dwu], [dwd], scratch)
+    torch.cuda.synchronize()
+    for r in _some_rows(ROWS).tolist() + [counts[0] - 1, counts[0]]:
+        e = int(r >= counts[0])
+        args = [_f64(t[e]) for t in (wg, wu, wd)]
+        gt, up, _, want = L.ffn(_f64(x[r:r + 1]), *args)
+        assert _rel(_f64(y[r:r + 1]), want) <= 2 * HALF and _rel(_f64(saved[r:r + 1]), np.concatenate([gt, up], 1)) <= HALF
+        sv = _f64(saved[r:r + 1])
+        b = L.ffn_backward(_f64(dy[r:r + 1]), _f64(x[r:r + 1]), sv[:, :I], sv[:, I:], *args)
+        assert _rel(_f64(dx[r:r + 1]), b["dx"]) <= 2 * HALF
+    at = 0
+    for e, n in enumerate(counts):
+        refs = [torch.zeros(I, H4, dtype=torch.float64, device=DEV), torch.zeros(I, H4, dtype=torch.float64, device=DEV),
+                torch.zeros(H4, I, dtype=torch.float64, device=DEV)]
+        for i in range(at, at + n, 50_000):
+            s = slice(i, min(i + 50_000, at + n))
+            gt, up, d = saved[s, :I].double(), saved[s, I:].double(), dy[s].double()
+            sg = torch.sigmoid(gt)
+            dh = d @ wd[e].double()
+            refs[0] += (dh * up * sg * (1 + gt * (1 - sg))).T @ x[s].double()
+            refs[1] += (dh * gt * sg).T @ x[s].double()
+            refs[2] += d.T @ (gt * sg * up)
+        at += n
+        for got, ref in zip((dwg[e], dwu[e], dwd[e]), refs):
+            assert float((got.double() - ref).norm() / ref.norm()) <= 2 * HALF
