@@ -342,6 +342,58 @@ __device__ __forceinline__ void unpack_half(const u32x4& o, float (&v)[8]) {
   }
 }
 
+// Register index against lane within each quad: afterwards v[k] of lane q is
+// what v[q] of the quad's lane k was.
+template <class V>
+__device__ __forceinline__ void transpose_quad(V (&v)[4], int lane) {
+  const auto trade = [](V& x, V& y, bool odd, auto ctrl) {  // lanes with the bit take x from the partner's y, the others y from its x
+    const V px = x, py = y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t fx = __builtin_amdgcn_update_dpp(0, px[i], decltype(ctrl)::value, 0xf, 0xf, true);
+      const uint32_t fy = __builtin_amdgcn_update_dpp(0, py[i], decltype(ctrl)::value, 0xf, 0xf, true);
+      x[i] = odd ? fy : px[i];
+      y[i] = odd ? py[i] : fx;
+    }
+  };
+  constexpr std::integral_constant<int, 0xB1> xor1{};  // lanes 1 0 3 2
+  constexpr std::integral_constant<int, 0x4E> xor2{};  // lanes 2 3 0 1
+  trade(v[0], v[1], lane & 1, xor1);
+  trade(v[2], v[3], lane & 1, xor1);
+  trade(v[0], v[2], lane & 2, xor2);
+  trade(v[1], v[3], lane & 2, xor2);
+}
+
+// Two blocks x, y as bf16 for stores of 64 contiguous bytes per quad: lane l holds, of
+// block l / 32, columns 8 (l % 4) .. + 7 of row 4 (l % 32 / 4) + k as v[k].
+__device__ __forceinline__ void pack_two(const f32x16& x, const f32x16& y, int lane, u32x4 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t a0 = bf16_bits(x[4 * j]) | (bf16_bits(x[4 * j + 1]) << 16);
+    uint32_t a1 = bf16_bits(x[4 * j + 2]) | (bf16_bits(x[4 * j + 3]) << 16);
+    uint32_t b0 = bf16_bits(y[4 * j]) | (bf16_bits(y[4 * j + 1]) << 16);
+    uint32_t b1 = bf16_bits(y[4 * j + 2]) | (bf16_bits(y[4 * j + 3]) << 16);
+    swap_halves(a0, b0);
+    swap_halves(a1, b1);
+    v[j] = u32x4{a0, a1, b0, b1};
+  }
+  transpose_quad(v, lane);
+}
+
+// The same in fp32, 16 of the 32 columns at a time: columns 16 p + 4 (l % 4) .. + 3.
+__device__ __forceinline__ void trade_two(const f32x16& x, const f32x16& y, int p, int lane, u32x4 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a = __float_as_uint(x[8 * p + 4 * j + i]), b = __float_as_uint(y[8 * p + 4 * j + i]);
+      swap_halves(a, b);
+      v[2 * j][i] = a;
+      v[2 * j + 1][i] = b;
+    }
+  transpose_quad(v, lane);
+}
+
 // bf16 store of a block: columns n0 .. n0 + 31 of the lane's row (ok: the row exists).
 __device__ __forceinline__ void store_block(char* row, uint64_t n0, uint64_t N, bool ok, int lane, const f32x16& v) {
 #pragma unroll
@@ -589,8 +641,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
       to1 = {pick(in1, cur.A, then.A), pick(in1, cur.B, then.B), in1 ? k0 + 3 * kTileK : kTileK, in1 ? K : then_K};
       step(A1, B1, A0, B0, to1, to0);
     }
-    const bool odd = k0 < K || K == 0;
-    if (odd) {  // one more step, from buffer 0; the next tile's fragments are read after the epilogue
+    if (k0 < K || K == 0) {  // one more step, from buffer 0
       if (K <= kTileK) {
         __builtin_amdgcn_s_waitcnt(kLoadsDone);  // of what was loaded into buffer 1 for this tile: nothing, as zeros
         to1 = {then.A, then.B, kTileK, then_K};
@@ -681,43 +732,36 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
           }
         }
       }
-    } else if constexpr (!WGRAD) {
+    } else {
+      // Rows mb .. + 3 of two blocks side by side.  H and F are multiples of 8, so
+      // of a weight gradient all four exist or none, and in one of its matrices.
+      const int64_t mb = m0 + (wm * MB + i) * 32 + (lane & 28);
+      const uint64_t M = KIND == kDwDown ? H : KIND == kDwGateUp ? 2 * F : sg.rows, N = KIND == kDwDown ? F : H;
+      constexpr int ES = F32OUT ? 4 : 2;
+      char* out;
+      if constexpr (KIND == kDwDown) out = sg.dw_down + mb * N * ES;
+      else if constexpr (KIND == kDwGateUp) out = static_cast<uint64_t>(mb) < F ? sg.dw_gate + mb * N * ES : sg.dw_up + (mb - static_cast<int64_t>(F)) * N * ES;
+      else out = sg.y + mb * N * ES;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          __builtin_amdgcn_sched_barrier(0);
-          store_block(sg.y + m * H * 2, n0 + (wn * NB + j) * 32, H, m < sg.rows, lane, acc[i][j]);
-        }
-      } else {
-        constexpr int ES = F32OUT ? 4 : 2;
-        const uint64_t M = KIND == kDwDown ? H : 2 * F, N = KIND == kDwDown ? F : H;
-        const bool row = static_cast<uint64_t>(m) < M;
-        char* out;
-        if constexpr (KIND == kDwDown) out = sg.dw_down + m * N * ES;
-        else out = static_cast<uint64_t>(m) < F ? sg.dw_gate + m * N * ES : sg.dw_up + (m - static_cast<int64_t>(F)) * N * ES;
+      for (int p = 0; p < (F32OUT ? 2 : 1); ++p) {
+        __builtin_amdgcn_sched_barrier(0);
+        const uint64_t n = n0 + (wn * NB + (lane >> 5)) * 32 + (F32OUT ? 16 * p + 4 * (lane & 3) : 8 * (lane & 3));
+        u32x4 v[4];
+        if constexpr (F32OUT) trade_two(acc[i][0], acc[i][1], p, lane, v);
+        else pack_two(acc[i][0], acc[i][1], lane, v);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          __builtin_amdgcn_sched_barrier(0);
-          const uint64_t n = n0 + (wn * NB + j) * 32;
-          if constexpr (F32OUT) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint64_t c = n + 8 * q + 4 * (lane >> 5);
-              if (row && c < N)
-                *reinterpret_cast<u32x4*>(out + c * 4) =
-                    u32x4{__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
-                          __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])};
-            }
-          } else {
-            store_block(out, n, N, row, lane, acc[i][j]);
-          }
-        }
+        for (int k = 0; k < 4; ++k)
+          if (static_cast<uint64_t>(mb + (WGRAD ? 0 : k)) < M && n < N) *reinterpret_cast<u32x4*>(out + (k * N + n) * ES) = v[k];
       }
     }
-    if (!more) break;
-    if (odd) {
-      loads_barrier();
-      read(A0, B0, 0);
     }
+    // Every way to the next tile waits here, the last one's too.  Waiting only
+    // after an odd number of steps would be enough, but the compiler then sees a
+    // way to the loop with buffer 0 still loading and waits for every load at the
+    // loop's head (3 to 5 % of a large product).
+    loads_barrier();
+    if (!more) break;
+    read(A0, B0, 0);
     cur = then;
   }
 }
