@@ -14,6 +14,14 @@
 // values); the second kind is read through the transposing LDS load, so no
 // operand is ever laid out again in memory.
 //
+// h, dgate and dup are kept as bf16 between the products: one more rounding of half
+// a step, of the same size as the result's own, averaged over the rows and sums
+// that a value enters.  With few rows per expert little is averaged, and the
+// products wait for the weights anyway: there (SPLIT) each is kept as the sum of two
+// bf16 values, the second the first's rounding error (within 2^-17 of the value
+// together).  A row product's tile then holds 32 rows and 32 rests, whose results
+// its two halves add; a weight gradient sums over the rows and then the rests.
+//
 // The number of rows of each expert is known on the device alone (the routing
 // plan's split table): a plan kernel turns it into a table of blocks and row
 // tiles, and the grid is sized for the most tiles those rows can make.
@@ -31,6 +39,7 @@ using namespace gcdev;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef gci::FfnSeg Seg;
 
 constexpr int kTileN = 256;
@@ -198,6 +207,7 @@ struct Tile {
   ConstSeg* sg;
   Side A, B;
   uint32_t K;              // below 2^31
+  uint32_t part, sum;      // split operands: the length of each part (a multiple of 64), the summed values in it
   int64_t m0, n0;
 };
 
@@ -209,7 +219,7 @@ __device__ __forceinline__ Side pick(bool c, const Side& x, const Side& y) {
 // One step's loads: summed indices from k0 of K.
 struct Load {
   Side a, b;
-  uint32_t k0, K;
+  uint32_t k0, K, part, sum;
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // past every descriptor's range, whatever is added: the load gives zeros
@@ -441,6 +451,12 @@ __device__ __forceinline__ void load_half8(const char* row, uint64_t n, uint64_t
   }
 }
 
+// What rounding v to bf16 takes away; nothing where that is not finite.
+__device__ __forceinline__ float rounded_off(float v) {
+  const float d = v - __uint_as_float(bf16_bits(v) << 16);
+  return fabsf(d) < __builtin_inff() ? d : 0.0f;
+}
+
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // Instruction classes of the scheduling barriers.
@@ -474,8 +490,10 @@ enum SavedKind { kNoSaved, kSaved16, kSaved8 };
 // A product's tiles of TM x 256 outputs, by eight wavefronts: two along the
 // rows, four along the columns, each with MB x 2 blocks of 32 x 32.
 // SAVED: the checkpoint's type (kGateUp, kDh).  F32OUT: fp32 weight gradients.
-template <int KIND, int TM, int SAVED, bool F32OUT>
-__global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel(const GemmArgs a) {
+// SPLIT: rows of h are [h | rest], of g [dgate | dup | rests of both], each part
+// padded to a multiple of 64 values with zeros, and row tiles half as high.
+template <int KIND, int TM, int SAVED, bool F32OUT, bool SPLIT>
+__global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == kDown || KIND == kDx)) ? 4 : 2) ffn_gemm_kernel(const GemmArgs a) {
   constexpr int WM = 2, WN = kWaves / WM;
   constexpr int MB = TM / WM / 32, NB = kTileN / WN / 32;
   constexpr bool WGRAD = KIND == kDwDown || KIND == kDwGateUp;
@@ -490,9 +508,15 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / WN, wn = w % WN;
   const uint64_t H = a.H, F = a.F;
+  const uint64_t FP = SPLIT ? (F + 63) & ~uint64_t(63) : F;          // a part
+  const uint64_t FH = SPLIT ? 2 * FP : F, FG = (SPLIT ? 4 : 2) * FP;  // values per row of h and g
+  constexpr bool PARTS = SPLIT && (KIND == kDx || WGRAD);             // sums over two parts
+  constexpr bool RESTS = SPLIT && (KIND == kDown || KIND == kDx);     // rests in the tile's second half
+  constexpr int ROWS = SPLIT && !WGRAD ? TM / 2 : TM;                 // rows per tile
+  __shared__ f32x4 rests[RESTS ? WN : 1][RESTS ? NB * 4 : 1][kWave];
   constexpr bool A_WIDE = KIND == kDx || KIND == kDwGateUp;  // rows of 2F values
-  const Loader<A_KC, TM, false> load_a(KIND == kGateUp || KIND == kDh || KIND == kDwDown ? H * 2 : A_WIDE ? F * 4 : F * 2, w, lane);
-  const Loader<B_KC, kTileN, KIND == kGateUp> load_b(KIND == kGateUp || KIND == kDx || KIND == kDwGateUp ? H * 2 : F * 2, w, lane);
+  const Loader<A_KC, TM, RESTS> load_a(KIND == kGateUp || KIND == kDh || KIND == kDwDown ? H * 2 : A_WIDE ? FG * 2 : FH * 2, w, lane);
+  const Loader<B_KC, kTileN, KIND == kGateUp> load_b(KIND == kGateUp || KIND == kDx || KIND == kDwGateUp ? H * 2 : KIND == kDwDown ? FH * 2 : F * 2, w, lane);
   const uint32_t total = a.mtiles * a.ntiles * (WGRAD ? a.segs_n : 1u);  // below 2^31, checked on the host
 
   // Tile t of the product.  Tiles are numbered four row tiles deep, so that
@@ -510,33 +534,38 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
     if (seg < 0) return false;
     const ConstSeg& sg = as_constant(a.segs)[seg];
     r.sg = &sg;
-    const int64_t m0 = r.m0 = static_cast<int64_t>(WGRAD ? mt : mt - sg.tile0) * TM;
+    const int64_t m0 = r.m0 = static_cast<int64_t>(WGRAD ? mt : mt - sg.tile0) * ROWS;
     const int64_t n0 = r.n0 = static_cast<int64_t>(nt) * (KIND == kGateUp ? kTileN / 2 : kTileN);
     Side &A = r.A, &B = r.B;
+    const uint32_t rows64 = (static_cast<uint32_t>(sg.rows) + 63) & ~63u;
+    r.part = WGRAD ? rows64 : static_cast<uint32_t>(FP);
+    r.sum = WGRAD ? static_cast<uint32_t>(sg.rows) : static_cast<uint32_t>(F);
     const auto left = [](int64_t most, uint64_t n) { return static_cast<int32_t>(std::min<int64_t>(most, n)); };
     if constexpr (KIND == kGateUp) {
       r.K = H;
-      A = {sg.x + m0 * H * 2, nullptr, left(TM, sg.rows - m0)};
+      A = {sg.x + m0 * H * 2, nullptr, left(ROWS, sg.rows - m0)};
       B = {sg.w_gate + n0 * H * 2, sg.w_up + n0 * H * 2, left(kTileN / 2, F - n0)};
     } else if constexpr (KIND == kDown) {
       r.K = F;
-      A = {a.h + (sg.row + m0) * F * 2, nullptr, left(TM, sg.rows - m0)};
+      A = {a.h + (sg.row + m0) * FH * 2, a.h + ((sg.row + m0) * FH + FP) * 2, left(ROWS, sg.rows - m0)};
       B = {sg.w_down + n0 * F * 2, nullptr, left(kTileN, H - n0)};
     } else if constexpr (KIND == kDh) {
       r.K = H;
-      A = {sg.dy + m0 * H * 2, nullptr, left(TM, sg.rows - m0)};
+      A = {sg.dy + m0 * H * 2, nullptr, left(ROWS, sg.rows - m0)};
       B = {sg.w_down + n0 * 2, nullptr, left(kTileN, F - n0)};
     } else if constexpr (KIND == kDx) {
-      r.K = 2 * F;
-      A = {a.g + (sg.row + m0) * F * 4, nullptr, left(TM, sg.rows - m0)};
+      r.K = 2 * FP;
+      A = {a.g + (sg.row + m0) * FG * 2, a.g + ((sg.row + m0) * FG + 2 * FP) * 2, left(ROWS, sg.rows - m0)};
       B = {sg.w_gate + n0 * 2, sg.w_up + n0 * 2, left(kTileN, H - n0)};
     } else if constexpr (KIND == kDwDown) {
-      r.K = sg.rows;
+      r.K = SPLIT ? 2 * rows64 : sg.rows;
       A = {sg.dy + m0 * 2, nullptr, left(TM, H - m0)};
-      B = {a.h + (sg.row * F + n0) * 2, nullptr, left(kTileN, F - n0)};
+      B = {a.h + (sg.row * FH + n0) * 2, nullptr, left(kTileN, F - n0)};
+      B.p2 = B.p + FP * 2;
     } else {
-      r.K = sg.rows;
-      A = {a.g + (sg.row * 2 * F + m0) * 2, nullptr, left(TM, 2 * F - m0)};
+      r.K = SPLIT ? 2 * rows64 : sg.rows;
+      A = {a.g + (sg.row * FG + m0) * 2, nullptr, left(TM, 2 * FP - m0)};
+      A.p2 = A.p + FP * 4;
       B = {sg.x + n0 * 2, nullptr, left(kTileN, H - n0)};
     }
     return true;
@@ -579,14 +608,26 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
   // Loads of one step that run behind the barrier (the first SPLIT_A and SPLIT_B
   // instructions of each operand) and the rest, in the step that follows.
   constexpr int SPLIT_A = LA * 2 / 4, SPLIT_B = LB * 2 / 4;
-  auto load_first = [&](char* ta, char* tb, const Load& l) {
-    load_a.template run<0, SPLIT_A>(ta, l.a, l.k0, l.K, NO_K1);
-    load_b.template run<0, SPLIT_B>(tb, l.b, l.k0, l.K, K1);
+  // The operand in one of the parts, of which `second` are read from p2.
+  auto in_part = [](const Side& x, bool second) -> Side { return {second ? x.p2 : x.p, nullptr, x.n}; };
+  auto load = [&](auto i0, auto a1, auto j0, auto b1, char* ta, char* tb, const Load& l) {
+    if constexpr (PARTS) {
+      const uint32_t q = uniform(l.k0 >= l.part), k = uniform(l.k0 - q * l.part);
+      if constexpr (WGRAD) load_a.template run<i0.value, a1.value>(ta, in_part(l.a, KIND == kDwGateUp && q), k, l.sum, NO_K1);
+      else load_a.template run<i0.value, a1.value>(ta, l.a, l.k0, l.K, NO_K1);
+      load_b.template run<j0.value, b1.value>(tb, in_part(l.b, (KIND == kDx || KIND == kDwDown) && q), k, l.sum, NO_K1);
+    } else {
+      load_a.template run<i0.value, a1.value>(ta, l.a, l.k0, l.K, NO_K1);
+      load_b.template run<j0.value, b1.value>(tb, l.b, l.k0, l.K, K1);
+    }
   };
-  auto load_rest = [&](char* ta, char* tb, const Load& l) {
-    load_a.template run<SPLIT_A, LA>(ta, l.a, l.k0, l.K, NO_K1);
-    load_b.template run<SPLIT_B, LB>(tb, l.b, l.k0, l.K, K1);
-  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, SPLIT_A> ca{};
+  constexpr std::integral_constant<int, SPLIT_B> cb{};
+  constexpr std::integral_constant<int, LA> ea{};
+  constexpr std::integral_constant<int, LB> eb{};
+  auto load_first = [&](char* ta, char* tb, const Load& l) { load(c0, ca, c0, cb, ta, tb, l); };
+  auto load_rest = [&](char* ta, char* tb, const Load& l) { load(ca, ea, cb, eb, ta, tb, l); };
   // One step of 64 summed values from buffer (ta, tb), whose first fragments are
   // read already.  Fragments are read 16 summed values ahead of the matrix
   // instructions, across the barrier too: behind it the buffer is free, the
@@ -614,7 +655,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
 
   Tile cur;
   if (!advance(cur)) return;
-  Load to0{cur.A, cur.B, 0, cur.K}, to1{cur.A, cur.B, kTileK, cur.K};  // what each buffer is filled from
+  Load to0{cur.A, cur.B, 0, cur.K, cur.part, cur.sum}, to1{cur.A, cur.B, kTileK, cur.K, cur.part, cur.sum};  // what each buffer is filled from
   load_first(A0, B0, to0);
   load_rest(A0, B0, to0);
   load_first(A1, B1, to1);
@@ -627,7 +668,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
     Tile then = cur;
     const bool more = advance(then);
-    const uint32_t then_K = more ? then.K : 0;
+    const uint32_t then_K = more ? then.K : 0, then_sum = more ? then.sum : 0;
     // Two steps a turn, one from each buffer: with the buffers known at compile
     // time the reads of one need not wait for the loads into the other.  A
     // tile starts in buffer 0; its last steps already load the next tile's first
@@ -636,15 +677,17 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
     uint32_t k0 = 0;
     for (; k0 + kTileK < K; k0 += 2 * kTileK) {
       const bool in0 = k0 + 2 * kTileK < K, in1 = k0 + 3 * kTileK < K;
-      to0 = {pick(in0, cur.A, then.A), pick(in0, cur.B, then.B), in0 ? k0 + 2 * kTileK : 0, in0 ? K : then_K};
+      to0 = {pick(in0, cur.A, then.A), pick(in0, cur.B, then.B), in0 ? k0 + 2 * kTileK : 0, in0 ? K : then_K,
+             in0 ? cur.part : then.part, in0 ? cur.sum : then_sum};
       step(A0, B0, A1, B1, to0, to1);
-      to1 = {pick(in1, cur.A, then.A), pick(in1, cur.B, then.B), in1 ? k0 + 3 * kTileK : kTileK, in1 ? K : then_K};
+      to1 = {pick(in1, cur.A, then.A), pick(in1, cur.B, then.B), in1 ? k0 + 3 * kTileK : kTileK, in1 ? K : then_K,
+             in1 ? cur.part : then.part, in1 ? cur.sum : then_sum};
       step(A1, B1, A0, B0, to1, to0);
     }
     if (k0 < K || K == 0) {  // one more step, from buffer 0
       if (K <= kTileK) {
         __builtin_amdgcn_s_waitcnt(kLoadsDone);  // of what was loaded into buffer 1 for this tile: nothing, as zeros
-        to1 = {then.A, then.B, kTileK, then_K};
+        to1 = {then.A, then.B, kTileK, then_K, then.part, then_sum};
         load_first(A1, B1, to1);
       }
 #pragma unroll
@@ -654,7 +697,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
       }
       multiply(STEPS - 1);
       loads_barrier();
-      to0 = {then.A, then.B, 0, then_K};
+      to0 = {then.A, then.B, 0, then_K, then.part, then_sum};
       load_first(A0, B0, to0);
       load_rest(A0, B0, to0);
     }
@@ -664,11 +707,28 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
     asm volatile("" : "+v"(lane));
     ConstSeg& sg = *cur.sg;
     const int64_t m0 = cur.m0, n0 = cur.n0;
+    if constexpr (RESTS) {
+      static_assert(MB == 1, "one block of rows, one of rests");
+      if (wm == 1) {
+#pragma unroll
+        for (int e = 0; e < NB * 4; ++e)
+          rests[wn][e][lane] = f32x4{acc[0][e / 4][e % 4 * 4], acc[0][e / 4][e % 4 * 4 + 1], acc[0][e / 4][e % 4 * 4 + 2], acc[0][e / 4][e % 4 * 4 + 3]};
+      }
+      __syncthreads();
+      if (wm == 0) {
+#pragma unroll
+        for (int e = 0; e < NB * 4; ++e) {
+          const f32x4 q = rests[wn][e][lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[0][e / 4][e % 4 * 4 + i] += q[i];
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int64_t m = m0 + (wm * MB + i) * 32 + (lane & 31);
       if constexpr (KIND == kGateUp) {
-        const bool row = m < sg.rows;
+        const bool row = m < sg.rows && (!SPLIT || wm == 0);
 #pragma unroll
         for (int j = 0; j < NB / 2; ++j) {
           __builtin_amdgcn_sched_barrier(0);
@@ -676,8 +736,14 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
           const f32x16 &gate = acc[i][j], &up = acc[i][NB / 2 + j];
           f32x16 hv;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) hv[e] = gate[e] * sigmoid(gate[e]) * up[e];
-          store_block(a.h + (sg.row + m) * F * 2, n, F, row, lane, hv);
+          for (int e = 0; e < 16; ++e) hv[e] = SPLIT && n + 8 * (e / 4) >= F ? 0.0f : gate[e] * sigmoid(gate[e]) * up[e];
+          char* const out_h = a.h + (sg.row + m) * FH * 2;
+          store_block(out_h, n, FP, row, lane, hv);
+          if constexpr (SPLIT) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) hv[e] = rounded_off(hv[e]);
+            store_block(out_h + FP * 2, n, FP, row, lane, hv);
+          }
           if constexpr (SAVED == kSaved16) {
             store_block(sg.saved + m * a.saved_row, n, F, row, lane, gate);
             store_block(sg.saved + m * a.saved_row + F * 2, n, F, row, lane, up);
@@ -690,13 +756,13 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
           }
         }
       } else if constexpr (KIND == kDh) {
-        const bool row = m < sg.rows;
+        const bool row = m < sg.rows && (!SPLIT || wm == 0);
         const char* in = sg.saved + static_cast<uint64_t>(std::min<int64_t>(m, sg.rows - 1)) * a.saved_row;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           __builtin_amdgcn_sched_barrier(0);
           const uint64_t n = n0 + (wn * NB + j) * 32;
-          if (n >= F) continue;
+          if (n >= FP) continue;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {  // half a block at a time, to hold few registers
           const uint64_t c = n + 8 * (2 * p + (lane >> 5));
@@ -706,41 +772,47 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
             unpack_half(*reinterpret_cast<const u32x4*>(in + in_c * 2), gate);
             unpack_half(*reinterpret_cast<const u32x4*>(in + (F + in_c) * 2), up);
           } else {
-            load_half8(in, 2 * F, n, p, lane, gate);
-            load_half8(in, 2 * F, F + n, p, lane, up);
+            const uint64_t in_n = std::min<uint64_t>(n, F - 32);
+            load_half8(in, 2 * F, in_n, p, lane, gate);
+            load_half8(in, 2 * F, F + in_n, p, lane, up);
           }
-          const bool ok = row && c < F;
-          char* const out_h = a.h + (sg.row + m) * F * 2 + c * 2;
-          char* const out_g = a.g + (sg.row + m) * F * 4 + c * 2;
+          const bool ok = row && c < FP;
+          char* const out_h = a.h + (sg.row + m) * FH * 2 + c * 2;
+          char* const out_g = a.g + (sg.row + m) * FG * 2 + c * 2;
+          auto put = [&](char* out, uint64_t rest) {  // r, zeros in a part's padding
+            const u32x4 o = pack_half(r);
+            if (ok) *reinterpret_cast<u32x4*>(out) = SPLIT && c >= F ? u32x4{} : o;
+            if constexpr (SPLIT) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) r[e] = rounded_off(r[e]);
+              const u32x4 q = pack_half(r);
+              if (ok) *reinterpret_cast<u32x4*>(out + rest * 2) = c >= F ? u32x4{} : q;
+            }
+          };
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             sig[e] = sigmoid(gate[e]);
             r[e] = gate[e] * sig[e] * up[e];
           }
-          const u32x4 hv = pack_half(r);
+          put(out_h, FP);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             r[e] = acc[i][j][8 * p + e] * up[e] * (sig[e] * (1.0f + gate[e] * (1.0f - sig[e])));
-          const u32x4 dg = pack_half(r);
+          put(out_g, 2 * FP);
 #pragma unroll
           for (int e = 0; e < 8; ++e) r[e] = acc[i][j][8 * p + e] * (gate[e] * sig[e]);
-          const u32x4 du = pack_half(r);
-          if (ok) {
-            *reinterpret_cast<u32x4*>(out_h) = hv;
-            *reinterpret_cast<u32x4*>(out_g) = dg;
-            *reinterpret_cast<u32x4*>(out_g + F * 2) = du;
-          }
+          put(out_g + FP * 2, 2 * FP);
         }
       }
     } else {
       // Rows mb .. + 3 of two blocks side by side.  H and F are multiples of 8, so
       // of a weight gradient all four exist or none, and in one of its matrices.
       const int64_t mb = m0 + (wm * MB + i) * 32 + (lane & 28);
-      const uint64_t M = KIND == kDwDown ? H : KIND == kDwGateUp ? 2 * F : sg.rows, N = KIND == kDwDown ? F : H;
+      const uint64_t M = KIND == kDwDown ? H : KIND == kDwGateUp ? FP + F : RESTS && wm == 1 ? 0 : sg.rows, N = KIND == kDwDown ? F : H;
       constexpr int ES = F32OUT ? 4 : 2;
       char* out;
       if constexpr (KIND == kDwDown) out = sg.dw_down + mb * N * ES;
-      else if constexpr (KIND == kDwGateUp) out = static_cast<uint64_t>(mb) < F ? sg.dw_gate + mb * N * ES : sg.dw_up + (mb - static_cast<int64_t>(F)) * N * ES;
+      else if constexpr (KIND == kDwGateUp) out = static_cast<uint64_t>(mb) < FP ? sg.dw_gate + mb * N * ES : sg.dw_up + (mb - static_cast<int64_t>(FP)) * N * ES;
       else out = sg.y + mb * N * ES;
 #pragma unroll
       for (int p = 0; p < (F32OUT ? 2 : 1); ++p) {
@@ -751,7 +823,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
         else pack_two(acc[i][0], acc[i][1], lane, v);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (static_cast<uint64_t>(mb + (WGRAD ? 0 : k)) < M && n < N) *reinterpret_cast<u32x4*>(out + (k * N + n) * ES) = v[k];
+          if (static_cast<uint64_t>(mb + (WGRAD ? 0 : k)) < M && n < N && !(SPLIT && KIND == kDwGateUp && static_cast<uint64_t>(mb) >= F && static_cast<uint64_t>(mb) < FP)) *reinterpret_cast<u32x4*>(out + (k * N + n) * ES) = v[k];
       }
     }
     }
@@ -774,11 +846,11 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 ? 4 : 2) ffn_gemm_kernel
 // straight into the matrix instructions' registers (16 rows x 32 summed values
 // each, 64 bytes a row and instruction, kFewLoads KiB in flight).  The
 // workgroup's eight wavefronts are `shares` shares of 8 / shares column groups;
-// shares are added through LDS in a fixed order.  The expert's rows are found
+// shares are added through LDS in a fixed order.  h is kept as two bf16 values here
+// too: the down product takes eight rows at a time, with their rests as the other
+// eight columns of the matrix instructions.  The expert's rows are found
 // from the split table by the workgroup itself, so the whole forward is two
 // launches.
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFewWaves = 8;
 constexpr int kFewLoads = 8;  // weight vectors in flight per lane
@@ -807,6 +879,7 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t x) {
 template <bool GATE_UP, int P>
 __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P> a) {
   constexpr int U = GATE_UP ? kFewLoads / 2 : kFewLoads;
+  constexpr int TURN = GATE_UP ? 16 : 8;  // rows at a time; down: beside their rests
   __shared__ f32x4 part[kFewWaves][GATE_UP ? 2 : 1][kWave];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const uint32_t share = w % a.shares, group = w / a.shares, groups = kFewWaves / a.shares;
@@ -829,12 +902,12 @@ __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P
   const uint64_t w0 = (static_cast<uint64_t>(e) * a.n + col) * a.K * 2;
   const char* const wa = a.wa[d] + w0;
   const char* const wb = GATE_UP ? a.wb[d] + w0 : nullptr;
-  for (int64_t m0 = 0; m0 < rows; m0 += 16) {
-    const int64_t m = min(m0 + (lane & 15), rows - 1);
-    const char* const x = GATE_UP ? a.x[d] + (start + m) * a.K * 2 : a.h + (a.base[d] + start + m) * a.K * 2;
+  for (int64_t m0 = 0; m0 < rows; m0 += TURN) {
+    const int64_t m = min(m0 + lane % TURN, rows - 1);
+    const char* const x = GATE_UP ? a.x[d] + (start + m) * a.K * 2 : a.h + ((a.base[d] + start + m) * 2 + (lane >> 3 & 1)) * a.K * 2;
     f32x4 ga{}, ua{};
     for (uint64_t k0 = static_cast<uint64_t>(share) * 32 * U; k0 < a.K; k0 += 32 * U * a.shares) {
-      u32x4 va[U], vb[U], vx[U];
+      u32x4 va[U], vb[U], vx[U];  // vb: up
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const uint64_t k = k0 + i * 32 + (lane >> 4) * 8;
@@ -863,15 +936,25 @@ __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P
         ga += part[w + q][0][lane];
         if constexpr (GATE_UP) ua += part[w + q][1][lane];
       }
-      // lane l: row m0 + l % 16, columns n0 + 4 (l / 16) .. + 3
+      if constexpr (!GATE_UP) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ga[i] += __shfl_xor(ga[i], 8);
+      }
+      // lane l: row m0 + l % 16 (down: and its rest, l % 8), columns n0 + 4 (l / 16) .. + 3
       const uint64_t n = n0 + 4 * (lane >> 4);
-      if (m0 + (lane & 15) < rows && n < a.n) {
+      if (m0 + lane % TURN < rows && (lane & 15) < TURN && n < a.n) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = GATE_UP ? ga[i] * sigmoid(ga[i]) * ua[i] : ga[i];
-        char* const out = GATE_UP ? a.h + (a.base[d] + start + m) * a.n * 2 : a.y[d] + (start + m) * a.n * 2;
+        char* const out = GATE_UP ? a.h + (a.base[d] + start + m) * a.n * 4 : a.y[d] + (start + m) * a.n * 2;
         *reinterpret_cast<u32x2*>(out + n * 2) =
             u32x2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+        if constexpr (GATE_UP) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = rounded_off(v[i]);
+          *reinterpret_cast<u32x2*>(out + (a.n + n) * 2) =
+              u32x2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+        }
       }
     }
     __syncthreads();
@@ -968,19 +1051,28 @@ template <int KIND, int SAVED>
 gc_status row_product(GemmArgs a, const gci::FfnGeom& g, int64_t ntiles, hipStream_t stream) {
   a.mtiles = g.tiles;
   a.ntiles = ntiles;
-  const uint64_t grid = grid_for(a.mtiles * a.ntiles, g.tile_rows == 64 ? 2 : 1);
-  if (g.tile_rows == 256) return launch(ffn_gemm_kernel<KIND, 256, SAVED, false>, a, grid, 64 * kWaves, stream);
-  if (g.tile_rows == 128) return launch(ffn_gemm_kernel<KIND, 128, SAVED, false>, a, grid, 64 * kWaves, stream);
-  return launch(ffn_gemm_kernel<KIND, 64, SAVED, false>, a, grid, 64 * kWaves, stream);
+  const uint64_t grid = grid_for(a.mtiles * a.ntiles, g.tile_rows > 64 || (g.split && (KIND == kDown || KIND == kDx)) ? 1 : 2);
+  if (g.split) return launch(ffn_gemm_kernel<KIND, 64, SAVED, false, true>, a, grid, 64 * kWaves, stream);
+  if (g.tile_rows == 256) return launch(ffn_gemm_kernel<KIND, 256, SAVED, false, false>, a, grid, 64 * kWaves, stream);
+  if (g.tile_rows == 128) return launch(ffn_gemm_kernel<KIND, 128, SAVED, false, false>, a, grid, 64 * kWaves, stream);
+  return launch(ffn_gemm_kernel<KIND, 64, SAVED, false, false>, a, grid, 64 * kWaves, stream);
 }
 
-template <int KIND>
+template <int KIND, bool SPLIT>
 gc_status weight_product(GemmArgs a, uint64_t M, uint64_t N, bool f32, hipStream_t stream) {
   a.mtiles = ceil_div(M, 256);
   a.ntiles = ceil_div(N, kTileN);
   const uint64_t grid = grid_for(a.mtiles * a.ntiles * a.segs_n, 1);
-  if (f32) return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, true>, a, grid, 64 * kWaves, stream);
-  return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, false>, a, grid, 64 * kWaves, stream);
+  if (f32) return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, true, SPLIT>, a, grid, 64 * kWaves, stream);
+  return launch(ffn_gemm_kernel<KIND, 256, kNoSaved, false, SPLIT>, a, grid, 64 * kWaves, stream);
+}
+
+template <bool SPLIT>
+gc_status weight_gradients(const gci::FfnCall& c, const GemmArgs& a) {
+  const gc_status st = weight_product<kDwDown, SPLIT>(a, c.hidden, c.inter, c.dw_t == GC_FP32, c.stream);
+  if (st != GC_OK) return st;
+  const uint64_t part = SPLIT ? (c.inter + 63) & ~uint64_t(63) : c.inter;
+  return weight_product<kDwGateUp, SPLIT>(a, 2 * part, c.hidden, c.dw_t == GC_FP32, c.stream);
 }
 
 // Shares of the summed index: about four turns of a wavefront's loads each, so
@@ -1059,9 +1151,7 @@ gc_status launch_moe_ffn_backward(const FfnCall& c) {
     if (st == GC_OK) st = row_product<kDx, kNoSaved>(a, g, ceil_div(c.hidden, kTileN), c.stream);
     if (st != GC_OK) return st;
   }
-  st = weight_product<kDwDown>(a, c.hidden, c.inter, c.dw_t == GC_FP32, c.stream);
-  if (st != GC_OK) return st;
-  return weight_product<kDwGateUp>(a, 2 * c.inter, c.hidden, c.dw_t == GC_FP32, c.stream);
+  return g.split ? weight_gradients<true>(c, a) : weight_gradients<false>(c, a);
 }
 
 }  // namespace gci

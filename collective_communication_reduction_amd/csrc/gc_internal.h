@@ -271,7 +271,8 @@ struct FfnGeom {
   int64_t rows = 0;          // of all ranks
   int32_t segs = 0;          // experts of all ranks
   int32_t tile_rows = 0;     // rows per tile of the row products
-  bool few = false;          // few rows per expert: the serving forward streams the weights instead
+  bool split = false;        // few rows per expert: h and the gradients of gate and up are kept in two parts
+  bool few = false;          // and the serving forward streams the weights instead
   int64_t tiles = 0;         // most row tiles the experts' blocks can make
   uint64_t map = 0, x = 0, h = 0, g = 0, bytes = 0;  // offsets (segment table at 0) and total
 };
