@@ -9,7 +9,9 @@
 // 64 x 2 units take one wavefront each (no barrier), longer ones a workgroup
 // (4096 bf16, 512 units: 630 us with a workgroup's 2 units per lane, 641 with a
 // wavefront's 8, for 8 x 16384 rows), and rows past a workgroup's registers are
-// read a second time (from the caches, mostly).
+// read a second time (from the caches, mostly).  Those 8 x 16384 rows: forward to
+// 8-bit rows 630 us, 6.0 TB/s; backward 790 us, 5.3 TB/s (three streams read, one
+// written).
 
 #include <algorithm>
 #include <type_traits>

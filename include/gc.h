@@ -385,8 +385,8 @@ gc_status gc_mx8_unpack(const void* const* packed, const int64_t* rows, int nran
  *                      residual[r] itself.
  *   y[r]               rows of y_t: t, or GC_MX8 (8-bit rows, from y in fp32).
  *   rstd[r]            DEVICE fp32 [ntokens[r]], for the backward; may be NULL.
- * Rows of all ranks below 2^31.  A zero row gives zeros.  Other overlaps of
- * outputs with anything are refused.
+ * Rows of all ranks below 2^31.  A zero row gives zeros where eps > 0.  Other
+ * overlaps of outputs with anything are refused.
  */
 gc_status gc_rms_norm(const void* const* x, const void* const* residual, const void* const* weight,
                       const int64_t* ntokens, int nranks, size_t hidden, float eps, gc_dtype t,
@@ -432,8 +432,9 @@ gc_status gc_rms_norm_backward(const void* const* dy, const void* const* dsum, c
  *   y[d]       DEVICE bf16 [rows[d]] rows of hidden.
  *   scratch    DEVICE, 256-byte aligned, gc_moe_ffn_scratch_bytes() bytes;
  *              calls that may run at once need one each.
- * Sums are fp32; h is rounded to bf16 (it feeds the second product), gate and
- * up only where they are saved.  Rows of y and saved that no expert takes keep
+ * Sums are fp32; h is rounded to bf16 (it feeds the second product; with fewer
+ * than 8 rows per expert or 64 in all to two bf16 values, 16 bits), gate and up
+ * only where they are saved.  Rows of y and saved that no expert takes keep
  * what they held.  hidden is a multiple of 8, inter of 8 (of 32 with GC_MX8
  * checkpoints), both at most 2^20; nranks * E <= 8192; rows of all ranks below
  * 2^31 (GC_ERR_UNSUPPORTED beyond).  All buffers are 16-byte aligned; outputs
@@ -453,7 +454,8 @@ gc_status gc_moe_ffn(const void* const* x, gc_dtype x_t, const int64_t* rows, co
  *   dh = dy Wd,  dgate = dh * up * silu'(gate),  dup = dh * silu(gate),
  *   dx = dgate Wg + dup Wu,
  *   dWg = dgate^T x,  dWu = dup^T x,  dWd = dy^T h   per expert.
- * dgate, dup and h are rounded to bf16 between the products; sums are fp32.
+ * dgate, dup and h are rounded between the products as h is in the forward;
+ * sums are fp32.
  *   dx[d]                   DEVICE bf16 rows of hidden; rows that no expert takes keep
  *                           what they held.
  *   dw_gate, dw_up, dw_down  shaped as the weights, of type dw_t (GC_BF16 or
