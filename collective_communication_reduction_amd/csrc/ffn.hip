@@ -973,8 +973,6 @@ __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P
 
 // ------------------------------------------------------------------ host side
 
-uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
-
 template <class Kern, class A>
 gc_status launch(Kern kernel, const A& args, uint64_t grid, uint32_t threads, hipStream_t stream) {
   void* params[] = {const_cast<A*>(&args)};
