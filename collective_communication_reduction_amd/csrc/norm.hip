@@ -89,7 +89,10 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs<P> a) {
     residual_sum<U>(xv[j], rv[j], a.has_res, v[j], s);
     if (a.has_sum && ok) U::store(sum + lane + j * LANES, s);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) ss = fmaf(ok ? v[j][e] : 0.0f, v[j][e], ss);
+    for (int e = 0; e < VE; ++e) {
+      const float q = ok ? v[j][e] : 0.0f;  // both factors: 0 times an infinity in the row's last unit would be NaN
+      ss = fmaf(q, q, ss);
+    }
   }
   const float rs = 1.0f / sqrtf(lanes_sum<LANES>(ss, lds) / static_cast<float>(a.H) + a.eps);
   if (a.has_rstd && lane == 0) a.rstd[rank][row] = rs;
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(LANES) norm_backward_kernel(const NormBackward
       for (int e = 0; e < VE; ++e) {
         const float g = y[e] * (n[e] * rs);
         dw[j][e] += g;
-        dot = fmaf(ok[j] ? g : 0.0f, w[e], dot);
+        dot = ok[j] ? fmaf(g, w[e], dot) : dot;  // not 0 * w: the clamped weight may be infinite
       }
     }
     const float mean = lanes_sum<LANES>(dot, lds) / static_cast<float>(a.H);

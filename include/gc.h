@@ -385,8 +385,10 @@ gc_status gc_mx8_unpack(const void* const* packed, const int64_t* rows, int nran
  *                      residual[r] itself.
  *   y[r]               rows of y_t: t, or GC_MX8 (8-bit rows, from y in fp32).
  *   rstd[r]            DEVICE fp32 [ntokens[r]], for the backward; may be NULL.
- * Rows of all ranks below 2^31.  A zero row gives zeros where eps > 0.  Other
- * overlaps of outputs with anything are refused.
+ * Rows of all ranks below 2^31.  A zero row gives zeros where eps > 0.  A row
+ * with an infinity in any column, or whose squares sum past fp32's range, has
+ * rstd 0: its finite values give zeros, an infinity gives NaN.  A NaN makes its
+ * whole row NaN.  Other overlaps of outputs with anything are refused.
  */
 gc_status gc_rms_norm(const void* const* x, const void* const* residual, const void* const* weight,
                       const int64_t* ntokens, int nranks, size_t hidden, float eps, gc_dtype t,
