@@ -436,7 +436,8 @@ gc_status gc_rms_norm_backward(const void* const* dy, const void* const* dsum, c
  *              calls that may run at once need one each.
  * Sums are fp32; h is rounded to bf16 (it feeds the second product; where the
  * buffers hold fewer than 8 rows per expert, or 64 in all, to two bf16 values,
- * 16 bits), gate and up only where they are saved.  Rows of y and saved that no
+ * 16 bits), gate and up only where they are saved.  Infinite and NaN operands give
+ * what the formulas give, whatever the number of rows.  Rows of y and saved that no
  * expert takes keep what they held.  hidden is a multiple of 8, inter of 8 (of 32 with GC_MX8
  * checkpoints), both at most 2^20; nranks * E <= 8192; rows of all ranks below
  * 2^31 (GC_ERR_UNSUPPORTED beyond).  All buffers are 16-byte aligned; outputs
