@@ -154,6 +154,19 @@ gc_status launch_moe_combine(const MoeMoveCall& call);
 
 // ---- operators of the layer around the experts (norm.hip, mx8.hip, moe_grad.hip, ffn.hip)
 
+// A launch holds fewer than 2^32 work items in a dimension, so a longer grid goes
+// in launches of at most 2^31, one after the other on the stream.
+// one(first, n) launches workgroups first .. first + n - 1 of `blocks`.
+template <class F>
+gc_status in_launches(uint64_t blocks, uint32_t threads, F one) {
+  const uint64_t most = (uint64_t(1) << 31) / threads;
+  for (uint64_t b = 0; b < blocks; b += most) {
+    const gc_status st = one(static_cast<uint32_t>(b), static_cast<uint32_t>(blocks - b < most ? blocks - b : most));
+    if (st != GC_OK) return st;
+  }
+  return GC_OK;
+}
+
 // Bytes of an 8-bit row of n values: codes, a scale per 32 values, zeros to a multiple of 16.
 inline uint64_t mx8_row_bytes(uint64_t n) { return (n + (n + 31) / 32 + 15) / 16 * 16; }
 

@@ -27,7 +27,8 @@ struct CombineBackwardArgs {
   float* dw[P];
   int64_t rows[P];
   int64_t tok[P];
-  int32_t tile0[P + 1];
+  int32_t tile0[P + 1];  // first workgroup of each rank
+  uint32_t block0;       // first workgroup of this launch
   uint64_t R;            // units per row
   int32_t N, K, lanes_log2;
 };
@@ -41,8 +42,9 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Combin
   const int K = KT > 0 ? KT : a.K;
   const int S = 1 << a.lanes_log2;
   const int lane = threadIdx.x & (S - 1);
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
-  const int64_t t = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * (kThreads >> a.lanes_log2) +
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t t = static_cast<int64_t>(block - a.tile0[rank]) * (kThreads >> a.lanes_log2) +
                     (threadIdx.x >> a.lanes_log2);
   const bool live = t < a.tok[rank];
   const int64_t tc = live ? t : a.tok[rank] - 1;  // the last token again: reads stay inside, nothing is written
@@ -133,12 +135,14 @@ gc_status combine_backward_impl(const gci::MoeCombineBackwardCall& c, CombineBac
     run += static_cast<int32_t>((c.tokens[s] + per - 1) / per);
   }
   for (int s = c.nranks; s <= P; ++s) a.tile0[s] = run;
-  if (!run) return GC_OK;
   void* params[] = {&a};
   const void* k = c.topk == 1   ? reinterpret_cast<const void*>(combine_backward_kernel<In, VEC, 1, P>)
                   : c.topk == 2 ? reinterpret_cast<const void*>(combine_backward_kernel<In, VEC, 2, P>)
                                 : reinterpret_cast<const void*>(combine_backward_kernel<In, VEC, 0, P>);
-  return gci::hip_status(hipLaunchKernel(k, dim3(run), dim3(kThreads), params, 0, c.stream));
+  return gci::in_launches(run, kThreads, [&](uint32_t first, uint32_t blocks) {
+    a.block0 = first;
+    return gci::hip_status(hipLaunchKernel(k, dim3(blocks), dim3(kThreads), params, 0, c.stream));
+  });
 }
 
 template <class In, int P>

@@ -22,6 +22,7 @@ struct Mx8Args {
   char* dst[P];
   int64_t rows[P];
   int32_t tile0[P + 1];  // first workgroup of each rank
+  uint32_t block0;       // first workgroup of this launch
   uint64_t n;            // values per row
   uint64_t row8;         // bytes per 8-bit row
   int32_t N;
@@ -32,9 +33,10 @@ __global__ void __launch_bounds__(kThreads) mx8_pack_kernel(const Mx8Args<P> a) 
   typedef RowUnit<In, VEC> U;
   typedef typename U::T T;
   constexpr int VE = U::VE;
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
   const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * (kThreads / LANES) +
+  const int64_t row = static_cast<int64_t>(block - a.tile0[rank]) * (kThreads / LANES) +
                       threadIdx.x / LANES;
   if (row >= a.rows[rank]) return;
   const uint64_t units = a.n / VE;
@@ -64,9 +66,10 @@ __global__ void __launch_bounds__(kThreads) mx8_unpack_kernel(const Mx8Args<P> a
   typedef typename U::T T;
   constexpr int VE = U::VE;
   typedef typename std::conditional<VE == 8, u32x2, typename std::conditional<VE == 4, uint32_t, uint8_t>::type>::type C;
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
   const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * (kThreads / LANES) +
+  const int64_t row = static_cast<int64_t>(block - a.tile0[rank]) * (kThreads / LANES) +
                       threadIdx.x / LANES;
   if (row >= a.rows[rank]) return;
   const uint64_t units = a.n / VE;
@@ -116,14 +119,16 @@ gc_status mx8_impl(const gci::Mx8Call& c, Mx8Args<P>& a) {
     run += static_cast<int32_t>((c.rows[s] + per - 1) / per);
   }
   for (int s = c.nranks; s <= P; ++s) a.tile0[s] = run;
-  if (!run) return GC_OK;
   void* params[] = {&a};
   const void* k;
   if (c.unpack) k = wave ? reinterpret_cast<const void*>(mx8_unpack_kernel<In, VEC, kWave, P>)
                          : reinterpret_cast<const void*>(mx8_unpack_kernel<In, VEC, kThreads, P>);
   else k = wave ? reinterpret_cast<const void*>(mx8_pack_kernel<In, VEC, kWave, P>)
                 : reinterpret_cast<const void*>(mx8_pack_kernel<In, VEC, kThreads, P>);
-  return gci::hip_status(hipLaunchKernel(k, dim3(run), dim3(kThreads), params, 0, c.stream));
+  return gci::in_launches(run, kThreads, [&](uint32_t first, uint32_t blocks) {
+    a.block0 = first;
+    return gci::hip_status(hipLaunchKernel(k, dim3(blocks), dim3(kThreads), params, 0, c.stream));
+  });
 }
 
 template <class In, int P>

@@ -32,6 +32,7 @@ struct NormArgs {
   float* rstd[P];
   int64_t tok[P];
   int32_t tile0[P + 1];  // first workgroup of each rank
+  uint32_t block0;       // first workgroup of this launch
   uint64_t H;            // elements per row
   uint64_t y_row;        // bytes per output row
   float eps;
@@ -62,9 +63,10 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs<P> a) {
   typedef typename U::T T;
   constexpr int VE = U::VE;
   __shared__ float lds[kThreads / kWave];
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
   const int lane = threadIdx.x % LANES;
-  const int64_t row = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * (kThreads / LANES) +
+  const int64_t row = static_cast<int64_t>(block - a.tile0[rank]) * (kThreads / LANES) +
                       threadIdx.x / LANES;
   if (row >= a.tok[rank]) return;  // whole wavefronts (LANES == kThreads: never)
   const uint64_t units = a.H / VE;
@@ -119,8 +121,9 @@ __global__ void __launch_bounds__(kThreads) norm_long_kernel(const NormArgs<P> a
   typedef typename U::T T;
   constexpr int VE = U::VE;
   __shared__ float lds[kThreads / kWave];
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
-  const int64_t row = static_cast<int32_t>(blockIdx.x) - a.tile0[rank];
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t row = block - a.tile0[rank];
   const uint64_t units = a.H / VE;
   const T* x = reinterpret_cast<const T*>(a.x[rank]) + row * units;
   const T* r = reinterpret_cast<const T*>(a.res[rank]) + row * units;
@@ -173,6 +176,7 @@ struct NormBackwardArgs {
   float* dw[P];
   int64_t tok[P];
   int32_t tile0[P + 1];  // first block of each rank; block b leaves its partial in row b of `partial`
+  uint32_t block0;       // first workgroup of this launch
   float* partial;
   uint64_t H;
   int64_t rows_per_block;
@@ -190,8 +194,9 @@ __global__ void __launch_bounds__(LANES) norm_backward_kernel(const NormBackward
   typedef typename U::T T;
   constexpr int VE = U::VE;
   __shared__ float lds[LANES / kWave];
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
-  const int64_t first = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * a.rows_per_block;
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t first = static_cast<int64_t>(block - a.tile0[rank]) * a.rows_per_block;
   const int64_t last = min(first + a.rows_per_block, a.tok[rank]);
   const uint64_t units = a.H / VE;
   uint32_t c[NV];  // the lane's units; past the row's end its last unit again
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(LANES) norm_backward_kernel(const NormBackward
       if (ok[j]) U::store(dx + c[j], U::narrow(d));
     }
   }
-  float* part = a.partial + static_cast<uint64_t>(blockIdx.x) * a.H;
+  float* part = a.partial + static_cast<uint64_t>(block) * a.H;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if (ok[j])
@@ -284,12 +289,13 @@ __global__ void __launch_bounds__(kThreads) norm_backward_long_kernel(const Norm
   typedef typename U::T T;
   constexpr int VE = U::VE;
   __shared__ float lds[kThreads / kWave];
-  const int rank = rank_of<P>(a.tile0, a.N, blockIdx.x);
-  const int64_t first = static_cast<int64_t>(static_cast<int32_t>(blockIdx.x) - a.tile0[rank]) * a.rows_per_block;
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t first = static_cast<int64_t>(block - a.tile0[rank]) * a.rows_per_block;
   const int64_t last = min(first + a.rows_per_block, a.tok[rank]);
   const uint64_t units = a.H / VE;
   const T* wt = reinterpret_cast<const T*>(a.w[rank]);
-  float* part = a.partial + static_cast<uint64_t>(blockIdx.x) * a.H;
+  float* part = a.partial + static_cast<uint64_t>(block) * a.H;
   for (int64_t row = first; row < last; ++row) {
     const T* dy = reinterpret_cast<const T*>(a.dy[rank]) + row * units;
     const T* ds = reinterpret_cast<const T*>(a.dsum[rank]) + row * units;
@@ -332,7 +338,7 @@ template <int P>
 __global__ void __launch_bounds__(kThreads) norm_weight_kernel(const NormBackwardArgs<P> a) {
   __shared__ float lds[kThreads / kWave][kWave];
   const int rank = blockIdx.y, w = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const uint64_t col = static_cast<uint64_t>(blockIdx.x) * kWave + lane;
+  const uint64_t col = (static_cast<uint64_t>(a.block0) + blockIdx.x) * kWave + lane;
   constexpr int Q = kThreads / kWave;
   float acc = 0.0f;
   if (col < a.H) {
@@ -355,10 +361,14 @@ __global__ void __launch_bounds__(kThreads) norm_weight_kernel(const NormBackwar
 
 // ------------------------------------------------------------- host side
 
+// `blocks` workgroups in x, `ranks` in y.
 template <class Kern, class A>
-gc_status launch(Kern kernel, const A& args, dim3 grid, hipStream_t stream, int threads = kThreads) {
-  void* params[] = {const_cast<A*>(&args)};
-  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), params, 0, stream));
+gc_status launch(Kern kernel, A& args, uint64_t blocks, hipStream_t stream, int threads = kThreads, int ranks = 1) {
+  void* params[] = {&args};
+  return gci::in_launches(blocks, threads, [&](uint32_t first, uint32_t n) {
+    args.block0 = first;
+    return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(n, ranks), dim3(threads), params, 0, stream));
+  });
 }
 
 uint64_t addr(const void* p) { return reinterpret_cast<uint64_t>(p); }
@@ -379,9 +389,7 @@ template <class In, bool VEC, bool MX, int P>
 gc_status norm_impl(const gci::NormCall& c, NormArgs<P>& a) {
   const uint64_t units = c.hidden / RowUnit<In, VEC>::VE;
   const int64_t per = units <= 2 * kWave ? kThreads / kWave : 1;
-  const int32_t grid = fill_tiles<P>(a.tile0, a.tok, c.tokens, c.nranks, per);
-  if (!grid) return GC_OK;
-  const dim3 g(grid);
+  const int32_t g = fill_tiles<P>(a.tile0, a.tok, c.tokens, c.nranks, per);
   if (units <= 1 * kWave) return launch(norm_kernel<In, VEC, MX, 1, kWave, P>, a, g, c.stream);
   if (units <= 2 * kWave) return launch(norm_kernel<In, VEC, MX, 2, kWave, P>, a, g, c.stream);
   if (units <= 1 * kThreads) return launch(norm_kernel<In, VEC, MX, 1, kThreads, P>, a, g, c.stream);
@@ -419,11 +427,10 @@ gc_status norm_typed(const gci::NormCall& c) {
 }
 
 template <class In, bool VEC, int P>
-gc_status norm_backward_impl(const gci::NormBackwardCall& c, const NormBackwardArgs<P>& a) {
+gc_status norm_backward_impl(const gci::NormBackwardCall& c, NormBackwardArgs<P>& a) {
   const uint64_t units = c.hidden / RowUnit<In, VEC>::VE;
-  const int32_t blocks = a.tile0[c.nranks];
-  if (blocks) {
-    const dim3 g(blocks);
+  const int32_t g = a.tile0[c.nranks];
+  if (g) {
     gc_status st;
     if (units <= 256) st = launch(norm_backward_kernel<In, VEC, 1, 256, P>, a, g, c.stream, 256);
     else if (units <= 512) st = launch(norm_backward_kernel<In, VEC, 2, 256, P>, a, g, c.stream, 256);
@@ -433,7 +440,7 @@ gc_status norm_backward_impl(const gci::NormBackwardCall& c, const NormBackwardA
     else st = launch(norm_backward_long_kernel<In, VEC, P>, a, g, c.stream);
     if (st != GC_OK) return st;
   }
-  return launch(norm_weight_kernel<P>, a, dim3((c.hidden + kWave - 1) / kWave, c.nranks), c.stream);
+  return launch(norm_weight_kernel<P>, a, (c.hidden + kWave - 1) / kWave, c.stream, kThreads, c.nranks);
 }
 
 template <class In, int P>
