@@ -239,6 +239,7 @@ extern "C" gc_status gc_moe_combine_backward(const void* const* dout, const void
 // ------------------------------------------------------------- experts
 
 namespace {
+uint64_t up64(uint64_t x) { return (x + 63) & ~uint64_t(63); }
 uint64_t up256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 }  // namespace
 
@@ -264,7 +265,7 @@ gci::FfnGeom gci::ffn_geom(const int64_t* rows, int nranks, int E, uint64_t hidd
   g.split = avg < 8 || g.rows < 64;
   g.tile_rows = avg >= 192 ? 256 : avg >= 96 ? 128 : g.split ? 32 : 64;
   g.few = avg < 8 && g.segs <= 1024;
-  const uint64_t part = g.split ? 2 * ((inter + 63) & ~uint64_t(63)) : inter;  // values of h per row
+  const uint64_t part = g.split ? 2 * up64(inter) : inter;  // values of h per row
   for (int d = 0; d < nranks; ++d) g.tiles += rows[d] / g.tile_rows + std::min<int64_t>(E, rows[d]);
   g.map = up256(static_cast<uint64_t>(g.segs) * sizeof(gci::FfnSeg));
   g.x = g.map + up256(static_cast<uint64_t>(g.tiles) * 4);
@@ -308,9 +309,11 @@ gc_status ffn_check(const gci::FfnCall& c, size_t scratch_bytes, bool backward, 
   const gci::FfnGeom g = gci::ffn_geom(c.rows, N, c.experts_per_rank, c.hidden, c.inter, c.x_t, backward);
   if (scratch_bytes < g.bytes) return GC_ERR_INVALID_ARG;
   b.one(c.scratch, 256, g.bytes, true);
-  // blocks of the largest product's grid
-  const uint64_t most = std::max<uint64_t>(static_cast<uint64_t>(g.tiles), static_cast<uint64_t>(g.segs) * ((2 * c.inter + 128) / 256 + 1));
-  if (most * (std::max(c.hidden, 2 * c.inter) / 128 + 1) >= (uint64_t(1) << 31)) return GC_ERR_UNSUPPORTED;
+  // Tiles of each product: 32-bit numbers.  Buffers that could make 2^31 of them are past kMaxExtent in any case.
+  const auto tiles = [](uint64_t m, uint64_t n, uint64_t by) { return m * ((n + by - 1) / by); };
+  uint64_t most = std::max(tiles(g.tiles, c.inter, 128), tiles(g.tiles, c.hidden, 256));
+  if (backward) most = std::max(most, tiles(tiles(g.segs, 2 * up64(c.inter), 256), c.hidden, 256));
+  if (most >= (uint64_t(1) << 31)) return GC_ERR_UNSUPPORTED;
   return b.check();
 }
 

@@ -94,6 +94,9 @@ int main() {
           gc_moe_combine_backward(in<void>(), in<void>(), &rows, in<int32_t>(), in<float>(), &tokens, 1, 1, 257, GC_BF16, list(),
                                   reinterpret_cast<float* const*>(list()), nullptr), (1 << 25) + 2);
   }
+  experts("experts, 5 rows, 1024 of 8 x 2^20", 5, 1024, 8, size_t(1) << 20, GC_BF16, false, 1024 * 8192);
+  experts("experts' backward, 1024 of 8 x 2^20", 5, 1024, 8, size_t(1) << 20, GC_BF16, true, 1000);
+  experts("experts' backward, 8192 of 8 x 2^16", 9000, 8192, 8, size_t(1) << 16, GC_BF16, true, 1000);
   experts("experts, 5 rows, 1024 of 2^20 x 8", 5, 1024, size_t(1) << 20, 8, GC_BF16, false, 1024 * 8192);
   experts("experts, 2^26 + 5 8-bit rows of 8", (int64_t(1) << 26) + 5, 1, 8, 8, GC_MX8, false, (1 << 24) + 2);
   experts("experts' backward, 2^26 + 5 8-bit rows", (int64_t(1) << 26) + 5, 1, 8, 8, GC_MX8, true, (1 << 24) + 2);
