@@ -244,13 +244,23 @@ uint64_t up256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 }  // namespace
 
 // Row tiles follow the mean block: a tile's rows past its block are computed
-// and dropped, so few rows per expert take lower tiles.  Below eight rows per
-// expert a serving forward streams the weights instead: 16 rows over 8 experts
-// of 4096 x 11008 take 336 us so and 483 in tiles, 64 over 16 of 2048 x 1024
-// 49 and 76; at 16 rows per expert the tiles win everywhere (309 us against
-// 568 for 64 experts of 4096 x 1024).  Each of its workgroups adds up its rank's
-// table up to its expert, which past 1024 experts would take as long.
-//
+// and dropped, so few rows per expert take lower tiles.  A serving forward of a
+// handful of rows streams the weights instead.  It reads an expert's weights once
+// per 16 rows of that expert (down: 8), and the host does not know which expert gets
+// them, so the rule bounds the rows of all of them: us streamed / in tiles, for rows
+// spread evenly, as 1 / k over the experts, all on one:
+//     16 experts of 2048 x 1024, 16 rows     48 / 58    45 / 47    47 / 43
+//                                32          52 / 74    51 / 65    90 / 44
+//                                64          61 / 75    77 / 68   175 / 44
+//      8 experts of 4096 x 11008, 16        376 / 502  372 / 487  123 / 295
+//                                32         489 / 554  486 / 525  225 / 312
+//     64 experts of 4096 x 1024, 32         156 / 164  116 / 138   99 / 64
+//                                64         225 / 235  170 / 175  189 / 66
+//                               256         338 / 317  395 / 266  721 / 83
+// Each of its workgroups also adds up its rank's table up to its expert, and every
+// expert has workgroups: 256 of 2048 x 1024 with 8 rows take 77 / 56, 74 / 45, 59 / 44.
+constexpr int kFewRows = 32, kFewSegs = 64;
+
 // With few rows per expert, or few in all, h and the gradients of gate and up are
 // kept in two parts: a single bf16 rounding of them adds about as much to the
 // results' 2-norm error as the results' own rounding (sqrt 2 together), and with few
@@ -264,7 +274,7 @@ gci::FfnGeom gci::ffn_geom(const int64_t* rows, int nranks, int E, uint64_t hidd
   const int64_t avg = g.rows / g.segs;
   g.split = avg < 8 || g.rows < 64;
   g.tile_rows = avg >= 192 ? 256 : avg >= 96 ? 128 : g.split ? 32 : 64;
-  g.few = avg < 8 && g.segs <= 1024;
+  g.few = avg < 8 && g.rows <= kFewRows && g.segs <= kFewSegs;
   const uint64_t part = g.split ? 2 * up64(inter) : inter;  // values of h per row
   for (int d = 0; d < nranks; ++d) g.tiles += rows[d] / g.tile_rows + std::min<int64_t>(E, rows[d]);
   g.map = up256(static_cast<uint64_t>(g.segs) * sizeof(gci::FfnSeg));

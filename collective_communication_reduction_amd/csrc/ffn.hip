@@ -907,9 +907,8 @@ struct FewArgs {
   const int64_t* splits;
   char* h;
   uint64_t K, n;           // summed values, output columns
-  uint32_t N, E, tiles;    // column tiles per expert
+  uint32_t N, E, tiles;    // column tiles per expert: at most 2^16 of at most kFewSegs experts, 2^31 work items
   uint32_t shares;         // of the summed index: 1, 2, 4 or 8
-  uint32_t block0;         // first workgroup of this launch
 };
 
 __device__ __forceinline__ int64_t wave_sum64(int64_t x) {
@@ -925,8 +924,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P
   __shared__ f32x4 part[kFewWaves][GATE_UP ? 2 : 1][kWave];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const uint32_t share = w % a.shares, group = w / a.shares, groups = kFewWaves / a.shares;
-  const uint32_t block = a.block0 + blockIdx.x;
-  const uint32_t seg = block / a.tiles;
+  const uint32_t seg = blockIdx.x / a.tiles;
   const uint32_t d = seg / a.E, e = seg - d * a.E;
   int64_t before = 0, count = 0;
   for (uint32_t i = lane; i < (e + 1) * a.N; i += kWave) {
@@ -940,7 +938,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) ffn_few_kernel(const FewArgs<P
   count = wave_sum64(count);
   const int64_t start = min(before, a.rows[d]);
   const int64_t rows = min(before + count, a.rows[d]) - start;
-  const uint64_t n0 = static_cast<uint64_t>((block - seg * a.tiles) * groups + group) * 16;
+  const uint64_t n0 = static_cast<uint64_t>((blockIdx.x - seg * a.tiles) * groups + group) * 16;
   const uint64_t col = min(n0 + (lane & 15), a.n - 1);  // past the last: the last again, not stored
   const uint64_t w0 = (static_cast<uint64_t>(e) * a.n + col) * a.K * 2;
   const char* const wa = a.wa[d] + w0;
@@ -1126,14 +1124,6 @@ void split_few(A& a, int unroll) {
   a.tiles = static_cast<uint32_t>(ceil_div(a.n, 16 * (kFewWaves / a.shares)));
 }
 
-template <class Kern, class A>
-gc_status launch_few(Kern kernel, A& a, uint64_t segs, hipStream_t stream) {
-  return gci::in_launches(segs * a.tiles, 64 * kFewWaves, [&](uint32_t first, uint32_t n) {
-    a.block0 = first;
-    return launch(kernel, a, n, 64 * kFewWaves, stream);
-  });
-}
-
 template <int P>
 gc_status forward_few(const gci::FfnCall& c, const gci::FfnGeom& g) {
   FewArgs<P> a{};
@@ -1155,13 +1145,13 @@ gc_status forward_few(const gci::FfnCall& c, const gci::FfnGeom& g) {
   a.N = c.nranks;
   a.E = c.experts_per_rank;
   split_few(a, kFewLoads / 2);
-  const gc_status st = launch_few(ffn_few_kernel<true, P>, a, g.segs, c.stream);
+  const gc_status st = launch(ffn_few_kernel<true, P>, a, static_cast<uint64_t>(g.segs) * a.tiles, 64 * kFewWaves, c.stream);
   if (st != GC_OK) return st;
   for (int d = 0; d < c.nranks; ++d) a.wa[d] = static_cast<const char*>(c.w_down[d]);
   a.K = c.inter;
   a.n = c.hidden;
   split_few(a, kFewLoads);
-  return launch_few(ffn_few_kernel<false, P>, a, g.segs, c.stream);
+  return launch(ffn_few_kernel<false, P>, a, static_cast<uint64_t>(g.segs) * a.tiles, 64 * kFewWaves, c.stream);
 }
 
 }  // namespace

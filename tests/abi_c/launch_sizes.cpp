@@ -53,6 +53,18 @@ void pack(const char* what, int64_t rows, size_t n, gc_dtype t, uint64_t least) 
   check(what, gc_mx8_unpack(in<void>(), &rows, 1, n, t, list(), nullptr), least);
 }
 
+// Launches of a forward without checkpoint: 2 streamed (each reads an expert's weights again
+// for every 16 or 8 of its rows), 3 in tiles.
+void forward_launches(int64_t rows, int E, size_t hidden, size_t inter, size_t want) {
+  const size_t need = gc_moe_ffn_scratch_bytes(&rows, 1, E, hidden, inter, GC_BF16, 0);
+  gc_moe_ffn(in<void>(), GC_BF16, &rows, static_cast<int64_t*>(buf()), 1, E, hidden, inter, in<void>(), in<void>(), in<void>(), nullptr,
+             GC_BF16, list(), buf(), need, nullptr);
+  const size_t got = g_launches.size();
+  g_failures += got != want;
+  std::printf("experts' forward, %lld rows over %d: %zu launches: %s\n", static_cast<long long>(rows), E, got, got == want ? "ok" : "FAILED");
+  g_launches.clear();
+}
+
 void experts(const char* what, int64_t rows, int E, size_t hidden, size_t inter, gc_dtype xt, bool backward, uint64_t least) {
   const size_t need = gc_moe_ffn_scratch_bytes(&rows, 1, E, hidden, inter, xt, backward);
   const int64_t* splits = static_cast<int64_t*>(buf());
@@ -94,12 +106,20 @@ int main() {
           gc_moe_combine_backward(in<void>(), in<void>(), &rows, in<int32_t>(), in<float>(), &tokens, 1, 1, 257, GC_BF16, list(),
                                   reinterpret_cast<float* const*>(list()), nullptr), (1 << 25) + 2);
   }
-  experts("experts, 5 rows, 1024 of 8 x 2^20", 5, 1024, 8, size_t(1) << 20, GC_BF16, false, 1024 * 8192);
+  experts("experts, 5 rows, 1024 of 8 x 2^20", 5, 1024, 8, size_t(1) << 20, GC_BF16, false, 500);
   experts("experts' backward, 1024 of 8 x 2^20", 5, 1024, 8, size_t(1) << 20, GC_BF16, true, 1000);
   experts("experts' backward, 8192 of 8 x 2^16", 9000, 8192, 8, size_t(1) << 16, GC_BF16, true, 1000);
-  experts("experts, 5 rows, 1024 of 2^20 x 8", 5, 1024, size_t(1) << 20, 8, GC_BF16, false, 1024 * 8192);
+  experts("experts, 5 rows, 1024 of 2^20 x 8", 5, 1024, size_t(1) << 20, 8, GC_BF16, false, 200);
+  experts("experts, streamed, 64 of 8 x 2^20", 5, 64, 8, size_t(1) << 20, GC_BF16, false, 64 * 8192);
   experts("experts, 2^26 + 5 8-bit rows of 8", (int64_t(1) << 26) + 5, 1, 8, 8, GC_MX8, false, (1 << 24) + 2);
   experts("experts' backward, 2^26 + 5 8-bit rows", (int64_t(1) << 26) + 5, 1, 8, 8, GC_MX8, true, (1 << 24) + 2);
+  // one expert may get every row, so the streamed form is for few rows in all
+  forward_launches(8000, 1024, 2048, 1024, 3);
+  forward_launches(500, 64, 2048, 1024, 3);
+  forward_launches(33, 64, 2048, 1024, 3);
+  forward_launches(8, 256, 2048, 1024, 3);
+  forward_launches(32, 64, 2048, 1024, 2);
+  forward_launches(1, 8, 4096, 11008, 2);
   std::printf("%d failures\n", g_failures);
   return g_failures != 0;
 }
