@@ -178,16 +178,21 @@ def _bufs(xs, n, nbytes, what):
     if isinstance(xs, ctypes.Array):
         return xs
     arr = _ptr_array(m)()
-    same = nbytes if isinstance(nbytes, int) else None
-    for i, x in enumerate(xs):
-        need = 0 if i >= n else same if same is not None else nbytes[i]
+    need = [nbytes] * n if isinstance(nbytes, int) else nbytes
+    if m > n:
+        need = [*need[:n], *[0] * (m - n)]
+    try:
         # the checks of _buf in line: this loop is most of a short call's time on the host
-        if x is None or type(x) is int:
-            arr[i] = x
-        elif x.is_cuda and x.is_contiguous() and x.numel() * x.element_size() >= need:
-            arr[i] = x.data_ptr()
-        else:
-            arr[i] = _buf(x, need, f"{what}[{i}]")
+        for i, x in enumerate(xs):
+            if x is None or type(x) is int:
+                arr[i] = x
+            elif x.is_cuda and x.is_contiguous() and x.nbytes >= need[i]:
+                arr[i] = x.data_ptr()
+            else:
+                arr[i] = _buf(x, need[i], f"{what}[{i}]")
+    except AttributeError:      # addresses of another integer type, tensors of another library
+        for i, x in enumerate(xs):
+            arr[i] = _buf(x, need[i], f"{what}[{i}]")
     return arr
 
 
