@@ -5,8 +5,10 @@ arguments: it turns lists of tensors (or raw device addresses) into pointer
 arrays, maps dtype/op/order names onto the C enums, passes torch's current HIP
 stream, and raises GcError for a non-OK status.  Since the library sees only
 addresses, a tensor is checked here first (a contiguous device tensor that
-holds every byte the call touches, else ValueError); raw addresses and
-gc_pointers arrays are the caller's responsibility.  Every collective runs in the
+holds every byte the call touches, else ValueError; the norm, the 8-bit rows,
+the experts and the combine's gradient also check its type, where integer
+tensors count as raw bits); raw addresses and gc_pointers arrays are the
+caller's responsibility.  Every collective runs in the
 HIP kernels of libgc.so; there is no other implementation to fall back to, and
 importing this package fails if the library has not been built
 (python collective_communication_reduction_amd/build.py).
@@ -145,7 +147,22 @@ def _check(status, what):
 _ES = {GC_INT32: 4, GC_FP32: 4, GC_BF16: 2}
 
 
-def _buf(x, nbytes, what):
+# Tensors that hold values of a type (a code, or int64): its own, or integers as raw bits.  A stand-in
+# without a dtype (None) passes.
+_HOLDS = {}
+
+
+def _holds(t):
+    if not _HOLDS and torch is not None:
+        raw = (torch.uint8, torch.int8, None)
+        _HOLDS.update({GC_BF16: frozenset((torch.bfloat16, torch.int16, torch.uint16) + raw),
+                       GC_FP32: frozenset((torch.float32, torch.int32, torch.uint32) + raw),
+                       GC_INT32: frozenset((torch.int32, torch.uint32) + raw), GC_MX8: frozenset(raw),
+                       "int64": frozenset((torch.int64, torch.uint64) + raw)})
+    return _HOLDS.get(t)
+
+
+def _buf(x, nbytes, what, holds=None):
     """Address of one device buffer that a call reads or writes for nbytes bytes.
 
     A tensor must be a contiguous device tensor of at least nbytes bytes: the C
@@ -161,15 +178,19 @@ def _buf(x, nbytes, what):
     have = x.numel() * x.element_size()
     if have < nbytes:
         raise ValueError(f"{what}: {have} bytes, the call touches {nbytes}")
+    if holds is not None and nbytes and getattr(x, "dtype", None) not in holds:
+        names = ", ".join(sorted(str(t).replace("torch.", "") for t in holds if t is not None))
+        raise ValueError(f"{what}: a tensor of {x.dtype}, where the call takes one of {names}")
     return x.data_ptr()
 
 
-def _bufs(xs, n, nbytes, what):
+def _bufs(xs, n, nbytes, what, t=None):
     """Pointer array of the first n buffers of xs, each checked by _buf.
 
     nbytes is one size for every buffer or a sequence with one size per buffer.
     A pointer array made by gc_pointers passes unchecked but must hold n
-    entries; None passes as NULL (the library rejects it)."""
+    entries; None passes as NULL (the library rejects it).  t: the type of the
+    values, where the tensors' types are checked too."""
     if xs is None:
         return None
     m = len(xs)
@@ -179,6 +200,7 @@ def _bufs(xs, n, nbytes, what):
         return xs
     arr = _ptr_array(m)()
     need = [nbytes] * n if isinstance(nbytes, int) else nbytes
+    holds = None if t is None else _holds(t)
     if m > n:
         need = [*need[:n], *[0] * (m - n)]
     try:
@@ -186,13 +208,13 @@ def _bufs(xs, n, nbytes, what):
         for i, x in enumerate(xs):
             if x is None or type(x) is int:
                 arr[i] = x
-            elif x.is_cuda and x.is_contiguous() and x.nbytes >= need[i]:
+            elif x.is_cuda and x.is_contiguous() and x.nbytes >= need[i] and (holds is None or x.dtype in holds):
                 arr[i] = x.data_ptr()
             else:
-                arr[i] = _buf(x, need[i], f"{what}[{i}]")
+                arr[i] = _buf(x, need[i], f"{what}[{i}]", holds)
     except AttributeError:      # addresses of another integer type, tensors of another library
         for i, x in enumerate(xs):
-            arr[i] = _buf(x, need[i], f"{what}[{i}]")
+            arr[i] = _buf(x, need[i], f"{what}[{i}]", holds)
     return arr
 
 
@@ -500,12 +522,12 @@ def gc_moe_combine_backward(dout, expert_out, expert_rows, dest, weights, ntoken
     n, t = len(ntokens), _dtype_code(dtype)
     rb = max(0, int(hidden)) * _ES.get(t, 0)
     rows = [max(0, int(r)) * rb for r in expert_rows]
-    _check(_c_moe_combine_bwd(_bufs(dout, n, [max(0, int(x)) * rb for x in ntokens], "dout"),
-                              _bufs(expert_out, n, rows, "expert_out"), _i64_array(expert_rows),
-                              _bufs(dest, n, _per_route(ntokens, topk, 8), "dest"),
-                              _bufs(weights, n, _per_route(ntokens, topk, 4), "weights"), _i64_array(ntokens), n,
-                              int(topk), int(hidden), t, _bufs(dexpert, n, rows, "dexpert"),
-                              _bufs(dweights, n, _per_route(ntokens, topk, 4), "dweights"),
+    _check(_c_moe_combine_bwd(_bufs(dout, n, [max(0, int(x)) * rb for x in ntokens], "dout", t),
+                              _bufs(expert_out, n, rows, "expert_out", t), _i64_array(expert_rows),
+                              _bufs(dest, n, _per_route(ntokens, topk, 8), "dest", GC_INT32),
+                              _bufs(weights, n, _per_route(ntokens, topk, 4), "weights", GC_FP32), _i64_array(ntokens), n,
+                              int(topk), int(hidden), t, _bufs(dexpert, n, rows, "dexpert", t),
+                              _bufs(dweights, n, _per_route(ntokens, topk, 4), "dweights", GC_FP32),
                               _stream(stream, _first(dexpert))), "gc_moe_combine_backward")
     return dexpert, dweights
 
@@ -528,8 +550,8 @@ def _rows_of(counts, row):
 def gc_mx8_pack(x, rows, n, packed, dtype=None, stream=None):
     """x[r]: rows[r] rows of n bf16 or fp32 values -> packed[r]: as many 8-bit rows (uint8)."""
     N, t = len(rows), _infer_dtype(x, dtype)
-    _check(_c_mx8_pack(_bufs(x, N, _rows_of(rows, _row_bytes(n, t)), "x"), _i64_array(rows), N, int(n), t,
-                       _bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed"),
+    _check(_c_mx8_pack(_bufs(x, N, _rows_of(rows, _row_bytes(n, t)), "x", t), _i64_array(rows), N, int(n), t,
+                       _bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed", GC_MX8),
                        _stream(stream, _first(packed))), "gc_mx8_pack")
     return packed
 
@@ -537,8 +559,8 @@ def gc_mx8_pack(x, rows, n, packed, dtype=None, stream=None):
 def gc_mx8_unpack(packed, rows, n, out, dtype=None, stream=None):
     """Inverse of gc_mx8_pack: the values that 8-bit rows stand for, exact in bf16 and fp32."""
     N, t = len(rows), _infer_dtype(out, dtype)
-    _check(_c_mx8_unpack(_bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed"), _i64_array(rows), N,
-                         int(n), t, _bufs(out, N, _rows_of(rows, _row_bytes(n, t)), "out"),
+    _check(_c_mx8_unpack(_bufs(packed, N, _rows_of(rows, _row_bytes(n, GC_MX8)), "packed", GC_MX8), _i64_array(rows), N,
+                         int(n), t, _bufs(out, N, _rows_of(rows, _row_bytes(n, t)), "out", t),
                          _stream(stream, _first(out))), "gc_mx8_unpack")
     return out
 
@@ -551,10 +573,10 @@ def gc_rms_norm(x, weight, ntokens, hidden, y, residual=None, sum_out=None, rstd
     yt = _infer_dtype(y, y_dtype)
     full = _rows_of(ntokens, _row_bytes(hidden, t))
     one = [_row_bytes(hidden, t) if int(c) > 0 else 0 for c in ntokens]
-    _check(_c_norm(_bufs(x, N, full, "x"), _bufs(residual, N, full, "residual"), _bufs(weight, N, one, "weight"),
-                   _i64_array(ntokens), N, int(hidden), float(eps), t, _bufs(sum_out, N, full, "sum_out"),
-                   _bufs(y, N, _rows_of(ntokens, _row_bytes(hidden, yt)), "y"), yt,
-                   _bufs(rstd, N, _rows_of(ntokens, 4), "rstd"), _stream(stream, _first(y))), "gc_rms_norm")
+    _check(_c_norm(_bufs(x, N, full, "x", t), _bufs(residual, N, full, "residual", t), _bufs(weight, N, one, "weight", t),
+                   _i64_array(ntokens), N, int(hidden), float(eps), t, _bufs(sum_out, N, full, "sum_out", t),
+                   _bufs(y, N, _rows_of(ntokens, _row_bytes(hidden, yt)), "y", yt), yt,
+                   _bufs(rstd, N, _rows_of(ntokens, 4), "rstd", GC_FP32), _stream(stream, _first(y))), "gc_rms_norm")
     return y
 
 
@@ -572,10 +594,10 @@ def gc_rms_norm_backward(dy, sum, weight, rstd, ntokens, hidden, dx, dweight, sc
         scratch_bytes = scratch.numel() * scratch.element_size()
     full = _rows_of(ntokens, _row_bytes(hidden, t))
     one = [_row_bytes(hidden, t) if int(c) > 0 else 0 for c in ntokens]
-    _check(_c_norm_bwd(_bufs(dy, N, full, "dy"), _bufs(dsum, N, full, "dsum"), _bufs(sum, N, full, "sum"),
-                       _bufs(weight, N, one, "weight"), _bufs(rstd, N, _rows_of(ntokens, 4), "rstd"),
-                       _i64_array(ntokens), N, int(hidden), t, _bufs(dx, N, full, "dx"),
-                       _bufs(dweight, N, max(0, int(hidden)) * 4, "dweight"),
+    _check(_c_norm_bwd(_bufs(dy, N, full, "dy", t), _bufs(dsum, N, full, "dsum", t), _bufs(sum, N, full, "sum", t),
+                       _bufs(weight, N, one, "weight", t), _bufs(rstd, N, _rows_of(ntokens, 4), "rstd", GC_FP32),
+                       _i64_array(ntokens), N, int(hidden), t, _bufs(dx, N, full, "dx", t),
+                       _bufs(dweight, N, max(0, int(hidden)) * 4, "dweight", GC_FP32),
                        _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes), _stream(stream, _first(dx))),
            "gc_rms_norm_backward")
     return dx, dweight
@@ -594,8 +616,8 @@ def _ffn_common(rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_d
     w = E * max(0, int(hidden)) * max(0, int(inter))
     if scratch_bytes is None:
         scratch_bytes = scratch.numel() * scratch.element_size()
-    return (N, w, _buf(splits, N * N * E * 8, "splits"),
-            [_bufs(p, N, 2 * w, k) for p, k in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))],
+    return (N, w, _buf(splits, N * N * E * 8, "splits", _holds("int64")),
+            [_bufs(p, N, 2 * w, k, GC_BF16) for p, k in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))],
             _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes))
 
 
@@ -609,10 +631,10 @@ def gc_moe_ffn(x, rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w
                                          scratch_bytes)
     xt = _infer_dtype(x, x_dtype)
     st = GC_BF16 if saved is None else _infer_dtype(saved, saved_dtype)
-    _check(_c_ffn(_bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x"), xt, _i64_array(rows), sp, N,
+    _check(_c_ffn(_bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x", xt), xt, _i64_array(rows), sp, N,
                   int(experts_per_rank), int(hidden), int(inter), *ws,
-                  _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved"), st,
-                  _bufs(y, N, _rows_of(rows, 2 * max(0, int(hidden))), "y"), sc, scb, _stream(stream, _first(y))),
+                  _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved", st), st,
+                  _bufs(y, N, _rows_of(rows, 2 * max(0, int(hidden))), "y", GC_BF16), sc, scb, _stream(stream, _first(y))),
            "gc_moe_ffn")
     return y
 
@@ -625,10 +647,10 @@ def gc_moe_ffn_backward(dy, x, saved, rows, splits, experts_per_rank, hidden, in
                                         scratch_bytes)
     xt, st, wt = _infer_dtype(x, x_dtype), _infer_dtype(saved, saved_dtype), _infer_dtype(dw_gate, dw_dtype)
     row = _rows_of(rows, 2 * max(0, int(hidden)))
-    dws = [_bufs(p, N, w * _ES.get(wt, 0), k) for p, k in ((dw_gate, "dw_gate"), (dw_up, "dw_up"), (dw_down, "dw_down"))]
-    _check(_c_ffn_bwd(_bufs(dy, N, row, "dy"), _bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x"), xt,
-                      _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved"), st, _i64_array(rows), sp,
-                      N, int(experts_per_rank), int(hidden), int(inter), *ws, _bufs(dx, N, row, "dx"), *dws, wt, sc, scb,
+    dws = [_bufs(p, N, w * _ES.get(wt, 0), k, wt) for p, k in ((dw_gate, "dw_gate"), (dw_up, "dw_up"), (dw_down, "dw_down"))]
+    _check(_c_ffn_bwd(_bufs(dy, N, row, "dy", GC_BF16), _bufs(x, N, _rows_of(rows, _row_bytes(hidden, xt)), "x", xt), xt,
+                      _bufs(saved, N, _rows_of(rows, _row_bytes(2 * int(inter), st)), "saved", st), st, _i64_array(rows), sp,
+                      N, int(experts_per_rank), int(hidden), int(inter), *ws, _bufs(dx, N, row, "dx", GC_BF16), *dws, wt, sc, scb,
                       _stream(stream, _first(dx))), "gc_moe_ffn_backward")
     return dx, dw_gate, dw_up, dw_down
 
