@@ -466,7 +466,7 @@ __device__ __forceinline__ float with_rest(float v, float rest) { return fabsf(v
 // operand is to the rests (the values themselves have brought them into the sum).
 // on: 0x00800080, which carries an exponent of ones into the sign bit; 0 keeps all.
 // Packed 16-bit instructions, 64 or 32 a wavefront and 16 summed values: 3 % of a backward
-// of 64 rows over 16 experts of 2048 x 1024 (163 us against 158 without).
+// of 64 rows over 16 experts of 2048 x 1024 (163 us against 158 without; three routings).
 __device__ __forceinline__ bf16x8 finite_of(bf16x8 v, uint32_t on) {
   typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
   u32x4 w = __builtin_bit_cast(u32x4, v);
@@ -513,12 +513,13 @@ enum SavedKind { kNoSaved, kSaved16, kSaved8 };
 // tiles that the registers hold: each value read from LDS feeds as many matrix
 // instructions as possible, and each loaded one 256 or TM results.
 //
-// 32768 rows over 16 experts of 4096 x 2048: gate and up 1110 us (0.99 PFLOP/s),
-// down 555 (0.99), dh 817, dx 990 (1.11), weight gradients 510 and 935 (1.15).
-// Without its loads each takes about 80 % of that (908 us, 453, 646, 780, 405, 745):
-// a step's loads have one step to arrive, and a third LDS stage does not fit.
-// 8111 rows over 64 experts of 2048 x 1024: dh 148 us, dx 182, weight gradients
-// 141 and 246, of which storing them alone takes 66 and 129.
+// 32768 rows over 16 experts of 4096 x 2048: gate and up 1012 us without a checkpoint
+// (1.09 PFLOP/s), 1080 with one in bf16, 1070 in 8 bits; down 531 (1.04); dh 799 from
+// bf16, 823 from 8 bits; dx 994 (1.11); weight gradients 503 and 971 (1.13).  Without
+// its loads each takes about 80 % of that (gate and up 908 us, 453, 646, 780, 405, 745):
+// a step's loads have one step to arrive, and a third LDS stage of 64 values does not fit.
+// 8111 rows over 64 experts of 2048 x 1024: dh 141 us, dx 178, weight gradients
+// 133 and 228, of which storing them alone takes 66 and 129.
 // SAVED: the checkpoint's type (kGateUp, kDh).  F32OUT: fp32 weight gradients.
 // SPLIT: rows of h are [h | rest], of g [dgate | dup | rests of both], each part
 // padded to a multiple of 64 values with zeros, and row tiles half as high.
@@ -804,68 +805,68 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
           const uint64_t n = n0 + (wn * NB + j) * 32;
           if (n >= FP) continue;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {  // half a block at a time, to hold few registers
-          const uint64_t c = n + 8 * (2 * p + (lane >> 5));
-          float gate[8], up[8], sig[8], r[8];
-          if constexpr (SAVED == kSaved16) {
-            const uint64_t in_c = std::min<uint64_t>(c, F - 8);
-            unpack_half(*reinterpret_cast<const u32x4*>(in + in_c * 2), gate);
-            unpack_half(*reinterpret_cast<const u32x4*>(in + (F + in_c) * 2), up);
-          } else {
-            const uint64_t in_n = std::min<uint64_t>(n, F - 32);
-            load_half8(in, 2 * F, in_n, p, lane, gate);
-            load_half8(in, 2 * F, F + in_n, p, lane, up);
-          }
-          const bool ok = row && c < FP;
-          char* const out_h = a.h + (sg.row + m) * FH * 2 + c * 2;
-          char* const out_g = a.g + (sg.row + m) * FG * 2 + c * 2;
-          auto put = [&](char* out, uint64_t rest) {  // r, zeros in a part's padding
-            const u32x4 o = pack_half(r);
-            if (ok) *reinterpret_cast<u32x4*>(out) = SPLIT && c >= F ? u32x4{} : o;
-            if constexpr (SPLIT) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) r[e] = rounded_off(r[e]);
-              const u32x4 q = pack_half(r);
-              if (ok) *reinterpret_cast<u32x4*>(out + rest * 2) = c >= F ? u32x4{} : q;
+          for (int p = 0; p < 2; ++p) {  // half a block at a time, to hold few registers
+            const uint64_t c = n + 8 * (2 * p + (lane >> 5));
+            float gate[8], up[8], sig[8], r[8];
+            if constexpr (SAVED == kSaved16) {
+              const uint64_t in_c = std::min<uint64_t>(c, F - 8);
+              unpack_half(*reinterpret_cast<const u32x4*>(in + in_c * 2), gate);
+              unpack_half(*reinterpret_cast<const u32x4*>(in + (F + in_c) * 2), up);
+            } else {
+              const uint64_t in_n = std::min<uint64_t>(n, F - 32);
+              load_half8(in, 2 * F, in_n, p, lane, gate);
+              load_half8(in, 2 * F, F + in_n, p, lane, up);
             }
-          };
+            const bool ok = row && c < FP;
+            char* const out_h = a.h + (sg.row + m) * FH * 2 + c * 2;
+            char* const out_g = a.g + (sg.row + m) * FG * 2 + c * 2;
+            auto put = [&](char* out, uint64_t rest) {  // r, zeros in a part's padding
+              const u32x4 o = pack_half(r);
+              if (ok) *reinterpret_cast<u32x4*>(out) = SPLIT && c >= F ? u32x4{} : o;
+              if constexpr (SPLIT) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sig[e] = sigmoid(gate[e]);
-            r[e] = gate[e] * sig[e] * up[e];
+                for (int e = 0; e < 8; ++e) r[e] = rounded_off(r[e]);
+                const u32x4 q = pack_half(r);
+                if (ok) *reinterpret_cast<u32x4*>(out + rest * 2) = c >= F ? u32x4{} : q;
+              }
+            };
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              sig[e] = sigmoid(gate[e]);
+              r[e] = gate[e] * sig[e] * up[e];
+            }
+            put(out_h, FP);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              r[e] = acc[i][j][8 * p + e] * up[e] * (sig[e] * (1.0f + gate[e] * (1.0f - sig[e])));
+            put(out_g, 2 * FP);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = acc[i][j][8 * p + e] * (gate[e] * sig[e]);
+            put(out_g + FP * 2, 2 * FP);
           }
-          put(out_h, FP);
+        }
+      } else {
+        // Rows mb .. + 3 of two blocks side by side.  H and F are multiples of 8, so
+        // of a weight gradient all four exist or none, and in one of its matrices.
+        const int64_t mb = m0 + (wm * MB + i) * 32 + (lane & 28);
+        const uint64_t M = KIND == kDwDown ? H : KIND == kDwGateUp ? FP + F : RESTS && wm == 1 ? 0 : sg.rows, N = KIND == kDwDown ? F : H;
+        constexpr int ES = F32OUT ? 4 : 2;
+        char* out;
+        if constexpr (KIND == kDwDown) out = sg.dw_down + mb * N * ES;
+        else if constexpr (KIND == kDwGateUp) out = static_cast<uint64_t>(mb) < FP ? sg.dw_gate + mb * N * ES : sg.dw_up + (mb - static_cast<int64_t>(FP)) * N * ES;
+        else out = sg.y + mb * N * ES;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            r[e] = acc[i][j][8 * p + e] * up[e] * (sig[e] * (1.0f + gate[e] * (1.0f - sig[e])));
-          put(out_g, 2 * FP);
+        for (int p = 0; p < (F32OUT ? 2 : 1); ++p) {
+          __builtin_amdgcn_sched_barrier(0);
+          const uint64_t n = n0 + (wn * NB + (lane >> 5)) * 32 + (F32OUT ? 16 * p + 4 * (lane & 3) : 8 * (lane & 3));
+          u32x4 v[4];
+          if constexpr (F32OUT) trade_two(acc[i][0], acc[i][1], p, lane, v);
+          else pack_two(acc[i][0], acc[i][1], lane, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[e] = acc[i][j][8 * p + e] * (gate[e] * sig[e]);
-          put(out_g + FP * 2, 2 * FP);
+          for (int k = 0; k < 4; ++k)
+            if (static_cast<uint64_t>(mb + (WGRAD ? 0 : k)) < M && n < N && !(SPLIT && KIND == kDwGateUp && static_cast<uint64_t>(mb) >= F && static_cast<uint64_t>(mb) < FP)) *reinterpret_cast<u32x4*>(out + (k * N + n) * ES) = v[k];
         }
       }
-    } else {
-      // Rows mb .. + 3 of two blocks side by side.  H and F are multiples of 8, so
-      // of a weight gradient all four exist or none, and in one of its matrices.
-      const int64_t mb = m0 + (wm * MB + i) * 32 + (lane & 28);
-      const uint64_t M = KIND == kDwDown ? H : KIND == kDwGateUp ? FP + F : RESTS && wm == 1 ? 0 : sg.rows, N = KIND == kDwDown ? F : H;
-      constexpr int ES = F32OUT ? 4 : 2;
-      char* out;
-      if constexpr (KIND == kDwDown) out = sg.dw_down + mb * N * ES;
-      else if constexpr (KIND == kDwGateUp) out = static_cast<uint64_t>(mb) < FP ? sg.dw_gate + mb * N * ES : sg.dw_up + (mb - static_cast<int64_t>(FP)) * N * ES;
-      else out = sg.y + mb * N * ES;
-#pragma unroll
-      for (int p = 0; p < (F32OUT ? 2 : 1); ++p) {
-        __builtin_amdgcn_sched_barrier(0);
-        const uint64_t n = n0 + (wn * NB + (lane >> 5)) * 32 + (F32OUT ? 16 * p + 4 * (lane & 3) : 8 * (lane & 3));
-        u32x4 v[4];
-        if constexpr (F32OUT) trade_two(acc[i][0], acc[i][1], p, lane, v);
-        else pack_two(acc[i][0], acc[i][1], lane, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (static_cast<uint64_t>(mb + (WGRAD ? 0 : k)) < M && n < N && !(SPLIT && KIND == kDwGateUp && static_cast<uint64_t>(mb) >= F && static_cast<uint64_t>(mb) < FP)) *reinterpret_cast<u32x4*>(out + (k * N + n) * ES) = v[k];
-      }
-    }
     }
     // Every way to the next tile waits here, the last one's too.  Waiting only
     // after an odd number of steps would be enough, but the compiler then sees a
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
 // eight columns of the matrix instructions.  The expert's rows are found
 // from the split table by the workgroup itself, so the whole forward is two
 // launches.  HBM bytes bound it: two experts of 4096 x 11008 with a row each, gate
-// and up 82 us (4.4 TB/s), down 58 us (3.1 TB/s).
+// and up 84 us (4.3 TB/s), down 44 us (4.1 TB/s).
 
 constexpr int kFewWaves = 8;
 constexpr int kFewLoads = 8;  // weight vectors in flight per lane

@@ -10,8 +10,8 @@
 // (4096 bf16, 512 units: 630 us with a workgroup's 2 units per lane, 641 with a
 // wavefront's 8, for 8 x 16384 rows), and rows past a workgroup's registers are
 // read a second time (from the caches, mostly).  Those 8 x 16384 rows: forward to
-// 8-bit rows 630 us, 6.0 TB/s; backward 790 us, 5.3 TB/s (three streams read, one
-// written).
+// 8-bit rows 623 us, 6.1 TB/s; backward 799 us, 5.4 TB/s (three streams read, one
+// written), and 5 us for the weight gradient's partial sums.
 
 #include <algorithm>
 #include <type_traits>
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(LANES) norm_backward_kernel(const NormBackward
   const T* const ds = reinterpret_cast<const T*>(a.dsum[rank]);
   const T* const sm = reinterpret_cast<const T*>(a.sum[rank]);
   // With few units per lane the next row's loads are in flight while this one's
-  // sum goes round the workgroup (8 x 16384 x 4096 bf16: 792 against 817 us).
+  // sum goes round the workgroup (8 x 16384 x 4096 bf16: 25 us of 817 less).
   constexpr bool AHEAD = NV <= (LANES == 256 ? 2 : 1);  // else its registers would cost wavefronts
   T yn[NV], sn[NV], dn[NV];
   float rn = 0.0f;
