@@ -265,7 +265,7 @@ constexpr int kFewRows = 32, kFewSegs = 64;
 // kept in two parts: a single bf16 rounding of them adds about as much to the
 // results' 2-norm error as the results' own rounding (sqrt 2 together), and with few
 // rows its share of single results spreads to twice that.  It costs a backward of 64
-// rows over 16 experts of 2048 x 1024 163 us against 147 (three routings), a forward
+// rows over 16 experts of 2048 x 1024 160 us against 147 (three routings), a forward
 // of 40 rows in tiles over 8 of 4096 x 11008 509 against 501.
 gci::FfnGeom gci::ffn_geom(const int64_t* rows, int nranks, int E, uint64_t hidden, uint64_t inter, gc_dtype x_t, bool backward) {
   gci::FfnGeom g;

@@ -20,8 +20,7 @@
 // products wait for the weights anyway: there (SPLIT) each is kept as the sum of two
 // bf16 values, the second the first's rounding error (within 2^-17 of the value
 // together).  A row product's tile then holds 32 rows and 32 rests, whose results
-// its two halves add; a weight gradient sums over the rows and then the rests, taking
-// zeros there for infinities of its other operand.
+// its two halves add; a weight gradient sums over the rests and then the rows.
 //
 // The number of rows of each expert is known on the device alone (the routing
 // plan's split table): a plan kernel turns it into a table of blocks and row
@@ -462,22 +461,6 @@ __device__ __forceinline__ float rounded_off(float v) {
 // operand times a rest of 0, or of the other sign, would make NaN of an infinity.
 __device__ __forceinline__ float with_rest(float v, float rest) { return fabsf(v) < __builtin_inff() ? v + rest : v; }
 
-// Eight bf16 values, with zeros for infinities and NaN: what a weight gradient's other
-// operand is to the rests (the values themselves have brought them into the sum).
-// on: 0x00800080, which carries an exponent of ones into the sign bit; 0 keeps all.
-// Packed 16-bit instructions, 64 or 32 a wavefront and 16 summed values: 3 % of a backward
-// of 64 rows over 16 experts of 2048 x 1024 (163 us against 158 without; three routings).
-__device__ __forceinline__ bf16x8 finite_of(bf16x8 v, uint32_t on) {
-  typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
-  u32x4 w = __builtin_bit_cast(u32x4, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const i16x2 m = (__builtin_bit_cast(i16x2, w[i] & 0x7FFF7FFFu) + __builtin_bit_cast(i16x2, on)) >> 15;
-    w[i] &= ~__builtin_bit_cast(uint32_t, m);
-  }
-  return __builtin_bit_cast(bf16x8, w);
-}
-
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // Instruction classes of the scheduling barriers.
@@ -626,15 +609,7 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
 #pragma unroll
     for (int i = 0; i < MB; ++i) fa[kk & 1][i] = read_a(ta, i, kk);
   };
-  uint32_t finite = 0;  // of the step being multiplied: see finite_of
   auto multiply = [&](int kk) {
-    if constexpr (SPLIT && KIND == kDwDown) {
-#pragma unroll
-      for (int i = 0; i < MB; ++i) fa[kk & 1][i] = finite_of(fa[kk & 1][i], finite);
-    } else if constexpr (SPLIT && KIND == kDwGateUp) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) fb[kk & 1][j] = finite_of(fb[kk & 1][j], finite);
-    }
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -652,9 +627,9 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
   auto load = [&](auto i0, auto a1, auto j0, auto b1, char* ta, char* tb, const Load& l) {
     if constexpr (PARTS) {
       const uint32_t q = uniform(l.k0 >= l.part), k = uniform(l.k0 - q * l.part);
-      if constexpr (WGRAD) load_a.template run<i0.value, a1.value>(ta, in_part(l.a, KIND == kDwGateUp && q), k, l.sum, NO_K1);
+      if constexpr (WGRAD) load_a.template run<i0.value, a1.value>(ta, in_part(l.a, KIND == kDwGateUp && !q), k, l.sum, NO_K1);
       else load_a.template run<i0.value, a1.value>(ta, l.a, l.k0, l.K, NO_K1);
-      load_b.template run<j0.value, b1.value>(tb, in_part(l.b, (KIND == kDx || KIND == kDwDown) && q), k, l.sum, NO_K1);
+      load_b.template run<j0.value, b1.value>(tb, in_part(l.b, KIND == kDx ? q : KIND == kDwDown && !q), k, l.sum, NO_K1);
     } else {
       load_a.template run<i0.value, a1.value>(ta, l.a, l.k0, l.K, NO_K1);
       load_b.template run<j0.value, b1.value>(tb, l.b, l.k0, l.K, K1);
@@ -692,6 +667,20 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
     group_all<READS, SPLIT_A + SPLIT_B, MM>(std::make_integer_sequence<int, MM>{});
   };
 
+  // Between a weight gradient's rests and its values: an infinite operand times a rest of 0,
+  // or of the other sign, leaves NaN, which an infinity of the values would not replace.
+  // Any finite value does here, because that operand comes again (the median of a NaN and
+  // two numbers is one of them).  1 % of a backward of 64 rows over 16 experts of
+  // 2048 x 1024 (160 us, three routings).
+  auto bound_rests = [&] {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_amdgcn_fmed3f(acc[i][j][e], -__FLT_MAX__, __FLT_MAX__);
+  };
+
   Tile cur;
   if (!advance(cur)) return;
   Load to0{cur.A, cur.B, 0, cur.K, cur.part, cur.sum}, to1{cur.A, cur.B, kTileK, cur.K, cur.part, cur.sum};  // what each buffer is filled from
@@ -718,9 +707,9 @@ __global__ void __launch_bounds__(64 * kWaves, TM == 64 && !(SPLIT && (KIND == k
       const bool in0 = k0 + 2 * kTileK < K, in1 = k0 + 3 * kTileK < K;
       to0 = {pick(in0, cur.A, then.A), pick(in0, cur.B, then.B), in0 ? k0 + 2 * kTileK : 0, in0 ? K : then_K,
              in0 ? cur.part : then.part, in0 ? cur.sum : then_sum};
-      if constexpr (SPLIT && WGRAD) finite = k0 >= cur.part ? 0x00800080u : 0;
+      if (SPLIT && WGRAD && k0 == cur.part) bound_rests();
       step(A0, B0, A1, B1, to0, to1);
-      if constexpr (SPLIT && WGRAD) finite = k0 + kTileK >= cur.part ? 0x00800080u : 0;
+      if (SPLIT && WGRAD && k0 + kTileK == cur.part) bound_rests();
       to1 = {pick(in1, cur.A, then.A), pick(in1, cur.B, then.B), in1 ? k0 + 3 * kTileK : kTileK, in1 ? K : then_K,
              in1 ? cur.part : then.part, in1 ? cur.sum : then_sum};
       step(A1, B1, A0, B0, to1, to0);
