@@ -149,17 +149,12 @@ _ES = {GC_INT32: 4, GC_FP32: 4, GC_BF16: 2}
 
 # Tensors that hold values of a type (a code, or int64): its own, or integers as raw bits.  A stand-in
 # without a dtype (None) passes.
-_HOLDS = {}
-
-
-def _holds(t):
-    if not _HOLDS and torch is not None:
-        raw = (torch.uint8, torch.int8, None)
-        _HOLDS.update({GC_BF16: frozenset((torch.bfloat16, torch.int16, torch.uint16) + raw),
-                       GC_FP32: frozenset((torch.float32, torch.int32, torch.uint32) + raw),
-                       GC_INT32: frozenset((torch.int32, torch.uint32) + raw), GC_MX8: frozenset(raw),
-                       "int64": frozenset((torch.int64, torch.uint64) + raw)})
-    return _HOLDS.get(t)
+_RAW = () if torch is None else (torch.uint8, torch.int8, None)
+_HOLDS = {} if torch is None else {
+    GC_BF16: frozenset((torch.bfloat16, torch.int16, torch.uint16) + _RAW),
+    GC_FP32: frozenset((torch.float32, torch.int32, torch.uint32) + _RAW),
+    GC_INT32: frozenset((torch.int32, torch.uint32) + _RAW), GC_MX8: frozenset(_RAW),
+    "int64": frozenset((torch.int64, torch.uint64) + _RAW)}
 
 
 def _buf(x, nbytes, what, holds=None):
@@ -200,7 +195,7 @@ def _bufs(xs, n, nbytes, what, t=None):
         return xs
     arr = _ptr_array(m)()
     need = [nbytes] * n if isinstance(nbytes, int) else nbytes
-    holds = None if t is None else _holds(t)
+    holds = _HOLDS.get(t)
     if m > n:
         need = [*need[:n], *[0] * (m - n)]
     try:
@@ -616,7 +611,7 @@ def _ffn_common(rows, splits, experts_per_rank, hidden, inter, w_gate, w_up, w_d
     w = E * max(0, int(hidden)) * max(0, int(inter))
     if scratch_bytes is None:
         scratch_bytes = scratch.numel() * scratch.element_size()
-    return (N, w, _buf(splits, N * N * E * 8, "splits", _holds("int64")),
+    return (N, w, _buf(splits, N * N * E * 8, "splits", _HOLDS.get("int64")),
             [_bufs(p, N, 2 * w, k, GC_BF16) for p, k in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))],
             _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes))
 
