@@ -1,5 +1,5 @@
-// Argument checks shared by the C ABI files (api.cpp, api_layer.cpp): buffer
-// extents, spans and overlaps on integers, rank counts and enums.
+// Argument checks shared by the C ABI files (api*.cpp): buffer extents, spans
+// and overlaps on integers, rank and row counts, enums, the buffers of a call.
 #pragma once
 
 #include <algorithm>
@@ -79,5 +79,72 @@ inline gc_status check_ptrs(const void* const* p, int n, size_t es, uint64_t byt
     if (!p[i] || addr(p[i]) % es || !fits(p[i], bytes)) return GC_ERR_INVALID_ARG;
   return GC_OK;
 }
+
+// Token-row operators: rows of all ranks, and values of one row.
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr size_t kMaxRow = size_t(1) << 31;
+
+inline bool row_type(gc_dtype t) { return t == GC_BF16 || t == GC_FP32; }
+
+// Buffers of one call: each is checked as it is added (non-null, aligned,
+// inside the address space), and at the end no output may overlap another
+// buffer.  An input that may coincide with an output is not added where it does.
+class Buffers {
+ public:
+  // n buffers of bytes(i) bytes; empty ones are skipped.
+  template <class Bytes>
+  void add(const void* const* p, int n, size_t align, Bytes bytes, bool out) {
+    if (!p) {
+      bad_ = true;
+      return;
+    }
+    for (int i = 0; i < n; ++i) one(p[i], align, bytes(i), out);
+  }
+  void one(const void* p, size_t align, uint64_t bytes, bool out) {
+    if (!bytes) return;
+    if (!p || addr(p) % align || !fits(p, bytes)) {
+      bad_ = true;
+      return;
+    }
+    (out ? outs_[nout_++] : ins_[nin_++]) = span(p, bytes);
+  }
+  // No two outputs overlap, and no input overlaps an output.
+  gc_status check() {
+    if (bad_) return GC_ERR_INVALID_ARG;
+    std::sort(outs_, outs_ + nout_, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    for (int k = 1; k < nout_; ++k)
+      if (outs_[k].lo < outs_[k - 1].hi) return GC_ERR_INVALID_ARG;
+    for (int i = 0; i < nin_; ++i)
+      if (hits(ins_[i])) return GC_ERR_INVALID_ARG;
+    return GC_OK;
+  }
+
+ private:
+  // Whether s overlaps an output: the outputs are sorted and disjoint.
+  bool hits(const Span& s) const {
+    const Span* p = std::lower_bound(outs_, outs_ + nout_, s.lo, [](const Span& o, uint64_t lo) { return o.hi <= lo; });
+    return p != outs_ + nout_ && p->lo < s.hi;
+  }
+  static constexpr int kMost = 8 * GC_MAX_RANKS + 2;
+  Span outs_[kMost], ins_[kMost];
+  int nout_ = 0, nin_ = 0;
+  bool bad_ = false;
+};
+
+// Rows per rank, at least 0 and below 2^31 over all ranks.
+inline gc_status check_rows(const int64_t* rows, int nranks) {
+  GC_TRY(check_ranks(nranks));
+  if (!rows) return GC_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (rows[r] < 0) return GC_ERR_INVALID_ARG;
+    if (rows[r] >= kMaxRows) return GC_ERR_UNSUPPORTED;
+    total += rows[r];
+  }
+  return total >= kMaxRows ? GC_ERR_UNSUPPORTED : GC_OK;
+}
+
+// Whether output p[r] is exactly input q[r] (same start; the sizes agree).
+inline bool same(const void* const* p, const void* const* q, int r) { return p && q && p[r] == q[r]; }
 
 }  // namespace gca
