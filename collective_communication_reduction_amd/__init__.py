@@ -6,8 +6,8 @@ arrays, maps dtype/op/order names onto the C enums, passes torch's current HIP
 stream, and raises GcError for a non-OK status.  Since the library sees only
 addresses, a tensor is checked here first (a contiguous device tensor that
 holds every byte the call touches, else ValueError; the norm, the 8-bit rows,
-the experts and the combine's gradient also check its type, where integer
-tensors count as raw bits); raw addresses and gc_pointers arrays are the
+the experts, the combine's gradient, the embedding, dropout and log
+probabilities also check its type, where integer tensors count as raw bits); raw addresses and gc_pointers arrays are the
 caller's responsibility.  Every collective runs in the
 HIP kernels of libgc.so; there is no other implementation to fall back to, and
 importing this package fails if the library has not been built
@@ -19,7 +19,8 @@ The functions carry the C names:
   gc_bucket_pack, gc_bucket_unpack, gc_bucket_all_reduce, gc_status_string,
   gc_version, gc_last_hip_error; the MoE calls gc_moe_route, gc_moe_dispatch,
   gc_moe_combine and its gradient, gc_moe_ffn and its backward; gc_rms_norm and
-  its backward; gc_mx8_pack, gc_mx8_unpack
+  its backward; gc_mx8_pack, gc_mx8_unpack; gc_embedding and its backward,
+  gc_dropout, gc_token_logprob and its backward
 plus BucketPlan, a small owner of a gc_bucket_plan handle; RankArena, which
 gives each rank its own region of HBM; gc_rank_buffers, which lays N rank
 buffers out in one allocation with a per-rank stagger; and gc_pointers, which
@@ -111,6 +112,17 @@ _c_ffn = _sig("gc_moe_ffn", _int, _VPP, _int, _I64P, _vp, _int, _int, _sz, _sz, 
               _sz, _vp)
 _c_ffn_bwd = _sig("gc_moe_ffn_backward", _int, _VPP, _VPP, _int, _VPP, _int, _I64P, _vp, _int, _int, _sz, _sz, _VPP, _VPP,
                   _VPP, _VPP, _VPP, _VPP, _VPP, _int, _vp, _sz, _vp)
+_u64, _f32 = ctypes.c_uint64, ctypes.c_float
+_c_embed = _sig("gc_embedding", _int, _VPP, _VPP, _I64P, _int, _sz, _sz, _f32, _int, _VPP, _vp)
+_c_embed_bwd_scratch = _sig("gc_embedding_backward_scratch_bytes", _sz, _I64P, _int, _sz, _sz)
+_c_embed_bwd = _sig("gc_embedding_backward", _int, _VPP, _VPP, _I64P, _int, _sz, _sz, _f32, _int, _VPP, _int, _int, _vp,
+                    _sz, _vp)
+_c_dropout = _sig("gc_dropout", _int, _VPP, _VPP, _I64P, _int, _f32, _u64, _u64, _vp, _int, _VPP, _vp)
+_c_logprob_scratch = _sig("gc_token_logprob_scratch_bytes", _sz, _I64P, _int, _sz, _int)
+_c_logprob = _sig("gc_token_logprob", _int, _VPP, _VPP, _I64P, _int, _sz, _sz, _f32, _int, _VPP, _VPP, _VPP, _int, _VPP,
+                  _VPP, _VPP, _VPP, _VPP, _vp, _sz, _vp)
+_c_logprob_bwd = _sig("gc_token_logprob_backward", _int, _VPP, _VPP, _VPP, _VPP, _VPP, _VPP, _I64P, _int, _sz, _sz, _f32,
+                      _int, _VPP, _vp)
 _c_plan_destroy = _sig("gc_bucket_plan_destroy", None, _vp)
 _c_status = _sig("gc_status_string", ctypes.c_char_p, _int)
 _c_version = _sig("gc_version", _int)
@@ -648,6 +660,94 @@ def gc_moe_ffn_backward(dy, x, saved, rows, splits, experts_per_rank, hidden, in
                       N, int(experts_per_rank), int(hidden), int(inter), *ws, _bufs(dx, N, row, "dx", GC_BF16), *dws, wt, sc, scb,
                       _stream(stream, _first(dx))), "gc_moe_ffn_backward")
     return dx, dw_gate, dw_up, dw_down
+
+
+# ------------------------------------------------------------------ the two ends of a training step
+
+def gc_embedding(weight, tokens, ntokens, vocab, hidden, out, scale=1.0, dtype=None, stream=None):
+    """out[r][t] = scale * weight[r][tokens[r][t]], per rank; a token outside [0, vocab) gives a zero row.
+    tokens[r]: int32 [ntokens[r]]; weight[r]: [vocab][hidden] bf16 or fp32; out[r]: [ntokens[r]][hidden]."""
+    N, t = len(ntokens), _infer_dtype(weight, dtype)
+    row = _row_bytes(hidden, t)
+    full = [max(0, int(vocab)) * row if int(c) > 0 else 0 for c in ntokens]
+    _check(_c_embed(_bufs(weight, N, full, "weight", t), _bufs(tokens, N, _rows_of(ntokens, 4), "tokens", GC_INT32),
+                    _i64_array(ntokens), N, max(0, int(vocab)), max(0, int(hidden)), float(scale), t,
+                    _bufs(out, N, _rows_of(ntokens, row), "out", t), _stream(stream, _first(out))), "gc_embedding")
+    return out
+
+
+def gc_embedding_backward_scratch_bytes(ntokens, vocab, hidden):
+    """Scratch bytes gc_embedding_backward needs (0 if the sizes are invalid)."""
+    return int(_c_embed_bwd_scratch(_i64_array(ntokens), len(ntokens), max(0, int(vocab)), max(0, int(hidden))))
+
+
+def gc_embedding_backward(dout, tokens, ntokens, vocab, hidden, dweight, scratch, scale=1.0, accumulate=False,
+                          scratch_bytes=None, dtype=None, dw_dtype=None, stream=None):
+    """dweight[r][v] = scale * (sum of dout[r][t] over the tokens t equal to v), zeros for other rows; with accumulate
+    the sums are added to dweight, whose other rows stay.  dout and dweight: bf16 or fp32 each."""
+    N, t, wt = len(ntokens), _infer_dtype(dout, dtype), _infer_dtype(dweight, dw_dtype)
+    if scratch_bytes is None:
+        scratch_bytes = scratch.numel() * scratch.element_size()
+    _check(_c_embed_bwd(_bufs(dout, N, _rows_of(ntokens, _row_bytes(hidden, t)), "dout", t),
+                        _bufs(tokens, N, _rows_of(ntokens, 4), "tokens", GC_INT32), _i64_array(ntokens), N,
+                        max(0, int(vocab)), max(0, int(hidden)), float(scale), t,
+                        _bufs(dweight, N, max(0, int(vocab)) * _row_bytes(hidden, wt), "dweight", wt), wt,
+                        int(bool(accumulate)), _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes),
+                        _stream(stream, _first(dweight))), "gc_embedding_backward")
+    return dweight
+
+
+def gc_dropout(x, counts, p, seed, y, offset=0, step=None, residual=None, dtype=None, stream=None):
+    """y = residual + dropout(x) of each rank's counts[r] elements; y may be x or residual.  The mask follows from
+    (seed, offset + step, rank, element) alone, so the gradient is the same call on y's gradient without residual.
+    step: an int64 device tensor of one value that a replayed graph may count up, or None."""
+    N, t = len(counts), _infer_dtype(x, dtype)
+    nb = _rows_of(counts, _ES.get(t, 0))
+    _check(_c_dropout(_bufs(x, N, nb, "x", t), _bufs(residual, N, nb, "residual", t), _i64_array(counts), N, float(p),
+                      int(seed) & SIZE_MAX, int(offset) & SIZE_MAX, _buf(step, 8, "step", _HOLDS.get("int64")), t,
+                      _bufs(y, N, nb, "y", t), _stream(stream, _first(y))), "gc_dropout")
+    return y
+
+
+def gc_token_logprob_scratch_bytes(ntokens, vocab, top=0):
+    """Scratch bytes gc_token_logprob needs (0 if the sizes are invalid)."""
+    return int(_c_logprob_scratch(_i64_array(ntokens), len(ntokens), max(0, int(vocab)), int(top)))
+
+
+def gc_token_logprob(logits, ntokens, vocab, scratch, targets=None, logprob=None, entropy=None, lse=None, top=0,
+                     top_ids=None, top_logprob=None, dlogprob=None, dentropy=None, dlogits=None, stride=None, scale=1.0,
+                     scratch_bytes=None, dtype=None, stream=None):
+    """Per row of scale * logits[r] ([ntokens[r]] rows of stride elements, vocab of them read): the log probability of
+    the row's target, the entropy, the log of the sum of exponentials and the `top` most likely tokens with their log
+    probabilities, each where a buffer is given.  With dlogprob (and dentropy) the gradient is written to dlogits in
+    the same pass, as gc_token_logprob_backward would."""
+    N, t = len(ntokens), _infer_dtype(logits, dtype)
+    stride, vocab = int(vocab if stride is None else stride), max(0, int(vocab))
+    if scratch_bytes is None:
+        scratch_bytes = scratch.numel() * scratch.element_size()
+    rows, each, tops = (_rows_of(ntokens, k) for k in (_row_bytes(stride, t), 4, 4 * max(0, int(top))))
+    f = lambda xs, what: _bufs(xs, N, each, what, GC_FP32)  # noqa: E731
+    _check(_c_logprob(_bufs(logits, N, rows, "logits", t), _bufs(targets, N, each, "targets", GC_INT32), _i64_array(ntokens),
+                      N, vocab, max(0, stride), float(scale), t, f(logprob, "logprob"), f(entropy, "entropy"), f(lse, "lse"),
+                      int(top), _bufs(top_ids, N, tops, "top_ids", GC_INT32), _bufs(top_logprob, N, tops, "top_logprob", GC_FP32),
+                      f(dlogprob, "dlogprob"), f(dentropy, "dentropy"), _bufs(dlogits, N, rows, "dlogits", t),
+                      _buf(scratch, int(scratch_bytes), "scratch"), int(scratch_bytes), _stream(stream, _first(logits))),
+           "gc_token_logprob")
+    return logprob
+
+
+def gc_token_logprob_backward(logits, ntokens, vocab, lse, targets, dlogprob, dlogits, entropy=None, dentropy=None,
+                              stride=None, scale=1.0, dtype=None, stream=None):
+    """dlogits (may be logits) from dlogprob and, with the forward's entropy, dentropy; zeros in the padding columns."""
+    N, t = len(ntokens), _infer_dtype(logits, dtype)
+    stride, vocab = int(vocab if stride is None else stride), max(0, int(vocab))
+    rows, each = _rows_of(ntokens, _row_bytes(stride, t)), _rows_of(ntokens, 4)
+    f = lambda xs, what: _bufs(xs, N, each, what, GC_FP32)  # noqa: E731
+    _check(_c_logprob_bwd(_bufs(logits, N, rows, "logits", t), _bufs(targets, N, each, "targets", GC_INT32), f(lse, "lse"),
+                          f(entropy, "entropy"), f(dlogprob, "dlogprob"), f(dentropy, "dentropy"), _i64_array(ntokens), N,
+                          vocab, max(0, stride), float(scale), t, _bufs(dlogits, N, rows, "dlogits", t),
+                          _stream(stream, _first(dlogits))), "gc_token_logprob_backward")
+    return dlogits
 
 
 # ------------------------------------------------------------------ HBM layout

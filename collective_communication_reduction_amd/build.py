@@ -32,8 +32,8 @@ HIP_FLAGS = [
     "-Wall", "-Wno-unused-function",
 ]
 
-LIB_SOURCES = ["api.cpp", "api_layer.cpp", "reduce.hip", "movement.hip", "bucket.hip", "moe.hip", "hier.hip",
-               "norm.hip", "mx8.hip", "moe_grad.hip", "ffn.hip"]
+LIB_SOURCES = ["api.cpp", "api_layer.cpp", "api_token.cpp", "reduce.hip", "movement.hip", "bucket.hip", "moe.hip",
+               "hier.hip", "norm.hip", "mx8.hip", "moe_grad.hip", "ffn.hip", "embed.hip", "dropout.hip", "logprob.hip"]
 
 
 def _hipcc():

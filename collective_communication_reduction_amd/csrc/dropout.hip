@@ -1,0 +1,119 @@
+// Dropout with the residual's addition, from a counter-based generator, for gfx950.
+//
+//   y = residual + keep * x / (1 - p)
+//
+// keep of element i depends on (seed, offset + step, rank, i) alone: words of
+// Philox4x32-10 (J. Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+// SC 2011), so no mask is ever stored and the gradient's call makes the same one.
+// One 128-bit block of the generator serves eight elements, 16 bits each: with 32
+// bits each the generator's 20 quarter-rate products per block, not HBM, would
+// bound bf16 rows.
+
+#include <type_traits>
+
+#include "units.h"
+
+namespace {
+
+using namespace gcdev;
+
+constexpr int kPer = 8;   // elements of one generator block
+
+template <int P>
+struct DropoutArgs {
+  const char* x[P];
+  const char* res[P];
+  char* y[P];
+  int64_t n[P];
+  int32_t tile0[P + 1];
+  uint32_t block0;
+  int32_t N;
+  uint32_t key0, key1;
+  uint64_t offset;
+  const uint64_t* step;
+  uint32_t drop;
+  float scale;
+};
+
+__device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c[0], b = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
+    const uint32_t c1 = c[1], c3 = c[3];
+    c[0] = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c[1] = static_cast<uint32_t>(b);
+    c[2] = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c[3] = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// A lane takes one generator block; a workgroup kThreads consecutive ones.
+template <class In, bool RES, int P>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs<P> a) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE, Q = kPer / VE;
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const uint64_t b = static_cast<uint64_t>(block - a.tile0[rank]) * kThreads + threadIdx.x;
+  const uint64_t n = a.n[rank];
+  if (b * kPer >= n) return;
+  u32x4 x[Q], r[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    x[q] = U::load(a.x[rank], n, b * Q + q, 0);
+    if (RES) r[q] = U::load(a.res[rank], n, b * Q + q, 0);
+  }
+  const uint64_t at = a.offset + (a.step ? *a.step : 0);
+  uint32_t c[4] = {static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32) | static_cast<uint32_t>(rank) << 8,
+                   static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32)};
+  philox(c, a.key0, a.key1);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    float v[VE], s[VE];
+    U::widen(x[q], v);
+    if (RES) U::widen(r[q], s);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int i = q * VE + e;
+      const uint32_t u = i % 2 ? c[i / 2] >> 16 : c[i / 2] & 0xFFFFu;
+      const float k = u >= a.drop ? v[e] * a.scale : 0.0f;  // a dropped value counts as 0, whatever it is
+      v[e] = RES ? s[e] + k : k;
+    }
+    U::store(a.y[rank], n, b * Q + q, U::narrow(v));
+  }
+}
+
+template <class In, int P>
+gc_status dropout_typed(const gci::DropoutCall& c) {
+  DropoutArgs<P> a{};
+  for (int s = 0; s < c.nranks; ++s) {
+    a.x[s] = static_cast<const char*>(c.x[s]);
+    if (c.res) a.res[s] = static_cast<const char*>(c.res[s]);
+    a.y[s] = static_cast<char*>(c.y[s]);
+    a.n[s] = c.counts[s];
+  }
+  if (!fill_blocks<P>(a.tile0, c.counts, c.nranks, kThreads * kPer)) return GC_ERR_UNSUPPORTED;
+  a.N = c.nranks;
+  a.key0 = static_cast<uint32_t>(c.seed);
+  a.key1 = static_cast<uint32_t>(c.seed >> 32);
+  a.offset = c.offset;
+  a.step = c.step;
+  a.drop = c.drop;
+  a.scale = c.scale;
+  const int32_t g = a.tile0[c.nranks];
+  return c.res ? launch_blocks(dropout_kernel<In, true, P>, a, g, kThreads, c.stream)
+               : launch_blocks(dropout_kernel<In, false, P>, a, g, kThreads, c.stream);
+}
+
+}  // namespace
+
+namespace gci {
+
+gc_status launch_dropout(const DropoutCall& c) {
+  if (c.t == GC_BF16) return c.nranks <= 8 ? dropout_typed<InBf16, 8>(c) : dropout_typed<InBf16, 64>(c);
+  return c.nranks <= 8 ? dropout_typed<InF32, 8>(c) : dropout_typed<InF32, 64>(c);
+}
+
+}  // namespace gci

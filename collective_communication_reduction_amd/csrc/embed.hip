@@ -1,0 +1,412 @@
+// Token embedding and its gradient, for gfx950.
+//
+//   out[t] = scale * W[id t]          dW[v] = scale * sum over t with id t = v of dout[t]
+//
+// The gradient first sorts the tokens by id, stably (counting sort by one or two
+// digits of the id), so that each row's terms are added in token order whatever
+// the timing: results repeat bit for bit, and no atomic touches a gradient.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "units.h"
+
+namespace {
+
+using namespace gcdev;
+
+// ------------------------------------------------------------- lookup
+
+template <int P>
+struct EmbeddingArgs {
+  const char* w[P];
+  const int32_t* ids[P];
+  char* out[P];
+  int64_t tok[P];
+  int32_t tile0[P + 1];
+  uint32_t block0;
+  int32_t N;
+  uint32_t vocab;
+  uint64_t H;
+  uint64_t units;       // per row, the last may be short
+  uint32_t slices;      // of a row, NV << lanes_log2 units each
+  int32_t lanes_log2;   // lanes that share a row's slice
+  float scale;
+};
+
+template <class In, int NV, int P>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingArgs<P> a) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE;
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const uint64_t q = (static_cast<uint64_t>(block - a.tile0[rank]) * kThreads + threadIdx.x) >> a.lanes_log2;
+  const uint64_t row = a.slices == 1 ? q : q / a.slices;
+  if (row >= static_cast<uint64_t>(a.tok[rank])) return;
+  const uint32_t lanes = 1u << a.lanes_log2;
+  const uint64_t u0 = (q - row * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + (threadIdx.x & (lanes - 1));
+  const uint32_t id = static_cast<uint32_t>(a.ids[rank][row]);
+  const bool known = id < a.vocab;
+  const char* src = a.w[rank] + static_cast<uint64_t>(known ? id : 0) * a.H * In::ES;
+  char* dst = a.out[rank] + row * a.H * In::ES;
+  u32x4 x[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) x[j] = known ? U::template load<true>(src, a.H, u0 + j * lanes, 0) : u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float v[VE];
+    U::widen(x[j], v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = known ? v[e] * a.scale : 0.0f;
+    U::store(dst, a.H, u0 + j * lanes, U::narrow(v));
+  }
+}
+
+// ------------------------------------------------------------- sort by token
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWaves = kSortThreads / kWave;
+
+template <int P>
+struct SortArgs {
+  const int32_t* ids[P];
+  int64_t tok[P];
+  int64_t at[P];          // first entry of each rank in the scratch lists
+  int32_t tile0[P + 1];
+  uint32_t block0;
+  int32_t N;
+  int32_t chunk;          // entries per workgroup
+  uint32_t vocab;
+  int32_t shift, bits;    // the digit of this pass
+  uint64_t* pairs;        // id << 32 | token, between the passes
+  int32_t* keys;          // sorted ids and their tokens
+  int32_t* perm;
+  uint32_t* counts;       // [chunks][1 << bits]
+  int32_t* valid;         // tokens of each rank inside the vocabulary
+};
+
+// Entry i of the pass's input as id << 32 | token; ~0 for a token outside the vocabulary.
+template <bool FIRST, int P>
+__device__ __forceinline__ uint64_t sort_entry(const SortArgs<P>& a, int rank, int64_t i, int64_t n) {
+  if (i >= n) return ~uint64_t(0);
+  if constexpr (FIRST) {
+    const uint32_t id = static_cast<uint32_t>(a.ids[rank][i]);
+    return id < a.vocab ? static_cast<uint64_t>(id) << 32 | static_cast<uint32_t>(i) : ~uint64_t(0);
+  } else {
+    return a.pairs[a.at[rank] + i];
+  }
+}
+
+template <int P>
+__device__ __forceinline__ uint32_t digit_of(const SortArgs<P>& a, uint64_t entry) {
+  return static_cast<uint32_t>(entry >> (32 + a.shift)) & ((1u << a.bits) - 1);
+}
+
+// Digit counts of one chunk.
+template <bool FIRST, int P>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs<P> a) {
+  extern __shared__ uint32_t hist[];
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t n = FIRST ? a.tok[rank] : a.valid[rank];
+  const int64_t first = static_cast<int64_t>(block - a.tile0[rank]) * a.chunk;
+  const int bins = 1 << a.bits;
+  for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.chunk; i += kSortThreads) {
+    const uint64_t e = sort_entry<FIRST>(a, rank, first + i, n);
+    if (e != ~uint64_t(0)) atomicAdd(&hist[digit_of(a, e)], 1u);
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < bins; d += kSortThreads) a.counts[static_cast<uint64_t>(block) * bins + d] = hist[d];
+}
+
+// Exclusive sum over the workgroup's threads.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t x, uint32_t* lds, uint32_t& total) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  uint32_t s = x;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint32_t t = __shfl_up(s, o);
+    if (lane >= o) s += t;
+  }
+  if (lane == kWave - 1) lds[wave] = s;
+  __syncthreads();
+  uint32_t before = 0;
+  total = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    before += w < wave ? lds[w] : 0;
+    total += lds[w];
+  }
+  __syncthreads();
+  return before + s - x;
+}
+
+// Places one chunk's entries: behind all entries of smaller digits, those of the
+// same digit in earlier chunks, and those of earlier wavefronts and lanes.
+template <bool FIRST, bool LAST, int P>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs<P> a) {
+  extern __shared__ uint32_t next[];   // [wavefront][digit]: entries counted, then the place of the next one
+  __shared__ uint32_t sums[kSortWaves];
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int64_t n = FIRST ? a.tok[rank] : a.valid[rank];
+  const int32_t mine = block - a.tile0[rank], chunks = a.tile0[rank + 1] - a.tile0[rank];
+  const int bins = 1 << a.bits, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int per = a.chunk / kSortWaves;
+  const int64_t first = static_cast<int64_t>(mine) * a.chunk + wave * per;
+  uint32_t* my = next + wave * bins;
+  for (int d = threadIdx.x; d < kSortWaves * bins; d += kSortThreads) next[d] = 0;
+  __syncthreads();
+  for (int i = lane; i < per; i += kWave) {
+    const uint64_t e = sort_entry<FIRST>(a, rank, first + i, n);
+    if (e != ~uint64_t(0)) atomicAdd(&my[digit_of(a, e)], 1u);
+  }
+  __syncthreads();
+  // digits in order, a run of them per thread
+  const int run = (bins + kSortThreads - 1) / kSortThreads;
+  const uint32_t* counts = a.counts + static_cast<uint64_t>(a.tile0[rank]) * bins;
+  const int d0 = min(static_cast<int>(threadIdx.x) * run, bins), d1 = min(d0 + run, bins);
+  uint32_t sum = 0;
+  for (int d = d0; d < d1; ++d)
+    for (int c = 0; c < chunks; ++c) sum += counts[static_cast<uint64_t>(c) * bins + d];
+  uint32_t total;
+  uint32_t at = block_exclusive(sum, sums, total);
+  for (int d = d0; d < d1; ++d) {
+    uint32_t before = 0, all = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t k = counts[static_cast<uint64_t>(c) * bins + d];
+      all += k;
+      before += c < mine ? k : 0;
+    }
+    uint32_t place = at + before;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t k = next[w * bins + d];
+      next[w * bins + d] = place;
+      place += k;
+    }
+    at += all;
+  }
+  if (FIRST && mine == 0 && threadIdx.x == 0) a.valid[rank] = static_cast<int32_t>(total);
+  __syncthreads();
+  for (int i = 0; i < per; i += kWave) {
+    const uint64_t e = sort_entry<FIRST>(a, rank, first + i + lane, i + lane < per ? n : 0);
+    const bool ok = e != ~uint64_t(0);
+    const uint32_t d = ok ? digit_of(a, e) : 0;
+    uint64_t peers = __ballot(ok);
+    for (int b = 0; b < a.bits; ++b) {
+      const uint64_t ones = __ballot(d >> b & 1);
+      peers &= d >> b & 1 ? ones : ~ones;
+    }
+    const int before = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    const uint32_t place = ok ? my[d] + before : 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (ok && before == 0) my[d] += __popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (ok) {
+      if constexpr (LAST) {
+        a.keys[a.at[rank] + place] = static_cast<int32_t>(e >> 32);
+        a.perm[a.at[rank] + place] = static_cast<int32_t>(e);
+      } else {
+        a.pairs[a.at[rank] + place] = e;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- sums of sorted rows
+
+template <int P>
+struct RowSumArgs {
+  const char* dout[P];
+  char* dw[P];
+  int64_t at[P];
+  uint32_t block0;
+  int32_t N;
+  uint64_t vocab;
+  uint64_t H;
+  uint64_t units;
+  const int32_t* keys;
+  const int32_t* perm;
+  const int32_t* valid;
+  float scale;
+  bool accumulate;
+};
+
+// First of n sorted keys that is at least v.
+__device__ __forceinline__ int32_t first_key(const int32_t* keys, int32_t n, int32_t v) {
+  int32_t lo = 0;
+  while (n > 0) {
+    const int32_t half = n >> 1;
+    if (keys[lo + half] < v) {
+      lo += half + 1;
+      n -= half + 1;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
+// VE sums of one unit to the gradient's type, behind what is there already where `add`.
+template <class In, class OutT>
+__device__ __forceinline__ void put_sums(char* row, uint64_t H, uint64_t u, const float (&acc)[In::VE], float scale, bool add) {
+  constexpr int VE = In::VE;
+  if constexpr (std::is_same<In, OutT>::value) {
+    typedef AnyUnit<In> U;
+    float v[VE], old[VE];
+    if (add) U::widen(U::load(row, H, u, 0), old);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) v[e] = add ? acc[e] * scale + old[e] : acc[e] * scale;
+    U::store(row, H, u, U::narrow(v));
+  } else {
+    // units of the other type: two fp32 units for one of bf16, half a bf16 unit for one of fp32
+    typedef typename std::conditional<OutT::ES == 2, uint16_t, float>::type E;
+    E* p = reinterpret_cast<E*>(row) + u * VE;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (u * VE + e < H) {
+        float v = acc[e] * scale;
+        if (add) v += OutT::one(p, e);
+        if constexpr (OutT::ES == 2) p[e] = static_cast<uint16_t>(bf16_bits(v));
+        else p[e] = v;
+      }
+  }
+}
+
+template <class In, class OutT, int P>
+__global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE;
+  const uint64_t block = a.block0 + blockIdx.x;
+  const int rank = static_cast<int>(block / a.vocab);
+  const int32_t v = static_cast<int32_t>(block % a.vocab);
+  const int32_t* keys = a.keys + a.at[rank];
+  const int32_t* perm = a.perm + a.at[rank];
+  const int32_t n = a.valid[rank];
+  const int32_t first = first_key(keys, n, v), last = first + first_key(keys + first, n - first, v + 1);
+  if (a.accumulate && first == last) return;
+  char* row = a.dw[rank] + static_cast<uint64_t>(v) * a.H * OutT::ES;
+  for (uint64_t u = threadIdx.x; u < a.units; u += kThreads) {
+    float acc[VE] = {};
+    for (int32_t i = first; i < last; ++i) {
+      float x[VE];
+      U::widen(U::load(a.dout[rank] + static_cast<uint64_t>(perm[i]) * a.H * In::ES, a.H, u, 0), x);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) acc[e] += x[e];
+    }
+    put_sums<In, OutT>(row, a.H, u, acc, a.scale, a.accumulate);
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+template <class In, int NV, int P>
+gc_status embedding_impl(const gci::EmbeddingCall& c, EmbeddingArgs<P>& a) {
+  const uint64_t per = static_cast<uint64_t>(NV) << a.lanes_log2;
+  const uint64_t slices = (a.units + per - 1) / per;
+  a.slices = static_cast<uint32_t>(slices);
+  if (!fill_blocks<P>(a.tile0, c.tokens, c.nranks, kThreads >> a.lanes_log2, slices)) return GC_ERR_UNSUPPORTED;
+  return launch_blocks(embedding_kernel<In, NV, P>, a, a.tile0[c.nranks], kThreads, c.stream);
+}
+
+template <class In, int P>
+gc_status embedding_typed(const gci::EmbeddingCall& c) {
+  EmbeddingArgs<P> a{};
+  for (int s = 0; s < c.nranks; ++s) {
+    a.w[s] = static_cast<const char*>(c.w[s]);
+    a.ids[s] = c.ids[s];
+    a.out[s] = static_cast<char*>(c.out[s]);
+    a.tok[s] = c.tokens[s];
+  }
+  a.N = c.nranks;
+  a.vocab = static_cast<uint32_t>(c.vocab);
+  a.H = c.hidden;
+  a.units = (c.hidden + In::VE - 1) / In::VE;
+  a.scale = c.scale;
+  while (a.lanes_log2 < 6 && (uint64_t(1) << a.lanes_log2) < a.units) ++a.lanes_log2;
+  return a.units > kWave ? embedding_impl<In, 4, P>(c, a) : embedding_impl<In, 1, P>(c, a);
+}
+
+template <bool FIRST, bool LAST, int P>
+gc_status sort_pass(SortArgs<P>& a, const gci::EmbeddingGeom& g, hipStream_t stream) {
+  const size_t bins = size_t(1) << a.bits;
+  void* params[] = {&a};
+  const auto go = [&](const void* kernel, size_t lds) {
+    return gci::in_launches(g.chunks, kSortThreads, [&](uint32_t first, uint32_t n) {
+      a.block0 = first;
+      return gci::hip_status(hipLaunchKernel(kernel, dim3(n), dim3(kSortThreads), params, lds, stream));
+    });
+  };
+  const gc_status s = go(reinterpret_cast<const void*>(sort_count_kernel<FIRST, P>), bins * 4);
+  return s != GC_OK ? s : go(reinterpret_cast<const void*>(sort_place_kernel<FIRST, LAST, P>), kSortWaves * bins * 4);
+}
+
+template <class In, class OutT, int P>
+gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
+  const gci::EmbeddingGeom& g = c.geom;
+  char* scratch = static_cast<char*>(c.scratch);
+  SortArgs<P> s{};
+  RowSumArgs<P> r{};
+  int64_t at = 0;
+  for (int k = 0; k < c.nranks; ++k) {
+    s.ids[k] = c.ids[k];
+    s.tok[k] = c.tokens[k];
+    s.at[k] = r.at[k] = at;
+    r.dout[k] = static_cast<const char*>(c.dout[k]);
+    r.dw[k] = static_cast<char*>(c.dw[k]);
+    at += c.tokens[k];
+    s.tile0[k + 1] = s.tile0[k] + std::max<int32_t>(1, static_cast<int32_t>((c.tokens[k] + g.chunk - 1) / g.chunk));
+  }
+  for (int k = c.nranks; k < P; ++k) s.tile0[k + 1] = s.tile0[k];
+  s.N = r.N = c.nranks;
+  s.chunk = g.chunk;
+  s.vocab = static_cast<uint32_t>(c.vocab);
+  s.pairs = reinterpret_cast<uint64_t*>(scratch + g.pairs);
+  r.keys = s.keys = reinterpret_cast<int32_t*>(scratch + g.keys);
+  r.perm = s.perm = reinterpret_cast<int32_t*>(scratch + g.perm);
+  s.counts = reinterpret_cast<uint32_t*>(scratch + g.counts);
+  r.valid = s.valid = reinterpret_cast<int32_t*>(scratch + g.valid);
+  s.bits = g.low_bits;
+  gc_status st;
+  if (g.low_bits == g.bits) {
+    st = sort_pass<true, true, P>(s, g, c.stream);
+  } else {
+    st = sort_pass<true, false, P>(s, g, c.stream);
+    if (st != GC_OK) return st;
+    s.shift = g.low_bits;
+    s.bits = g.bits - g.low_bits;
+    st = sort_pass<false, true, P>(s, g, c.stream);
+  }
+  if (st != GC_OK) return st;
+  r.vocab = c.vocab;
+  r.H = c.hidden;
+  r.units = (c.hidden + In::VE - 1) / In::VE;
+  r.scale = c.scale;
+  r.accumulate = c.accumulate;
+  return launch_blocks(row_sum_kernel<In, OutT, P>, r, c.nranks * c.vocab, kThreads, c.stream);
+}
+
+template <class In, class OutT>
+gc_status embedding_backward_ranks(const gci::EmbeddingBackwardCall& c) {
+  return c.nranks <= 8 ? embedding_backward_typed<In, OutT, 8>(c) : embedding_backward_typed<In, OutT, 64>(c);
+}
+
+}  // namespace
+
+namespace gci {
+
+gc_status launch_embedding(const EmbeddingCall& c) {
+  if (c.t == GC_BF16) return c.nranks <= 8 ? embedding_typed<InBf16, 8>(c) : embedding_typed<InBf16, 64>(c);
+  return c.nranks <= 8 ? embedding_typed<InF32, 8>(c) : embedding_typed<InF32, 64>(c);
+}
+
+gc_status launch_embedding_backward(const EmbeddingBackwardCall& c) {
+  if (c.t == GC_BF16)
+    return c.dw_t == GC_BF16 ? embedding_backward_ranks<InBf16, InBf16>(c) : embedding_backward_ranks<InBf16, InF32>(c);
+  return c.dw_t == GC_BF16 ? embedding_backward_ranks<InF32, InBf16>(c) : embedding_backward_ranks<InF32, InF32>(c);
+}
+
+}  // namespace gci

@@ -295,4 +295,95 @@ FfnGeom ffn_geom(const int64_t* rows, int nranks, int experts_per_rank, uint64_t
 gc_status launch_moe_ffn(const FfnCall& call);
 gc_status launch_moe_ffn_backward(const FfnCall& call);
 
+// ---- the two ends of a training step (embed.hip, dropout.hip, logprob.hip)
+
+// Token lookup (see gc_embedding).
+struct EmbeddingCall {
+  const void* const* w;
+  const int32_t* const* ids;
+  const int64_t* tokens;
+  int nranks;
+  uint64_t vocab;
+  uint64_t hidden;
+  float scale;
+  gc_dtype t;
+  void* const* out;
+  hipStream_t stream;
+};
+gc_status launch_embedding(const EmbeddingCall& call);
+
+// Scratch areas of the lookup's gradient, as byte offsets, and its split of the
+// tokens: every rank's tokens are sorted in `chunk`-token pieces by two digits
+// of the id, the low one of `low_bits` bits.
+struct EmbeddingGeom {
+  int64_t tokens = 0;   // of all ranks
+  int32_t chunk = 0;
+  int32_t chunks = 0;   // of all ranks
+  int32_t bits = 0;     // of an id
+  int32_t low_bits = 0;
+  uint64_t pairs = 0, keys = 0, perm = 0, counts = 0, valid = 0, bytes = 0;
+};
+EmbeddingGeom embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden);
+
+struct EmbeddingBackwardCall {
+  const void* const* dout;
+  const int32_t* const* ids;
+  const int64_t* tokens;
+  int nranks;
+  uint64_t vocab;
+  uint64_t hidden;
+  float scale;
+  gc_dtype t;
+  void* const* dw;
+  gc_dtype dw_t;
+  bool accumulate;
+  void* scratch;
+  EmbeddingGeom geom;
+  hipStream_t stream;
+};
+gc_status launch_embedding_backward(const EmbeddingBackwardCall& call);
+
+// Dropout of every rank's elements (see gc_dropout); res and step may be null.
+struct DropoutCall {
+  const void* const* x;
+  const void* const* res;
+  const int64_t* counts;
+  int nranks;
+  uint32_t drop;        // values whose 16 random bits are below this are dropped
+  float scale;          // of the values kept
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* step;
+  gc_dtype t;
+  void* const* y;
+  hipStream_t stream;
+};
+gc_status launch_dropout(const DropoutCall& call);
+
+// Token log probabilities (see gc_token_logprob) and their gradient; which of
+// the lists are null says what is asked for.
+struct LogprobCall {
+  const void* const* logits;
+  const int32_t* const* targets;
+  const int64_t* tokens;
+  int nranks;
+  uint64_t vocab;
+  uint64_t stride;
+  float scale;
+  gc_dtype t;
+  float* const* logprob;
+  float* const* entropy;
+  float* const* lse;
+  int top;
+  int32_t* const* top_ids;
+  float* const* top_logprob;
+  const float* const* dlogprob;
+  const float* const* dentropy;
+  void* const* dlogits;
+  void* scratch;
+  hipStream_t stream;
+};
+gc_status launch_token_logprob(const LogprobCall& call);
+gc_status launch_token_logprob_backward(const LogprobCall& call);
+
 }  // namespace gci

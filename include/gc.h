@@ -476,6 +476,122 @@ gc_status gc_moe_ffn_backward(const void* const* dy, const void* const* x, gc_dt
                               void* scratch, size_t scratch_bytes, hipStream_t stream);
 
 /*
+ * Token embedding: row id of a rank's weight for each of its tokens,
+ *   out[t] = scale * weight[tokens[t]], the product rounded once to t.
+ *   weight[r]  DEVICE [vocab] rows of hidden elements of t (GC_BF16 or GC_FP32);
+ *              ranks may share one buffer.
+ *   tokens[r]  DEVICE int32 [ntokens[r]].  Ids outside [0, vocab) are padding:
+ *              a zero row, and no gradient.  (A rank that holds a slice of the
+ *              vocabulary passes its ids less the slice's start, and an
+ *              all-reduce sums the parts.)
+ *   out[r]     DEVICE [ntokens[r]] rows.
+ * vocab is at most 2^22; rows of all ranks below 2^31 (GC_ERR_UNSUPPORTED beyond).
+ * scale is finite.  Rows may start at any element's address.
+ */
+gc_status gc_embedding(const void* const* weight, const int32_t* const* tokens, const int64_t* ntokens, int nranks,
+                       size_t vocab, size_t hidden, float scale, gc_dtype t, void* const* out, hipStream_t stream);
+
+/* Scratch bytes gc_embedding_backward needs (0 if the sizes are invalid). */
+size_t gc_embedding_backward_scratch_bytes(const int64_t* ntokens, int nranks, size_t vocab, size_t hidden);
+
+/*
+ * Gradient of gc_embedding:
+ *   dweight[r][v] = scale * (sum over t with tokens[r][t] == v of dout[r][t]),
+ * added in fp32, rounded once to dw_t.  Every row is written, zeros for a token
+ * that does not occur; with accumulate nonzero the sums are added to what
+ * dweight holds (in fp32, before the rounding), and the other rows keep it.
+ * Tokens are sorted first and summed in an order that they alone fix, so runs
+ * repeat bit for bit.
+ *   dout[r]     DEVICE [ntokens[r]] rows of hidden elements of t.
+ *   dweight[r]  DEVICE [vocab] rows of hidden elements of dw_t, written also for a
+ *               rank without tokens.  t and dw_t: GC_BF16 or GC_FP32 each.
+ *   scratch     DEVICE, 256-byte aligned, gc_embedding_backward_scratch_bytes();
+ *               calls that may run at once need one each.
+ * Limits as gc_embedding; outputs and scratch must not overlap anything else.
+ */
+gc_status gc_embedding_backward(const void* const* dout, const int32_t* const* tokens, const int64_t* ntokens,
+                                int nranks, size_t vocab, size_t hidden, float scale, gc_dtype t,
+                                void* const* dweight, gc_dtype dw_t, int accumulate, void* scratch,
+                                size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Dropout of each rank's counts[r] elements with the residual's addition:
+ *   y[i] = residual[i] + (keep(i) ? x[i] * 65536 / (65536 - d) : 0),  d = p * 65536
+ * rounded to an integer: p counts in steps of 2^-16.  The product and the sum
+ * are fp32, the result is rounded once to t.  A dropped value counts as 0,
+ * whatever it is.  Without residual (NULL) this is plain dropout; its gradient is
+ * the same call on the gradient of y (and residual's gradient is that itself).
+ *
+ * keep(i) is never stored: with the Philox4x32-10 generator (Salmon et al., SC
+ * 2011), key (seed's low, high word) and counter (b's low word, b's high word +
+ * 256 * rank, s's low, high word), b = i / 8, s = offset + *step, element i takes
+ * half word i % 8 of the four result words (low halves first) and is kept where
+ * that is at least d.  Ranks have masks of their own; calls that shall differ
+ * (layers, steps) take different offsets or steps.
+ *   step      DEVICE pointer to one uint64 read when the kernel runs, or NULL for
+ *             0: a replayed graph gets new masks by adding to it in between.
+ *   y[r]      may be x[r] or residual[r] itself; no other overlap.
+ *   0 <= p <= 1.  t is GC_BF16 or GC_FP32.
+ */
+gc_status gc_dropout(const void* const* x, const void* const* residual, const int64_t* counts, int nranks, float p,
+                     uint64_t seed, uint64_t offset, const uint64_t* step, gc_dtype t, void* const* y,
+                     hipStream_t stream);
+
+/*
+ * Scratch bytes gc_token_logprob needs (0 if the sizes are invalid).
+ */
+size_t gc_token_logprob_scratch_bytes(const int64_t* ntokens, int nranks, size_t vocab, int top);
+
+/*
+ * Log probabilities of given tokens.  Per row, with z = scale * logits (scale a
+ * temperature's inverse, > 0):
+ *   lse = log(sum of e^z),  p = e^(z - lse),
+ *   logprob = z[target] - lse,  entropy = -sum of p * log(p),
+ *   and the `top` largest logits: their tokens and log probabilities, in
+ *   descending order, equal values by ascending token.
+ * Sums are fp32.
+ *   logits[r]   DEVICE [ntokens[r]] rows of `stride` >= vocab elements of t
+ *               (GC_BF16 or GC_FP32), the first vocab of them read.
+ *   targets[r]  DEVICE int32 [ntokens[r]]; a target outside [0, vocab) is none: its
+ *               logprob is 0 and takes no gradient.
+ *   logprob[r], entropy[r], lse[r]  DEVICE fp32 [ntokens[r]].  entropy and lse may
+ *               be NULL; targets and logprob may be NULL together.
+ *   top         0 to 64, at most vocab; top_ids[r] DEVICE int32 and top_logprob[r]
+ *               DEVICE fp32 [ntokens[r]][top], unused where top is 0.
+ *   dlogprob[r], dentropy[r], dlogits[r]  where the gradients of logprob and
+ *               entropy are known beforehand (a plain loss), the gradient of the
+ *               logits may be written in the same pass: see
+ *               gc_token_logprob_backward.  dlogits needs dlogprob and targets;
+ *               dentropy may be NULL.  All NULL: no gradient.
+ *   scratch     DEVICE, 256-byte aligned, gc_token_logprob_scratch_bytes(); calls
+ *               that may run at once need one each.
+ * Logits of -inf have probability 0.  A row of nothing else has lse and log
+ * probabilities of -inf (its target's too), entropy 0 and a zero gradient.  A NaN
+ * or +inf makes the row's numbers NaN; NaN logits are never alternatives, and
+ * where too few others are left the remaining ids are -1.  Rows of all ranks
+ * below 2^31; outputs and scratch must not overlap anything else, except that
+ * dlogits[r] may be logits[r] itself.
+ */
+gc_status gc_token_logprob(const void* const* logits, const int32_t* const* targets, const int64_t* ntokens,
+                           int nranks, size_t vocab, size_t stride, float scale, gc_dtype t, float* const* logprob,
+                           float* const* entropy, float* const* lse, int top, int32_t* const* top_ids,
+                           float* const* top_logprob, const float* const* dlogprob, const float* const* dentropy,
+                           void* const* dlogits, void* scratch, size_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Gradient of the logits from the saved lse (and entropy, where dentropy is given):
+ *   dlogits = scale * (dlogprob * ([token == target] - p) - dentropy * p * (log(p) + entropy)),
+ * fp32, rounded once to t; columns vocab to stride - 1 get zeros.
+ *   lse[r], entropy[r], dlogprob[r], dentropy[r]  DEVICE fp32 [ntokens[r]];
+ *               dentropy may be NULL, then entropy is not read.
+ *   dlogits[r]  DEVICE rows of stride elements of t; may be logits[r] itself.
+ */
+gc_status gc_token_logprob_backward(const void* const* logits, const int32_t* const* targets, const float* const* lse,
+                                    const float* const* entropy, const float* const* dlogprob,
+                                    const float* const* dentropy, const int64_t* ntokens, int nranks, size_t vocab,
+                                    size_t stride, float scale, gc_dtype t, void* const* dlogits, hipStream_t stream);
+
+/*
  * Bucket plan: DDP gradient buckets (AIG6 §6.2.4; NXMR §5.1) and the FSDP
  * FlatParameter layout (DTLM §4 FSDP1).
  *   Tensors are visited in reverse definition order when `reverse` is nonzero

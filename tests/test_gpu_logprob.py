@@ -1,0 +1,242 @@
+"""GPU parity of the log probabilities, entropy, alternatives and gradient with the 64-bit
+oracle, against bounds counted from the roundings (u = 2^-24 per fp32 operation)."""
+
+import numpy as np
+import pytest
+import torch
+
+import collective_communication_reduction_amd as gc
+from oracle import token as K
+from tests.gpu_util import DEV
+from tests.test_gpu_embed import HALF, TYPES, U, _f64, guarded, untouched
+
+pytestmark = pytest.mark.gpu
+NINF = float("-inf")
+
+
+def _logits(rng, shape, dtype, kind, V):
+    x = rng.normal(size=shape) * 3
+    if kind == "banned":
+        x[rng.random(shape) < 0.5] = -np.inf
+    elif kind == "few":                                        # all but three banned, one row with nothing left
+        keep = rng.integers(0, V, (shape[0], 3))
+        y = np.full(shape, -np.inf)
+        np.put_along_axis(y, keep, np.take_along_axis(x, keep, 1), 1)
+        if shape[0] > 1:
+            y[1] = -np.inf
+        x = y
+    elif kind == "ties":
+        x = np.round(x)
+    elif kind == "equal":
+        x[:] = 1.25
+    elif kind == "rising":
+        x = np.sort(x, axis=1)
+    elif kind == "far":                                        # one value far above the rest, large magnitudes
+        x = x * 40 - 500
+        x[:, V // 3] = 300
+    return torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
+
+
+def _bounds(x, lp, scale, V):
+    """Error bounds per row of log S and of the entropy, from the sums' terms."""
+    p = np.exp(lp)
+    m = np.max(np.where(np.isneginf(x), -1e300, x), axis=1, keepdims=True) * scale
+    d = np.where(p > 0, np.abs(x * scale - m), 0.0)
+    q1, q2 = (p * d).sum(1), (p * d * d).sum(1)
+    # additions one after the other: a lane's at most V / 256 + 8, then the lanes' 40; every raise of the running
+    # maximum multiplies once more (at most one in 8 values, and 30 in the joins); three roundings in each exponent
+    # and three more where it is raised; the exponential's own error 2 u
+    adds = V / 256 + 48 + 4 * (V / 2048 + 30) + 8
+    rel_s = 2 * U * (adds + 6 * q1)
+    rel_u = 2 * U * (adds * q1 + 6 * q2 + 6 * q1)
+    return rel_s, rel_u + rel_s * (1 + q1)
+
+
+ROWS = [
+    # ranks' rows, vocabulary, padding columns, type, element offset
+    ([1], 1, 0, "fp32", 0), ([1], 2, 0, "bf16", 0), ([3, 0, 2], 8, 0, "bf16", 0), ([2], 65, 0, "bf16", 0), ([4], 1003, 0, "fp32", 0),
+    ([4], 1003, 5, "bf16", 1), ([5, 1], 4096, 0, "bf16", 0), ([2], 8192, 64, "fp32", 0), ([3], 32003, 61, "fp32", 0),
+    ([2], 32000, 0, "bf16", 0), ([1], 131072, 0, "bf16", 0), ([1, 1], 131075, 0, "bf16", 3), ([1], 140001, 7, "fp32", 0),
+    ([1], 300007, 0, "bf16", 0), ([40], 515, 0, "bf16", 0), ([1 + s % 2 for s in range(64)], 300, 4, "bf16", 0),
+]
+KINDS = ["normal", "banned", "few", "ties", "equal", "rising", "far"]
+
+
+@pytest.mark.parametrize("rows,V,pad,dtype,offset", ROWS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_token_logprob(rows, V, pad, dtype, offset, kind):
+    if kind not in ("normal", "few") and len(rows) > 60:
+        pytest.skip("one pass over the ranks is enough")
+    rng = np.random.default_rng(V + len(rows) + len(kind))
+    S, top = V + pad, min(V, 20 if V % 2 else 5)
+    scale = 1.0 if V % 3 else 0.75
+    s32 = np.float64(np.float32(scale))
+    x, x64, targets, tg = [], [], [], []
+    for n in rows:
+        v = _logits(rng, (n, S), dtype, kind, V)
+        full = torch.zeros(offset + n * S, dtype=v.dtype, device=DEV)
+        view = full[offset:].view(n, S)
+        view.copy_(v)
+        if pad:
+            view[:, V:] = float("nan")                         # padding columns are not read
+        x.append(view)
+        x64.append(_f64(view[:, :V]))
+        t = rng.integers(0, V, n).astype(np.int32)
+        if n > 2:
+            t[0], t[2] = -1, V
+        targets.append(t)
+        tg.append(torch.from_numpy(t).to(DEV))
+    f = lambda *w: [guarded((n, *w), torch.float32) for n in rows]  # noqa: E731
+    logprob, entropy, lse, tlp = f(), f(), f(), f(top)
+    ids = [guarded((n, top), torch.int32) for n in rows]
+    a = [torch.from_numpy(rng.normal(size=n).astype(np.float32)).to(DEV) for n in rows]
+    b = [torch.from_numpy(rng.normal(size=n).astype(np.float32)).to(DEV) for n in rows]
+    grads = [guarded((n, S), TYPES[dtype], offset) for n in rows]
+    views = lambda g: [v[1] for v in g]  # noqa: E731
+    scratch = torch.full((gc.gc_token_logprob_scratch_bytes(rows, V, top) + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    common = dict(targets=tg, stride=S, scale=scale)
+    gc.gc_token_logprob(x, rows, V, scratch[:-256], logprob=views(logprob), entropy=views(entropy), lse=views(lse), top=top,
+                        top_ids=views(ids), top_logprob=views(tlp), **common)
+    assert (scratch[-256:] == 0xA5).all()
+    # the same with the gradient in the same pass, without alternatives
+    lp2, lse2, e2 = ([torch.empty(n, device=DEV) for n in rows] for _ in range(3))
+    need = gc.gc_token_logprob_scratch_bytes(rows, V, 0)
+    gc.gc_token_logprob(x, rows, V, scratch[:need], logprob=lp2, lse=lse2, entropy=e2, dlogprob=a, dentropy=b,
+                        dlogits=views(grads), scratch_bytes=need, **common)
+    later = [guarded((n, S), TYPES[dtype], offset) for n in rows]
+    gc.gc_token_logprob_backward(x, rows, V, lse2, dlogprob=a, dlogits=views(later), entropy=e2, dentropy=b, **common)
+    plain = [guarded((n, S), TYPES[dtype], offset) for n in rows]
+    gc.gc_token_logprob_backward(x, rows, V, lse2, dlogprob=a, dlogits=views(plain), **common)
+    for r, n in enumerate(rows):
+        if not n:
+            continue
+        lp, want_lse = K.log_softmax(x64[r], s32)
+        rel_s, abs_h = _bounds(x64[r], lp, s32, V)
+        empty = np.isneginf(want_lse)
+        biggest = np.where(empty, 0.0, np.abs(np.max(np.where(np.isneginf(x64[r]), -1e300, x64[r]), axis=1) * s32))
+
+        def close(got, want, tol):
+            got = _f64(got)
+            same = (got == want) | (np.isnan(got) & np.isnan(want))
+            with np.errstate(invalid="ignore"):
+                return (same | (np.abs(got - want) <= tol)).all()
+        with np.errstate(invalid="ignore"):
+            lg = np.abs(np.where(empty, 0.0, want_lse))
+            tol_lse = rel_s + 4 * U * (lg + 2 * biggest + 1)
+            want_lp = K.token_logprob(lp, targets[r])
+            tol_lp = np.where(np.isinf(want_lp), 0.0, rel_s + 6 * U * (np.abs(want_lp) + lg + biggest + 1))
+            want_h = K.entropy(lp)
+            tol_h = abs_h + 8 * U * (1 + np.abs(want_h) + lg)
+            for got in (lse[r][1], lse2[r]):
+                assert close(got, want_lse, tol_lse), r
+            for got in (logprob[r][1], lp2[r]):
+                assert close(got, want_lp, tol_lp), r
+            for got in (entropy[r][1], e2[r]):
+                assert close(got, want_h, tol_h), (r, np.abs(_f64(got) - want_h).max(), tol_h.min())
+        want_ids, want_tlp = K.alternatives(x64[r], lp, top)
+        assert np.array_equal(ids[r][1].cpu().numpy(), want_ids), r
+        with np.errstate(invalid="ignore"):
+            tol_t = np.where(np.isinf(want_tlp), 0.0, (rel_s + 6 * U * (lg + biggest + 1))[:, None] + 6 * U * np.abs(want_tlp))
+        assert close(tlp[r][1], want_tlp, tol_t), r
+        # gradients: of the exact lse for the joint pass, of the lse given for the later one
+        for got, base, ent, own in ((grads[r][1], want_lse, want_h, True), (later[r][1], _f64(lse2[r]), _f64(e2[r]), False),
+                                    (plain[r][1], _f64(lse2[r]), None, False)):
+            da, db = _f64(a[r]), None if ent is None else _f64(b[r])
+            want = K.token_logprob_backward(x64[r], targets[r], base, da, s32, ent, db)
+            with np.errstate(invalid="ignore", over="ignore"):
+                d = np.where(np.isneginf(x64[r]) | empty[:, None], 0.0, x64[r] * s32 - np.where(empty, 0.0, base)[:, None])
+                p = np.where(np.isneginf(x64[r]) | empty[:, None], 0.0, np.exp(d))
+                rel_p = (rel_s[:, None] if own else 0) + U * (8 + 4 * np.abs(d) + (4 * (lg + biggest)[:, None] if own else 0))
+                err = np.abs(da)[:, None] * (p * rel_p + 3 * U * (1 + p))
+                if db is not None:
+                    h = np.abs(d) + np.abs(ent)[:, None]
+                    err = err + np.abs(db)[:, None] * p * (h * (rel_p + 4 * U) + rel_p + (abs_h[:, None] + tol_h[:, None] if own else 0))
+                tol = s32 * err + (HALF[dtype] + 4 * U) * np.abs(want) * (1 + 2 ** -8) + 1e-37
+            g = _f64(got)
+            assert (np.abs(g[:, :V] - want) <= tol).all(), (r, own, np.abs(g[:, :V] - want).max())
+            assert (g[:, V:] == 0).all()
+    for lists, off in (((logprob, entropy, lse, tlp, ids), 0), ((grads, later, plain), offset)):
+        assert all(untouched(full, off, view.numel()) for pairs in lists for full, view in pairs)
+
+
+@pytest.mark.parametrize("V,top", [(700, 64), (32000, 64), (5, 5), (40000, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_many_alternatives(V, top, dtype, rows):
+    rng = np.random.default_rng(V + top)
+    for kind in KINDS:
+        x = _logits(rng, (rows, V), dtype, kind, V).to(DEV)
+        ids, tlp = torch.empty(rows, top, dtype=torch.int32, device=DEV), torch.empty(rows, top, device=DEV)
+        scratch = torch.empty(gc.gc_token_logprob_scratch_bytes([rows], V, top), dtype=torch.uint8, device=DEV)
+        gc.gc_token_logprob([x], [rows], V, scratch, top=top, top_ids=[ids], top_logprob=[tlp])
+        want, _ = K.alternatives(_f64(x), K.log_softmax(_f64(x))[0], top)
+        assert np.array_equal(ids.cpu().numpy(), want), kind
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [9, 5000, 70001])
+def test_nan_and_infinities(dtype, V):
+    """A NaN or +inf makes its own row's numbers NaN and no other's; NaN logits are never alternatives."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.normal(size=(5, V)).astype(np.float32)).to(TYPES[dtype]).to(DEV)
+    x[1, V // 2], x[2, V - 1], x[3] = float("nan"), float("inf"), float("nan")
+    x[3, 4] = 1.0
+    n, top = 5, 4
+    lp, h, lse, tlp = (torch.empty(n, *w, device=DEV) for w in ((), (), (), (top,)))
+    ids = torch.empty(n, top, dtype=torch.int32, device=DEV)
+    dx = torch.empty_like(x)
+    tg, one = torch.zeros(n, dtype=torch.int32, device=DEV), torch.ones(n, device=DEV)
+    scratch = torch.empty(gc.gc_token_logprob_scratch_bytes([n], V, top), dtype=torch.uint8, device=DEV)
+    gc.gc_token_logprob([x], [n], V, scratch, targets=[tg], logprob=[lp], entropy=[h], lse=[lse], top=top, top_ids=[ids],
+                        top_logprob=[tlp], dlogprob=[one], dlogits=[dx])
+    for t in (lp, h, tlp[:, 0], dx[:, 0].float()):
+        assert t[1:4].isnan().all() and t[[0, 4]].isfinite().all()
+    assert lse[[1, 3]].isnan().all() and lse[[0, 4]].isfinite().all()
+    want, _ = K.alternatives(_f64(x), np.zeros((n, V)), top)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    assert ids[3].tolist() == [4, -1, -1, -1] and ids[2, 0] == V - 1
+    back = torch.empty_like(x)
+    gc.gc_token_logprob_backward([x], [n], V, [lse], [tg], [one], [back])
+    assert back[[1, 3]].float().isnan().all() and back[[0, 4]].float().isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 4099), ("fp32", 33000), ("bf16", 140000)])
+def test_gradient_over_the_logits(dtype, V):
+    rng = np.random.default_rng(4)
+    n = [3, 2]
+    x = [_logits(rng, (k, V), dtype, "banned", V).to(DEV) for k in n]
+    tg = [torch.from_numpy(rng.integers(0, V, k).astype(np.int32)).to(DEV) for k in n]
+    w = [torch.full((k,), -0.5, device=DEV) for k in n]
+    f = lambda: [torch.empty(k, device=DEV) for k in n]  # noqa: E731
+    scratch = torch.empty(gc.gc_token_logprob_scratch_bytes(n, V, 0), dtype=torch.uint8, device=DEV)
+    far, lp, lse = [torch.empty_like(t) for t in x], f(), f()
+    gc.gc_token_logprob(x, n, V, scratch, targets=tg, logprob=lp, lse=lse, dlogprob=w, dlogits=far)
+    over, lp2 = [t.clone() for t in x], f()
+    gc.gc_token_logprob(over, n, V, scratch, targets=tg, logprob=lp2, dlogprob=w, dlogits=over)
+    assert all(torch.equal(p, q) for p, q in zip(far + lp, over + lp2))
+    later = [torch.empty_like(t) for t in x]
+    gc.gc_token_logprob_backward(x, n, V, lse, tg, w, later)
+    over = [t.clone() for t in x]
+    gc.gc_token_logprob_backward(over, n, V, lse, tg, w, over)
+    assert all(torch.equal(p, q) for p, q in zip(later, over))
+
+
+def test_gradient_against_differences():
+    """Central differences of sum(a * logprob + b * entropy) in 64 bits around fp32 logits."""
+    rng = np.random.default_rng(6)
+    n, V, scale = 4, 301, 1.25
+    x = torch.from_numpy(rng.normal(size=(n, V)).astype(np.float32)).to(DEV)
+    tg = torch.from_numpy(rng.integers(0, V, n).astype(np.int32)).to(DEV)
+    a, b = (torch.from_numpy(rng.normal(size=n).astype(np.float32)).to(DEV) for _ in range(2))
+    lp, dx = torch.empty(n, device=DEV), torch.empty(n, V, device=DEV)
+    scratch = torch.empty(gc.gc_token_logprob_scratch_bytes([n], V, 0), dtype=torch.uint8, device=DEV)
+    gc.gc_token_logprob([x], [n], V, scratch, targets=[tg], logprob=[lp], dlogprob=[a], dentropy=[b], dlogits=[dx], scale=scale)
+
+    def loss(v):
+        p, _ = K.log_softmax(v, scale)
+        return (_f64(a) * K.token_logprob(p, tg.cpu().numpy()) + _f64(b) * K.entropy(p)).sum()
+    for _ in range(4):
+        v, h = rng.normal(size=(n, V)), 1e-5
+        want = (loss(_f64(x) + h * v) - loss(_f64(x) - h * v)) / (2 * h)
+        # third-order term of the differences below 1e-8; the gradient's own error as in test_token_logprob, about 1e-5 of its norm
+        assert abs(want - (_f64(dx) * v).sum()) <= 1e-7 + 1e-5 * np.abs(_f64(dx) * v).sum()
