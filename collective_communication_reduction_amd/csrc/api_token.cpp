@@ -58,10 +58,11 @@ extern "C" gc_status gc_embedding(const void* const* weight, const int32_t* cons
 // make over 256 pieces: every piece reads the counts of all the others.
 gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden) {
   gci::EmbeddingGeom g;
-  (void)hidden;
   int64_t most = 0;
+  uint64_t runs = 0;
   for (int r = 0; r < nranks; ++r) {
     g.tokens += tokens[r];
+    runs += static_cast<uint64_t>(tokens[r] + kEmbeddingRun - 1) / kEmbeddingRun;
     most = std::max(most, tokens[r]);
   }
   g.chunk = static_cast<int32_t>(std::max<int64_t>(1024, (most / 256 + 511) / 512 * 512));
@@ -74,7 +75,9 @@ gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64
   g.perm = g.keys + up256(n * 4);
   g.counts = g.perm + up256(n * 4);
   g.valid = g.counts + up256(static_cast<uint64_t>(g.chunks) * 4 << g.low_bits);
-  g.bytes = g.valid + up256(static_cast<uint64_t>(nranks) * 4);
+  g.present = g.valid + up256(static_cast<uint64_t>(nranks) * 4);
+  g.partial = g.present + up256(nranks * vocab);
+  g.bytes = g.partial + up256(runs * 2 * embedding_pitch(hidden) * 4);
   return g;
 }
 

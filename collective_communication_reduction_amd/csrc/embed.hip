@@ -83,6 +83,7 @@ struct SortArgs {
   int32_t* perm;
   uint32_t* counts;       // [chunks][1 << bits]
   int32_t* valid;         // tokens of each rank inside the vocabulary
+  uint8_t* present;       // [ranks][vocab] whether a token occurs
 };
 
 // Entry i of the pass's input as id << 32 | token; ~0 for a token outside the vocabulary.
@@ -111,6 +112,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   const int64_t n = FIRST ? a.tok[rank] : a.valid[rank];
   const int64_t first = static_cast<int64_t>(block - a.tile0[rank]) * a.chunk;
   const int bins = 1 << a.bits;
+  if constexpr (FIRST) {  // the rank's map is cleared here and set by the placing kernel behind
+    const int32_t mine = block - a.tile0[rank], chunks = a.tile0[rank + 1] - a.tile0[rank];
+    uint8_t* map = a.present + static_cast<uint64_t>(rank) * a.vocab;
+    for (uint32_t v = mine * kSortThreads + threadIdx.x; v < a.vocab; v += chunks * kSortThreads) map[v] = 0;
+  }
   for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < a.chunk; i += kSortThreads) {
@@ -206,6 +212,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (ok) {
+      if constexpr (FIRST) a.present[static_cast<uint64_t>(rank) * a.vocab + (e >> 32)] = 1;
       if constexpr (LAST) {
         a.keys[a.at[rank] + place] = static_cast<int32_t>(e >> 32);
         a.perm[a.at[rank] + place] = static_cast<int32_t>(e);
@@ -217,30 +224,47 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
 }
 
 // ------------------------------------------------------------- sums of sorted rows
+//
+// The sorted tokens are cut into runs of kRun, whatever rows they belong to, so
+// that frequent tokens spread over the chip.  A row whose tokens all lie in one run
+// is finished there; what a run holds of a row that began before it, or goes on
+// behind it, is left as a partial sum (head, tail), and the run where the row
+// begins adds the parts up in a second launch.
+
+constexpr int kRun = gci::kEmbeddingRun;
+constexpr int kAhead = 4;      // rows whose loads are in flight together
 
 template <int P>
 struct RowSumArgs {
   const char* dout[P];
   char* dw[P];
   int64_t at[P];
+  int32_t run0[P + 1];   // first run of each rank
   uint32_t block0;
   int32_t N;
-  uint64_t vocab;
+  uint32_t vocab;
   uint64_t H;
   uint64_t units;
+  uint64_t pitch;        // floats of a partial row
+  uint64_t sum_blocks;   // workgroups of the runs; those behind clear rows
+  uint32_t slices;       // of a row, NV << lanes_log2 units each
+  int32_t lanes_log2;
+  uint32_t clear_rows;   // rows per clearing workgroup
   const int32_t* keys;
   const int32_t* perm;
   const int32_t* valid;
+  const uint8_t* present;
+  float* partial;        // [runs][head, tail][pitch]
   float scale;
   bool accumulate;
 };
 
-// First of n sorted keys that is at least v.
-__device__ __forceinline__ int32_t first_key(const int32_t* keys, int32_t n, int32_t v) {
+// First of n sorted keys that is above v.
+__device__ __forceinline__ int32_t past_key(const int32_t* keys, int32_t n, int32_t v) {
   int32_t lo = 0;
   while (n > 0) {
     const int32_t half = n >> 1;
-    if (keys[lo + half] < v) {
+    if (keys[lo + half] <= v) {
       lo += half + 1;
       n -= half + 1;
     } else {
@@ -250,55 +274,159 @@ __device__ __forceinline__ int32_t first_key(const int32_t* keys, int32_t n, int
   return lo;
 }
 
-// VE sums of one unit to the gradient's type, behind what is there already where `add`.
-template <class In, class OutT>
-__device__ __forceinline__ void put_sums(char* row, uint64_t H, uint64_t u, const float (&acc)[In::VE], float scale, bool add) {
-  constexpr int VE = In::VE;
-  if constexpr (std::is_same<In, OutT>::value) {
-    typedef AnyUnit<In> U;
-    float v[VE], old[VE];
-    if (add) U::widen(U::load(row, H, u, 0), old);
+// VE sums of unit u times scale, to a row of H elements of OutT, on top of what is there where `add`.
+template <class OutT, int VE>
+__device__ __forceinline__ void put_sums(char* row, uint64_t H, uint64_t u, const float (&acc)[VE], float scale, bool add) {
+  typedef typename std::conditional<OutT::ES == 2, OutBf16, OutF32>::type Out;
+  float v[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) v[e] = add ? acc[e] * scale + old[e] : acc[e] * scale;
-    U::store(row, H, u, U::narrow(v));
-  } else {
-    // units of the other type: two fp32 units for one of bf16, half a bf16 unit for one of fp32
-    typedef typename std::conditional<OutT::ES == 2, uint16_t, float>::type E;
-    E* p = reinterpret_cast<E*>(row) + u * VE;
+  for (int e = 0; e < VE; ++e) v[e] = acc[e] * scale;
+  char* p = row + u * VE * OutT::ES;
+  if (add)
 #pragma unroll
     for (int e = 0; e < VE; ++e)
-      if (u * VE + e < H) {
-        float v = acc[e] * scale;
-        if (add) v += OutT::one(p, e);
-        if constexpr (OutT::ES == 2) p[e] = static_cast<uint16_t>(bf16_bits(v));
-        else p[e] = v;
-      }
+      if (u * VE + e < H) v[e] += OutT::one(p, e);
+  if ((u + 1) * VE <= H) {
+    put<Out, VE, gci::kStoreDevNT>(p, pack<Out, VE>(v));
+    return;
   }
+  typedef typename std::conditional<OutT::ES == 2, uint16_t, uint32_t>::type E;
+#pragma unroll
+  for (int e = 0; e < VE; ++e)
+    if (u * VE + e < H) reinterpret_cast<E*>(p)[e] = static_cast<E>(OutT::ES == 2 ? bf16_bits(v[e]) : __float_as_uint(v[e]));
 }
 
-template <class In, class OutT, int P>
+template <class In, class OutT, int NV, int P>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
+  __shared__ int2 entries[kThreads / 8 * kRun];   // (id, token) of each group's run; groups have 8 lanes or more
   const uint64_t block = a.block0 + blockIdx.x;
-  const int rank = static_cast<int>(block / a.vocab);
-  const int32_t v = static_cast<int32_t>(block % a.vocab);
-  const int32_t* keys = a.keys + a.at[rank];
-  const int32_t* perm = a.perm + a.at[rank];
-  const int32_t n = a.valid[rank];
-  const int32_t first = first_key(keys, n, v), last = first + first_key(keys + first, n - first, v + 1);
-  if (a.accumulate && first == last) return;
-  char* row = a.dw[rank] + static_cast<uint64_t>(v) * a.H * OutT::ES;
-  for (uint64_t u = threadIdx.x; u < a.units; u += kThreads) {
-    float acc[VE] = {};
-    for (int32_t i = first; i < last; ++i) {
-      float x[VE];
-      U::widen(U::load(a.dout[rank] + static_cast<uint64_t>(perm[i]) * a.H * In::ES, a.H, u, 0), x);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) acc[e] += x[e];
+  if (block >= a.sum_blocks) {
+    // rows without a token
+    const uint64_t first = (block - a.sum_blocks) * a.clear_rows;
+    const uint64_t last = min(first + a.clear_rows, static_cast<uint64_t>(a.N) * a.vocab);
+    typedef AnyUnit<OutT> W;
+    const uint64_t units = (a.H + W::VE - 1) / W::VE;
+    for (uint64_t r = first; r < last; ++r) {
+      if (a.present[r]) continue;
+      char* row = a.dw[r / a.vocab] + r % a.vocab * a.H * OutT::ES;
+      for (uint64_t u = threadIdx.x; u < units; u += kThreads) W::store(row, a.H, u, u32x4{0, 0, 0, 0});
     }
-    put_sums<In, OutT>(row, a.H, u, acc, a.scale, a.accumulate);
+    return;
   }
+  const uint64_t q = (block * kThreads + threadIdx.x) >> a.lanes_log2;
+  const uint32_t run = static_cast<uint32_t>(a.slices == 1 ? q : q / a.slices);
+  const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  int2* mine = entries + (threadIdx.x >> a.lanes_log2) * kRun;
+  const bool real = run < static_cast<uint32_t>(a.run0[a.N]);
+  const int rank = real ? rank_of<P>(a.run0, a.N, static_cast<int32_t>(run)) : 0;
+  const int32_t* keys = a.keys + a.at[rank];
+  const int32_t n = a.valid[rank];
+  const int64_t first = real ? static_cast<int64_t>(run - a.run0[rank]) * kRun : n;
+  const int count = static_cast<int>(max(static_cast<int64_t>(0), min<int64_t>(kRun, n - first)));
+  for (int i = lane; i < count; i += lanes) mine[i] = int2{keys[first + i], a.perm[a.at[rank] + first + i]};
+  __syncthreads();
+  if (count == 0) return;
+  const uint64_t u0 = (q - static_cast<uint64_t>(run) * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + lane;
+  int32_t cur = mine[0].x;
+  bool began = first == 0 || keys[first - 1] != cur;      // the current row begins in this run
+  const bool goes_on = first + count < n && keys[first + count] == mine[count - 1].x;
+  const char* dout = a.dout[rank];
+  const uint64_t row_bytes = a.H * In::ES;
+  float acc[NV][VE] = {};
+  const auto flush = [&](bool ended) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint64_t u = u0 + (static_cast<uint64_t>(j) << a.lanes_log2);
+      if (u >= a.units) continue;
+      if (began && ended) {
+        put_sums<OutT, VE>(a.dw[rank] + static_cast<uint64_t>(cur) * a.H * OutT::ES, a.H, u, acc[j], a.scale, a.accumulate);
+      } else {
+        float* p = a.partial + (2 * static_cast<uint64_t>(run) + (began ? 1 : 0)) * a.pitch + u * VE;
+#pragma unroll
+        for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(p + e) = float4{acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]};
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) acc[j][e] = 0.0f;
+    }
+  };
+  for (int i = 0; i < count; i += kAhead) {
+    u32x4 x[kAhead][NV];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const char* row = dout + static_cast<uint64_t>(static_cast<uint32_t>(mine[min(i + k, count - 1)].y)) * row_bytes;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) x[k][j] = U::load(row, a.H, u0 + (static_cast<uint64_t>(j) << a.lanes_log2), 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k >= count) break;
+      const int32_t key = mine[i + k].x;
+      if (key != cur) {
+        flush(true);
+        cur = key;
+        began = true;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[VE];
+        U::widen(x[k][j], v);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[j][e] += v[e];
+      }
+    }
+  }
+  flush(!goes_on);
+}
+
+// Adds up the parts of the row that begins in run `blockIdx.x` and goes on behind
+// it: four groups of 256 lanes take every fourth part (four columns each), and
+// their sums are added in order.
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinGroups = kJoinThreads / 256;
+
+template <class OutT, int P>
+__global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs<P> a) {
+  __shared__ float4 sums[kJoinGroups - 1][256];
+  const uint64_t block = a.block0 + blockIdx.x;
+  const uint32_t run = static_cast<uint32_t>(block / a.slices);
+  const int rank = rank_of<P>(a.run0, a.N, static_cast<int32_t>(run));
+  const int32_t* keys = a.keys + a.at[rank];
+  const int32_t n = a.valid[rank];
+  const int64_t first = static_cast<int64_t>(run - a.run0[rank]) * kRun, end = first + kRun;
+  if (end >= n) return;
+  const int32_t key = keys[end - 1];
+  if (keys[end] != key || (first > 0 && keys[first - 1] == key)) return;
+  const int64_t last = end + past_key(keys + end, static_cast<int32_t>(n - end), key) - 1;   // the row's last token
+  const int parts = static_cast<int>(last / kRun - first / kRun) + 1;
+  const int group = threadIdx.x / 256, lane = threadIdx.x % 256;
+  const uint64_t u = (block - static_cast<uint64_t>(run) * a.slices) * 256 + lane;
+  float4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+  if (u * 4 < a.pitch) {
+    const float* p = a.partial + 2 * static_cast<uint64_t>(run) * a.pitch + u * 4;   // part i: the head of run + i; part 0: its own tail
+#pragma unroll 8
+    for (int i = group; i < parts; i += kJoinGroups) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (2 * static_cast<uint64_t>(i) + (i == 0 ? 1 : 0)) * a.pitch);
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  }
+  if (group > 0) sums[group - 1][lane] = acc;
+  __syncthreads();
+  if (group > 0 || u * 4 >= a.H) return;
+  float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int g = 0; g < kJoinGroups - 1; ++g) {
+    const float4 t = sums[g][lane];
+    v[0] += t.x;
+    v[1] += t.y;
+    v[2] += t.z;
+    v[3] += t.w;
+  }
+  put_sums<OutT, 4>(a.dw[rank] + static_cast<uint64_t>(key) * a.H * OutT::ES, a.H, u, v, a.scale, a.accumulate);
 }
 
 // ------------------------------------------------------------- host side
@@ -344,6 +472,20 @@ gc_status sort_pass(SortArgs<P>& a, const gci::EmbeddingGeom& g, hipStream_t str
   return s != GC_OK ? s : go(reinterpret_cast<const void*>(sort_place_kernel<FIRST, LAST, P>), kSortWaves * bins * 4);
 }
 
+template <class In, class OutT, int NV, int P>
+gc_status row_sums(RowSumArgs<P>& r, hipStream_t stream) {
+  const uint64_t per = static_cast<uint64_t>(NV) << r.lanes_log2, runs = r.run0[r.N];
+  r.slices = static_cast<uint32_t>((r.units + per - 1) / per);
+  r.sum_blocks = ((runs * r.slices << r.lanes_log2) + kThreads - 1) / kThreads;
+  const uint64_t row = r.H * OutT::ES, rows = static_cast<uint64_t>(r.N) * r.vocab;
+  r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, (64 << 10) / row));
+  const uint64_t clear = r.accumulate ? 0 : (rows + r.clear_rows - 1) / r.clear_rows;
+  gc_status st = launch_blocks(row_sum_kernel<In, OutT, NV, P>, r, r.sum_blocks + clear, kThreads, stream);
+  if (st != GC_OK) return st;
+  r.slices = static_cast<uint32_t>((r.pitch / 4 + 255) / 256);
+  return launch_blocks(row_join_kernel<OutT, P>, r, runs * r.slices, kJoinThreads, stream);
+}
+
 template <class In, class OutT, int P>
 gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   const gci::EmbeddingGeom& g = c.geom;
@@ -361,14 +503,17 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
     s.tile0[k + 1] = s.tile0[k] + std::max<int32_t>(1, static_cast<int32_t>((c.tokens[k] + g.chunk - 1) / g.chunk));
   }
   for (int k = c.nranks; k < P; ++k) s.tile0[k + 1] = s.tile0[k];
+  fill_blocks<P>(r.run0, c.tokens, c.nranks, kRun);
   s.N = r.N = c.nranks;
   s.chunk = g.chunk;
-  s.vocab = static_cast<uint32_t>(c.vocab);
+  s.vocab = r.vocab = static_cast<uint32_t>(c.vocab);
   s.pairs = reinterpret_cast<uint64_t*>(scratch + g.pairs);
   r.keys = s.keys = reinterpret_cast<int32_t*>(scratch + g.keys);
   r.perm = s.perm = reinterpret_cast<int32_t*>(scratch + g.perm);
   s.counts = reinterpret_cast<uint32_t*>(scratch + g.counts);
   r.valid = s.valid = reinterpret_cast<int32_t*>(scratch + g.valid);
+  r.present = s.present = reinterpret_cast<uint8_t*>(scratch + g.present);
+  r.partial = reinterpret_cast<float*>(scratch + g.partial);
   s.bits = g.low_bits;
   gc_status st;
   if (g.low_bits == g.bits) {
@@ -381,12 +526,14 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
     st = sort_pass<false, true, P>(s, g, c.stream);
   }
   if (st != GC_OK) return st;
-  r.vocab = c.vocab;
   r.H = c.hidden;
   r.units = (c.hidden + In::VE - 1) / In::VE;
+  r.pitch = gci::embedding_pitch(c.hidden);
   r.scale = c.scale;
   r.accumulate = c.accumulate;
-  return launch_blocks(row_sum_kernel<In, OutT, P>, r, c.nranks * c.vocab, kThreads, c.stream);
+  r.lanes_log2 = 3;
+  while (r.lanes_log2 < 8 && (uint64_t(1) << r.lanes_log2) < r.units) ++r.lanes_log2;
+  return r.units > kThreads ? row_sums<In, OutT, 2, P>(r, c.stream) : row_sums<In, OutT, 1, P>(r, c.stream);
 }
 
 template <class In, class OutT>
