@@ -11,7 +11,7 @@ namespace {
 
 using namespace gca;
 
-constexpr size_t kMaxVocab = size_t(1) << 22;   // of an embedding: two digits of at most 11 bits
+constexpr size_t kMaxVocab = size_t(1) << 22;   // of an embedding: two digits of gci::kEmbeddingDigit bits
 constexpr int kMaxTop = 64;
 
 gc_status check_row_type(gc_dtype t) {
@@ -59,24 +59,27 @@ extern "C" gc_status gc_embedding(const void* const* weight, const int32_t* cons
 gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden) {
   gci::EmbeddingGeom g;
   int64_t most = 0;
-  uint64_t runs = 0;
   for (int r = 0; r < nranks; ++r) {
     g.tokens += tokens[r];
-    runs += static_cast<uint64_t>(tokens[r] + kEmbeddingRun - 1) / kEmbeddingRun;
     most = std::max(most, tokens[r]);
   }
   g.chunk = static_cast<int32_t>(std::max<int64_t>(1024, (most / 256 + 511) / 512 * 512));
   for (int r = 0; r < nranks; ++r) g.chunks += static_cast<int32_t>(std::max<int64_t>(1, (tokens[r] + g.chunk - 1) / g.chunk));
   g.bits = 1;
   while (vocab > uint64_t(1) << g.bits) ++g.bits;
-  g.low_bits = g.bits <= 11 ? g.bits : (g.bits + 1) / 2;
+  g.low_bits = g.bits <= kEmbeddingDigit ? g.bits : (g.bits + 1) / 2;
+  g.run = 8;
+  while (g.run < 64 && g.tokens / g.run >= 1024) g.run *= 2;
+  uint64_t runs = 0;
+  for (int r = 0; r < nranks; ++r) runs += static_cast<uint64_t>(tokens[r] + g.run - 1) / g.run;
   const uint64_t n = static_cast<uint64_t>(g.tokens);
   g.keys = g.pairs + (g.low_bits < g.bits ? up256(n * 8) : 0);
   g.perm = g.keys + up256(n * 4);
   g.counts = g.perm + up256(n * 4);
   g.valid = g.counts + up256(static_cast<uint64_t>(g.chunks) * 4 << g.low_bits);
   g.present = g.valid + up256(static_cast<uint64_t>(nranks) * 4);
-  g.partial = g.present + up256(nranks * vocab);
+  g.long_rows = g.present + up256(nranks * vocab);
+  g.partial = g.long_rows + up256((runs + 1) * 4);
   g.bytes = g.partial + up256(runs * 2 * embedding_pitch(hidden) * 4);
   return g;
 }

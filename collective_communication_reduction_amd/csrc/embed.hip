@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingArgs
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kSortRun = (1 << gci::kEmbeddingDigit) / kSortThreads;   // digits per thread
 
 template <int P>
 struct SortArgs {
@@ -84,6 +85,7 @@ struct SortArgs {
   uint32_t* counts;       // [chunks][1 << bits]
   int32_t* valid;         // tokens of each rank inside the vocabulary
   uint8_t* present;       // [ranks][vocab] whether a token occurs
+  int32_t* long_rows;     // count, then the runs where rows of many runs begin
 };
 
 // Entry i of the pass's input as id << 32 | token; ~0 for a token outside the vocabulary.
@@ -116,6 +118,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
     const int32_t mine = block - a.tile0[rank], chunks = a.tile0[rank + 1] - a.tile0[rank];
     uint8_t* map = a.present + static_cast<uint64_t>(rank) * a.vocab;
     for (uint32_t v = mine * kSortThreads + threadIdx.x; v < a.vocab; v += chunks * kSortThreads) map[v] = 0;
+    if (block == 0 && threadIdx.x == 0) a.long_rows[0] = 0;
   }
   for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d] = 0;
   __syncthreads();
@@ -169,29 +172,36 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
     if (e != ~uint64_t(0)) atomicAdd(&my[digit_of(a, e)], 1u);
   }
   __syncthreads();
-  // digits in order, a run of them per thread
+  // digits in order, up to four of them per thread: entries of all chunks, and of those before this one
   const int run = (bins + kSortThreads - 1) / kSortThreads;
   const uint32_t* counts = a.counts + static_cast<uint64_t>(a.tile0[rank]) * bins;
-  const int d0 = min(static_cast<int>(threadIdx.x) * run, bins), d1 = min(d0 + run, bins);
-  uint32_t sum = 0;
-  for (int d = d0; d < d1; ++d)
-    for (int c = 0; c < chunks; ++c) sum += counts[static_cast<uint64_t>(c) * bins + d];
+  const int d0 = threadIdx.x * run;
+  uint32_t all[kSortRun] = {}, before[kSortRun] = {}, sum = 0;
+#pragma unroll
+  for (int k = 0; k < kSortRun; ++k) {
+    if (k >= run || d0 + k >= bins) break;
+#pragma unroll 8
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t t = counts[static_cast<uint64_t>(c) * bins + d0 + k];
+      all[k] += t;
+      before[k] += c < mine ? t : 0;
+    }
+    sum += all[k];
+  }
   uint32_t total;
   uint32_t at = block_exclusive(sum, sums, total);
-  for (int d = d0; d < d1; ++d) {
-    uint32_t before = 0, all = 0;
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t k = counts[static_cast<uint64_t>(c) * bins + d];
-      all += k;
-      before += c < mine ? k : 0;
-    }
-    uint32_t place = at + before;
+#pragma unroll
+  for (int k = 0; k < kSortRun; ++k) {
+    const int d = d0 + k;
+    if (k >= run || d >= bins) break;
+    uint32_t place = at + before[k];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t k = next[w * bins + d];
+      const uint32_t t = next[w * bins + d];
       next[w * bins + d] = place;
-      place += k;
+      place += t;
     }
-    at += all;
+    at += all[k];
   }
   if (FIRST && mine == 0 && threadIdx.x == 0) a.valid[rank] = static_cast<int32_t>(total);
   __syncthreads();
@@ -225,13 +235,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
 
 // ------------------------------------------------------------- sums of sorted rows
 //
-// The sorted tokens are cut into runs of kRun, whatever rows they belong to, so
-// that frequent tokens spread over the chip.  A row whose tokens all lie in one run
-// is finished there; what a run holds of a row that began before it, or goes on
-// behind it, is left as a partial sum (head, tail), and the run where the row
-// begins adds the parts up in a second launch.
+// The sorted tokens are cut into runs of equal length, whatever rows they belong
+// to, so that frequent tokens spread over the chip.  The run where a row begins
+// also takes what the next run holds of it, if the row ends there.  Longer rows
+// are left as partial sums, the first of them the tail of the run where the row
+// begins, the others the heads of the runs behind, and a second launch adds them up.
 
-constexpr int kRun = gci::kEmbeddingRun;
 constexpr int kAhead = 4;      // rows whose loads are in flight together
 
 template <int P>
@@ -254,22 +263,19 @@ struct RowSumArgs {
   const int32_t* perm;
   const int32_t* valid;
   const uint8_t* present;
+  int32_t* long_rows;    // count, then the runs where rows of many runs begin
   float* partial;        // [runs][head, tail][pitch]
+  int32_t run;           // sorted tokens per run
   float scale;
   bool accumulate;
 };
 
-// First of n sorted keys that is above v.
-__device__ __forceinline__ int32_t past_key(const int32_t* keys, int32_t n, int32_t v) {
-  int32_t lo = 0;
-  while (n > 0) {
-    const int32_t half = n >> 1;
-    if (keys[lo + half] <= v) {
-      lo += half + 1;
-      n -= half + 1;
-    } else {
-      n = half;
-    }
+// First of the sorted entries lo .. hi - 1 whose id is above key (hi: none).
+__device__ __forceinline__ int past(const int2* entries, int lo, int hi, int32_t key) {
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (entries[mid].x <= key) lo = mid + 1;
+    else hi = mid;
   }
   return lo;
 }
@@ -300,7 +306,7 @@ template <class In, class OutT, int NV, int P>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  __shared__ int2 entries[kThreads / 8 * kRun];   // (id, token) of each group's run; groups have 8 lanes or more
+  extern __shared__ int2 entries[];   // (id, token) of each group's run and the next one
   const uint64_t block = a.block0 + blockIdx.x;
   if (block >= a.sum_blocks) {
     // rows without a token
@@ -318,29 +324,48 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
   const uint64_t q = (block * kThreads + threadIdx.x) >> a.lanes_log2;
   const uint32_t run = static_cast<uint32_t>(a.slices == 1 ? q : q / a.slices);
   const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
-  int2* mine = entries + (threadIdx.x >> a.lanes_log2) * kRun;
+  int2* mine = entries + (threadIdx.x >> a.lanes_log2) * (2 * a.run);
   const bool real = run < static_cast<uint32_t>(a.run0[a.N]);
   const int rank = real ? rank_of<P>(a.run0, a.N, static_cast<int32_t>(run)) : 0;
   const int32_t* keys = a.keys + a.at[rank];
-  const int32_t n = a.valid[rank];
-  const int64_t first = real ? static_cast<int64_t>(run - a.run0[rank]) * kRun : n;
-  const int count = static_cast<int>(max(static_cast<int64_t>(0), min<int64_t>(kRun, n - first)));
-  for (int i = lane; i < count; i += lanes) mine[i] = int2{keys[first + i], a.perm[a.at[rank] + first + i]};
+  const int64_t n = a.valid[rank];
+  const int64_t first = real ? static_cast<int64_t>(run - a.run0[rank]) * a.run : n;
+  const auto entries_from = [&](int64_t at, int most) { return static_cast<int>(max<int64_t>(0, min<int64_t>(most, n - at))); };
+  int count = entries_from(first, a.run);
+  const int staged = entries_from(first, 2 * a.run);
+  for (int i = lane; i < staged; i += lanes) mine[i] = int2{keys[first + i], a.perm[a.at[rank] + first + i]};
+  const auto key_at = [&](int64_t i) { return i >= 0 && i < n ? keys[i] : -1; };
+  // the keys that decide about rows across the run's ends: before it, before the run ahead of it, behind the next run
+  const int32_t key_before = key_at(first - 1), key_ahead = key_at(first - a.run - 1), key_behind = key_at(first + 2 * a.run);
   __syncthreads();
   if (count == 0) return;
-  const uint64_t u0 = (q - static_cast<uint64_t>(run) * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + lane;
   int32_t cur = mine[0].x;
-  bool began = first == 0 || keys[first - 1] != cur;      // the current row begins in this run
-  const bool goes_on = first + count < n && keys[first + count] == mine[count - 1].x;
+  const int32_t last_key = mine[count - 1].x;
+  bool began = key_before != cur;      // the current row begins in this run
+  bool ended = count == staged || mine[count].x != last_key;   // the last row ends in it
+  int i0 = 0;
+  if (!began && key_ahead != cur && (last_key != cur || ended)) {
+    // the first row began in the run ahead and ends here: that run takes it
+    i0 = past(mine, 0, count, cur);
+    if (i0 == count) return;
+    cur = mine[i0].x;
+    began = true;
+  }
+  if (!ended && (began || last_key != cur) && key_behind != last_key) {
+    // the last row begins here and ends in the next run
+    count = past(mine, count, staged, last_key);
+    ended = true;
+  }
+  const uint64_t u0 = (q - static_cast<uint64_t>(run) * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + lane;
   const char* dout = a.dout[rank];
   const uint64_t row_bytes = a.H * In::ES;
   float acc[NV][VE] = {};
-  const auto flush = [&](bool ended) {
+  const auto flush = [&](bool whole) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint64_t u = u0 + (static_cast<uint64_t>(j) << a.lanes_log2);
       if (u >= a.units) continue;
-      if (began && ended) {
+      if (began && whole) {
         put_sums<OutT, VE>(a.dw[rank] + static_cast<uint64_t>(cur) * a.H * OutT::ES, a.H, u, acc[j], a.scale, a.accumulate);
       } else {
         float* p = a.partial + (2 * static_cast<uint64_t>(run) + (began ? 1 : 0)) * a.pitch + u * VE;
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
       for (int e = 0; e < VE; ++e) acc[j][e] = 0.0f;
     }
   };
-  for (int i = 0; i < count; i += kAhead) {
+  for (int i = i0; i < count; i += kAhead) {
     u32x4 x[kAhead][NV];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -377,56 +402,62 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
       }
     }
   }
-  flush(!goes_on);
+  flush(ended);
+  if (began && !ended && u0 == 0) a.long_rows[1 + atomicAdd(&a.long_rows[0], 1)] = static_cast<int32_t>(run);
 }
 
-// Adds up the parts of the row that begins in run `blockIdx.x` and goes on behind
-// it: four groups of 256 lanes take every fourth part (four columns each), and
-// their sums are added in order.
+// Adds up the partial sums of the listed rows, 1024 columns per workgroup: four
+// groups of 256 lanes take every fourth part (four columns a lane), and their sums
+// are added in order.  The list's order does not matter to the results.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinGroups = kJoinThreads / 256;
 
 template <class OutT, int P>
 __global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs<P> a) {
   __shared__ float4 sums[kJoinGroups - 1][256];
-  const uint64_t block = a.block0 + blockIdx.x;
-  const uint32_t run = static_cast<uint32_t>(block / a.slices);
-  const int rank = rank_of<P>(a.run0, a.N, static_cast<int32_t>(run));
-  const int32_t* keys = a.keys + a.at[rank];
-  const int32_t n = a.valid[rank];
-  const int64_t first = static_cast<int64_t>(run - a.run0[rank]) * kRun, end = first + kRun;
-  if (end >= n) return;
-  const int32_t key = keys[end - 1];
-  if (keys[end] != key || (first > 0 && keys[first - 1] == key)) return;
-  const int64_t last = end + past_key(keys + end, static_cast<int32_t>(n - end), key) - 1;   // the row's last token
-  const int parts = static_cast<int>(last / kRun - first / kRun) + 1;
   const int group = threadIdx.x / 256, lane = threadIdx.x % 256;
-  const uint64_t u = (block - static_cast<uint64_t>(run) * a.slices) * 256 + lane;
-  float4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-  if (u * 4 < a.pitch) {
-    const float* p = a.partial + 2 * static_cast<uint64_t>(run) * a.pitch + u * 4;   // part i: the head of run + i; part 0: its own tail
-#pragma unroll 8
-    for (int i = group; i < parts; i += kJoinGroups) {
-      const float4 v = *reinterpret_cast<const float4*>(p + (2 * static_cast<uint64_t>(i) + (i == 0 ? 1 : 0)) * a.pitch);
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+  const uint64_t items = static_cast<uint64_t>(a.long_rows[0]) * a.slices;
+  for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint64_t slot = item / a.slices;
+    const int32_t run = a.long_rows[1 + slot];
+    const int rank = rank_of<P>(a.run0, a.N, run);
+    const int32_t* keys = a.keys + a.at[rank];
+    const int64_t n = a.valid[rank], end = static_cast<int64_t>(run - a.run0[rank] + 1) * a.run;
+    const int32_t key = keys[end - 1];
+    int64_t parts = 1;   // and one more for each run behind that starts in the row
+    for (int more = kJoinThreads; more == kJoinThreads; parts += more) {
+      const int64_t i = end + (parts - 1 + threadIdx.x) * a.run;
+      more = __syncthreads_count(i < n && keys[i] == key);
     }
-  }
-  if (group > 0) sums[group - 1][lane] = acc;
-  __syncthreads();
-  if (group > 0 || u * 4 >= a.H) return;
-  float v[4] = {acc.x, acc.y, acc.z, acc.w};
+    const uint64_t u = (item - slot * a.slices) * 256 + lane;
+    float4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    if (u * 4 < a.pitch) {
+      const float* p = a.partial + 2 * static_cast<uint64_t>(run) * a.pitch + u * 4;
+#pragma unroll 8
+      for (int64_t i = group; i < parts; i += kJoinGroups) {
+        const float4 v = *reinterpret_cast<const float4*>(p + (2 * i + (i == 0 ? 1 : 0)) * a.pitch);
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+    }
+    if (group > 0) sums[group - 1][lane] = acc;
+    __syncthreads();
+    if (group == 0 && u * 4 < a.H) {
+      float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-  for (int g = 0; g < kJoinGroups - 1; ++g) {
-    const float4 t = sums[g][lane];
-    v[0] += t.x;
-    v[1] += t.y;
-    v[2] += t.z;
-    v[3] += t.w;
+      for (int g = 0; g < kJoinGroups - 1; ++g) {
+        const float4 t = sums[g][lane];
+        v[0] += t.x;
+        v[1] += t.y;
+        v[2] += t.z;
+        v[3] += t.w;
+      }
+      put_sums<OutT, 4>(a.dw[rank] + static_cast<uint64_t>(key) * a.H * OutT::ES, a.H, u, v, a.scale, a.accumulate);
+    }
+    __syncthreads();
   }
-  put_sums<OutT, 4>(a.dw[rank] + static_cast<uint64_t>(key) * a.H * OutT::ES, a.H, u, v, a.scale, a.accumulate);
 }
 
 // ------------------------------------------------------------- host side
@@ -473,17 +504,25 @@ gc_status sort_pass(SortArgs<P>& a, const gci::EmbeddingGeom& g, hipStream_t str
 }
 
 template <class In, class OutT, int NV, int P>
-gc_status row_sums(RowSumArgs<P>& r, hipStream_t stream) {
+gc_status row_sums(RowSumArgs<P>& r, bool long_rows, hipStream_t stream) {
   const uint64_t per = static_cast<uint64_t>(NV) << r.lanes_log2, runs = r.run0[r.N];
   r.slices = static_cast<uint32_t>((r.units + per - 1) / per);
   r.sum_blocks = ((runs * r.slices << r.lanes_log2) + kThreads - 1) / kThreads;
   const uint64_t row = r.H * OutT::ES, rows = static_cast<uint64_t>(r.N) * r.vocab;
   r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, (64 << 10) / row));
   const uint64_t clear = r.accumulate ? 0 : (rows + r.clear_rows - 1) / r.clear_rows;
-  gc_status st = launch_blocks(row_sum_kernel<In, OutT, NV, P>, r, r.sum_blocks + clear, kThreads, stream);
-  if (st != GC_OK) return st;
+  void* params[] = {&r};
+  const size_t lds = sizeof(int2) * 2 * r.run * (kThreads >> r.lanes_log2);
+  gc_status st = gci::in_launches(r.sum_blocks + clear, kThreads, [&](uint32_t first, uint32_t n) {
+    r.block0 = first;
+    return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(row_sum_kernel<In, OutT, NV, P>), dim3(n), dim3(kThreads),
+                                           params, lds, stream));
+  });
+  if (st != GC_OK || !long_rows) return st;
   r.slices = static_cast<uint32_t>((r.pitch / 4 + 255) / 256);
-  return launch_blocks(row_join_kernel<OutT, P>, r, runs * r.slices, kJoinThreads, stream);
+  const uint64_t most = std::min<uint64_t>(runs * r.slices, 1024);   // workgroups; two fit a CU
+  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(row_join_kernel<OutT, P>), dim3(static_cast<uint32_t>(most)),
+                                         dim3(kJoinThreads), params, 0, stream));
 }
 
 template <class In, class OutT, int P>
@@ -503,7 +542,10 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
     s.tile0[k + 1] = s.tile0[k] + std::max<int32_t>(1, static_cast<int32_t>((c.tokens[k] + g.chunk - 1) / g.chunk));
   }
   for (int k = c.nranks; k < P; ++k) s.tile0[k + 1] = s.tile0[k];
-  fill_blocks<P>(r.run0, c.tokens, c.nranks, kRun);
+  r.run = g.run;
+  fill_blocks<P>(r.run0, c.tokens, c.nranks, r.run);
+  bool long_rows = false;   // a row of more tokens than two runs is possible
+  for (int k = 0; k < c.nranks; ++k) long_rows |= c.tokens[k] > 2 * r.run;
   s.N = r.N = c.nranks;
   s.chunk = g.chunk;
   s.vocab = r.vocab = static_cast<uint32_t>(c.vocab);
@@ -513,6 +555,7 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   s.counts = reinterpret_cast<uint32_t*>(scratch + g.counts);
   r.valid = s.valid = reinterpret_cast<int32_t*>(scratch + g.valid);
   r.present = s.present = reinterpret_cast<uint8_t*>(scratch + g.present);
+  r.long_rows = s.long_rows = reinterpret_cast<int32_t*>(scratch + g.long_rows);
   r.partial = reinterpret_cast<float*>(scratch + g.partial);
   s.bits = g.low_bits;
   gc_status st;
@@ -533,7 +576,8 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   r.accumulate = c.accumulate;
   r.lanes_log2 = 3;
   while (r.lanes_log2 < 8 && (uint64_t(1) << r.lanes_log2) < r.units) ++r.lanes_log2;
-  return r.units > kThreads ? row_sums<In, OutT, 2, P>(r, c.stream) : row_sums<In, OutT, 1, P>(r, c.stream);
+  return r.units > kThreads ? row_sums<In, OutT, 2, P>(r, long_rows, c.stream)
+                            : row_sums<In, OutT, 1, P>(r, long_rows, c.stream);
 }
 
 template <class In, class OutT>
