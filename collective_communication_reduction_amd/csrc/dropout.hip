@@ -49,40 +49,39 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
   }
 }
 
-// A lane takes one generator block; a workgroup kThreads consecutive ones.
+// A lane takes one unit, a whole generator block of bf16 elements or half of one of
+// fp32: with both halves in one lane each of its stores would leave every other 16
+// bytes to the next store (2.4 TB/s instead of 6).  A workgroup takes kThreads units.
 template <class In, bool RES, int P>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs<P> a) {
   typedef AnyUnit<In> U;
-  constexpr int VE = U::VE, Q = kPer / VE;
+  constexpr int VE = U::VE, PER = kPer / VE;   // units per generator block
   const int32_t block = a.block0 + blockIdx.x;
   const int rank = rank_of<P>(a.tile0, a.N, block);
-  const uint64_t b = static_cast<uint64_t>(block - a.tile0[rank]) * kThreads + threadIdx.x;
+  const uint64_t u = static_cast<uint64_t>(block - a.tile0[rank]) * kThreads + threadIdx.x;
   const uint64_t n = a.n[rank];
-  if (b * kPer >= n) return;
-  u32x4 x[Q], r[Q];
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    x[q] = U::load(a.x[rank], n, b * Q + q, 0);
-    if (RES) r[q] = U::load(a.res[rank], n, b * Q + q, 0);
-  }
-  const uint64_t at = a.offset + (a.step ? *a.step : 0);
+  if (u * VE >= n) return;
+  const u32x4 x = U::load(a.x[rank], n, u);
+  u32x4 r;
+  if (RES) r = U::load(a.res[rank], n, u);
+  const uint64_t at = a.offset + (a.step ? *a.step : 0), b = u / PER;
   uint32_t c[4] = {static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32) | static_cast<uint32_t>(rank) << 8,
                    static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32)};
   philox(c, a.key0, a.key1);
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    float v[VE], s[VE];
-    U::widen(x[q], v);
-    if (RES) U::widen(r[q], s);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int i = q * VE + e;
-      const uint32_t u = i % 2 ? c[i / 2] >> 16 : c[i / 2] & 0xFFFFu;
-      const float k = u >= a.drop ? v[e] * a.scale : 0.0f;  // a dropped value counts as 0, whatever it is
-      v[e] = RES ? s[e] + k : k;
-    }
-    U::store(a.y[rank], n, b * Q + q, U::narrow(v));
+  if (PER == 2 && u % 2) {
+    c[0] = c[2];
+    c[1] = c[3];
   }
+  float v[VE], s[VE];
+  U::widen(x, v);
+  if (RES) U::widen(r, s);
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    const uint32_t bits = e % 2 ? c[e / 2] >> 16 : c[e / 2] & 0xFFFFu;
+    const float k = bits >= a.drop ? v[e] * a.scale : 0.0f;  // a dropped value counts as 0, whatever it is
+    v[e] = RES ? s[e] + k : k;
+  }
+  U::store(a.y[rank], n, u, U::narrow(v));
 }
 
 template <class In, int P>
@@ -94,7 +93,7 @@ gc_status dropout_typed(const gci::DropoutCall& c) {
     a.y[s] = static_cast<char*>(c.y[s]);
     a.n[s] = c.counts[s];
   }
-  if (!fill_blocks<P>(a.tile0, c.counts, c.nranks, kThreads * kPer)) return GC_ERR_UNSUPPORTED;
+  if (!fill_blocks<P>(a.tile0, c.counts, c.nranks, kThreads * In::VE)) return GC_ERR_UNSUPPORTED;
   a.N = c.nranks;
   a.key0 = static_cast<uint32_t>(c.seed);
   a.key1 = static_cast<uint32_t>(c.seed >> 32);

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingArgs
   char* dst = a.out[rank] + row * a.H * In::ES;
   u32x4 x[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) x[j] = known ? U::template load<true>(src, a.H, u0 + j * lanes, 0) : u32x4{0, 0, 0, 0};
+  for (int j = 0; j < NV; ++j) x[j] = known ? U::template load<true>(src, a.H, u0 + j * lanes) : u32x4{0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float v[VE];
@@ -283,41 +283,35 @@ __device__ __forceinline__ int past(const int2* entries, int lo, int hi, int32_t
 // VE sums of unit u times scale, to a row of H elements of OutT, on top of what is there where `add`.
 template <class OutT, int VE>
 __device__ __forceinline__ void put_sums(char* row, uint64_t H, uint64_t u, const float (&acc)[VE], float scale, bool add) {
-  typedef typename std::conditional<OutT::ES == 2, OutBf16, OutF32>::type Out;
-  float v[VE];
+  typedef AnyUnit<OutT, VE> W;
+  float v[VE], old[VE];
+  if (add) W::widen(W::load(row, H, u), old);
 #pragma unroll
-  for (int e = 0; e < VE; ++e) v[e] = acc[e] * scale;
-  char* p = row + u * VE * OutT::ES;
-  if (add)
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (u * VE + e < H) v[e] += OutT::one(p, e);
-  if ((u + 1) * VE <= H) {
-    put<Out, VE, gci::kStoreDevNT>(p, pack<Out, VE>(v));
-    return;
-  }
-  typedef typename std::conditional<OutT::ES == 2, uint16_t, uint32_t>::type E;
-#pragma unroll
-  for (int e = 0; e < VE; ++e)
-    if (u * VE + e < H) reinterpret_cast<E*>(p)[e] = static_cast<E>(OutT::ES == 2 ? bf16_bits(v[e]) : __float_as_uint(v[e]));
+  for (int e = 0; e < VE; ++e) v[e] = add ? acc[e] * scale + old[e] : acc[e] * scale;
+  W::store(row, H, u, W::narrow(v));
 }
+
+// Elements of a unit that is at most 16 bytes in either type, so that every store of a wavefront is one run of memory.
+template <class In, class OutT>
+constexpr int sum_unit() { return In::VE < OutT::VE ? In::VE : OutT::VE; }
 
 template <class In, class OutT, int NV, int P>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a) {
-  typedef AnyUnit<In> U;
-  constexpr int VE = U::VE;
+  constexpr int VE = sum_unit<In, OutT>();
+  typedef AnyUnit<In, VE> U;
   extern __shared__ int2 entries[];   // (id, token) of each group's run and the next one
   const uint64_t block = a.block0 + blockIdx.x;
   if (block >= a.sum_blocks) {
-    // rows without a token
-    const uint64_t first = (block - a.sum_blocks) * a.clear_rows;
+    // rows without a token: a group of lanes takes clear_rows of them
+    const uint64_t first = ((block - a.sum_blocks) * kThreads + threadIdx.x >> a.lanes_log2) * a.clear_rows;
     const uint64_t last = min(first + a.clear_rows, static_cast<uint64_t>(a.N) * a.vocab);
     typedef AnyUnit<OutT> W;
     const uint64_t units = (a.H + W::VE - 1) / W::VE;
+    const uint32_t lanes = 1u << a.lanes_log2;
     for (uint64_t r = first; r < last; ++r) {
       if (a.present[r]) continue;
       char* row = a.dw[r / a.vocab] + r % a.vocab * a.H * OutT::ES;
-      for (uint64_t u = threadIdx.x; u < units; u += kThreads) W::store(row, a.H, u, u32x4{0, 0, 0, 0});
+      for (uint64_t u = threadIdx.x & (lanes - 1); u < units; u += lanes) W::store(row, a.H, u, u32x4{0, 0, 0, 0});
     }
     return;
   }
@@ -377,12 +371,12 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
     }
   };
   for (int i = i0; i < count; i += kAhead) {
-    u32x4 x[kAhead][NV];
+    typename U::T x[kAhead][NV];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const char* row = dout + static_cast<uint64_t>(static_cast<uint32_t>(mine[min(i + k, count - 1)].y)) * row_bytes;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) x[k][j] = U::load(row, a.H, u0 + (static_cast<uint64_t>(j) << a.lanes_log2), 0);
+      for (int j = 0; j < NV; ++j) x[k][j] = U::load(row, a.H, u0 + (static_cast<uint64_t>(j) << a.lanes_log2));
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -509,8 +503,10 @@ gc_status row_sums(RowSumArgs<P>& r, bool long_rows, hipStream_t stream) {
   r.slices = static_cast<uint32_t>((r.units + per - 1) / per);
   r.sum_blocks = ((runs * r.slices << r.lanes_log2) + kThreads - 1) / kThreads;
   const uint64_t row = r.H * OutT::ES, rows = static_cast<uint64_t>(r.N) * r.vocab;
-  r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, (64 << 10) / row));
-  const uint64_t clear = r.accumulate ? 0 : (rows + r.clear_rows - 1) / r.clear_rows;
+  const uint64_t lane_bytes = row >> r.lanes_log2;   // about 256 bytes per lane of a clearing group
+  r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, 256 / std::max<uint64_t>(1, lane_bytes)));
+  const uint64_t groups = (rows + r.clear_rows - 1) / r.clear_rows;
+  const uint64_t clear = r.accumulate ? 0 : ((groups << r.lanes_log2) + kThreads - 1) / kThreads;
   void* params[] = {&r};
   const size_t lds = sizeof(int2) * 2 * r.run * (kThreads >> r.lanes_log2);
   gc_status st = gci::in_launches(r.sum_blocks + clear, kThreads, [&](uint32_t first, uint32_t n) {
@@ -570,7 +566,8 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   }
   if (st != GC_OK) return st;
   r.H = c.hidden;
-  r.units = (c.hidden + In::VE - 1) / In::VE;
+  constexpr int VE = sum_unit<In, OutT>();
+  r.units = (c.hidden + VE - 1) / VE;
   r.pitch = gci::embedding_pitch(c.hidden);
   r.scale = c.scale;
   r.accumulate = c.accumulate;

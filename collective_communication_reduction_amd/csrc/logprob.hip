@@ -139,7 +139,7 @@ template <class In, bool ENT>
 __device__ __forceinline__ void put_grads(const RowGrad& g, const char* row, char* out, uint64_t V, uint64_t stride) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80FF80u : 0xFF800000u;
+  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;
   const uint64_t units = (stride + VE - 1) / VE;
   for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
     float x[VE];
@@ -157,7 +157,7 @@ template <class In, int P>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs<P> a) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;   // -inf
   __shared__ Stat stats[kThreads / kWave];
   __shared__ uint64_t best[kThreads / kWave];
   const int32_t block = a.block0 + blockIdx.x;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const Logpro
             ENT ? a.dentropy[rank][r] : 0.0f, a.scale, target, lse == kNegInf};
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80FF80u : 0xFF800000u;
+  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;
   const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
   const char* row = a.logits[rank] + off;
   char* out = a.dlogits[rank] + off;
