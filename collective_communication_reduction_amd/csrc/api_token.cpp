@@ -54,8 +54,9 @@ extern "C" gc_status gc_embedding(const void* const* weight, const int32_t* cons
   return gci::launch_embedding({weight, tokens, ntokens, nranks, vocab, hidden, scale, t, out, stream});
 }
 
-// A sorting workgroup takes 1024 tokens (two of each wavefront's 64 lanes), more where a rank would
-// make over 256 pieces: every piece reads the counts of all the others.
+// Ranks of at most 4096 tokens are sorted by one workgroup each, in one launch; longer ones by a workgroup
+// per 1024 tokens (two of each lane), more where a rank would make over 256 pieces: every piece reads the
+// counts of all the others.
 gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden) {
   gci::EmbeddingGeom g;
   int64_t most = 0;
@@ -63,7 +64,8 @@ gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64
     g.tokens += tokens[r];
     most = std::max(most, tokens[r]);
   }
-  g.chunk = static_cast<int32_t>(std::max<int64_t>(1024, (most / 256 + 511) / 512 * 512));
+  const auto up512 = [](int64_t x) { return (std::max<int64_t>(x, 1) + 511) / 512 * 512; };
+  g.chunk = static_cast<int32_t>(most <= 4096 ? up512(most) : std::max<int64_t>(1024, up512(most / 256)));
   for (int r = 0; r < nranks; ++r) g.chunks += static_cast<int32_t>(std::max<int64_t>(1, (tokens[r] + g.chunk - 1) / g.chunk));
   g.bits = 1;
   while (vocab > uint64_t(1) << g.bits) ++g.bits;
@@ -78,7 +80,8 @@ gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64
   g.counts = g.perm + up256(n * 4);
   g.valid = g.counts + up256(static_cast<uint64_t>(g.chunks) * 4 << g.low_bits);
   g.present = g.valid + up256(static_cast<uint64_t>(nranks) * 4);
-  g.long_rows = g.present + up256(nranks * vocab);
+  g.present_row = (vocab + 15) / 16 * 16;
+  g.long_rows = g.present + up256(nranks * g.present_row);
   g.partial = g.long_rows + up256((runs + 1) * 4);
   g.bytes = g.partial + up256(runs * 2 * embedding_pitch(hidden) * 4);
   return g;

@@ -33,6 +33,7 @@ struct DropoutArgs {
   const uint64_t* step;
   uint32_t drop;
   float scale;
+  bool through;   // every y starts on a line
 };
 
 __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
@@ -58,12 +59,15 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs<P> 
   constexpr int VE = U::VE, PER = kPer / VE;   // units per generator block
   const int32_t block = a.block0 + blockIdx.x;
   const int rank = rank_of<P>(a.tile0, a.N, block);
-  const uint64_t u = static_cast<uint64_t>(block - a.tile0[rank]) * kThreads + threadIdx.x;
-  const uint64_t n = a.n[rank];
-  if (u * VE >= n) return;
-  const u32x4 x = U::load(a.x[rank], n, u);
+  const uint64_t first = static_cast<uint64_t>(block - a.tile0[rank]) * (kThreads * VE);   // the workgroup's elements
+  const uint32_t n = static_cast<uint32_t>(min<uint64_t>(kThreads * VE, a.n[rank] - first));
+  if (threadIdx.x * VE >= n) return;
+  const uint32_t here = min(n - threadIdx.x * VE, static_cast<uint32_t>(VE));   // elements of the unit
+  const uint64_t off = (first + threadIdx.x * VE) * In::ES;
+  const u32x4 x = U::load(a.x[rank] + off, here, 0);
   u32x4 r;
-  if (RES) r = U::load(a.res[rank], n, u);
+  if (RES) r = U::load(a.res[rank] + off, here, 0);
+  const uint64_t u = first / VE + threadIdx.x;
   const uint64_t at = a.offset + (a.step ? *a.step : 0), b = u / PER;
   uint32_t c[4] = {static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32) | static_cast<uint32_t>(rank) << 8,
                    static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32)};
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs<P> 
     const float k = bits >= a.drop ? v[e] * a.scale : 0.0f;  // a dropped value counts as 0, whatever it is
     v[e] = RES ? s[e] + k : k;
   }
-  U::store(a.y[rank], n, u, U::narrow(v));
+  U::store(a.y[rank] + off, here, 0, U::narrow(v), a.through);
 }
 
 template <class In, int P>
@@ -94,6 +98,9 @@ gc_status dropout_typed(const gci::DropoutCall& c) {
     a.n[s] = c.counts[s];
   }
   if (!fill_blocks<P>(a.tile0, c.counts, c.nranks, kThreads * In::VE)) return GC_ERR_UNSUPPORTED;
+  uint64_t m = 0;
+  for (int s = 0; s < c.nranks; ++s) m |= c.counts[s] ? reinterpret_cast<uint64_t>(c.y[s]) : 0;
+  a.through = m % kLine == 0;
   a.N = c.nranks;
   a.key0 = static_cast<uint32_t>(c.seed);
   a.key1 = static_cast<uint32_t>(c.seed >> 32);

@@ -28,9 +28,10 @@ struct EmbeddingArgs {
   int32_t N;
   uint32_t vocab;
   uint64_t H;
-  uint64_t units;       // per row, the last may be short
+  uint64_t units;       // per row
   uint32_t slices;      // of a row, NV << lanes_log2 units each
   int32_t lanes_log2;   // lanes that share a row's slice
+  bool through;         // every row written starts on a line
   float scale;
 };
 
@@ -44,21 +45,24 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingArgs
   const uint64_t row = a.slices == 1 ? q : q / a.slices;
   if (row >= static_cast<uint64_t>(a.tok[rank])) return;
   const uint32_t lanes = 1u << a.lanes_log2;
-  const uint64_t u0 = (q - row * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + (threadIdx.x & (lanes - 1));
+  const uint32_t u0 = static_cast<uint32_t>((q - row * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2)) + (threadIdx.x & (lanes - 1));
   const uint32_t id = static_cast<uint32_t>(a.ids[rank][row]);
   const bool known = id < a.vocab;
-  const char* src = a.w[rank] + static_cast<uint64_t>(known ? id : 0) * a.H * In::ES;
   char* dst = a.out[rank] + row * a.H * In::ES;
+  const char* src = a.w[rank] + static_cast<uint64_t>(known ? id : 0) * a.H * In::ES;
+  const uint32_t H = static_cast<uint32_t>(a.H);
   u32x4 x[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) x[j] = known ? U::template load<true>(src, a.H, u0 + j * lanes) : u32x4{0, 0, 0, 0};
+  for (int j = 0; j < NV; ++j)
+    x[j] = known && u0 + j * lanes < a.units ? U::template load<true>(src, H, U::start(H, u0 + j * lanes)) : u32x4{0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    if (u0 + j * lanes >= a.units) continue;
     float v[VE];
     U::widen(x[j], v);
 #pragma unroll
     for (int e = 0; e < VE; ++e) v[e] = known ? v[e] * a.scale : 0.0f;
-    U::store(dst, a.H, u0 + j * lanes, U::narrow(v));
+    U::store(dst, H, U::start(H, u0 + j * lanes), U::narrow(v), a.through);
   }
 }
 
@@ -78,13 +82,15 @@ struct SortArgs {
   int32_t N;
   int32_t chunk;          // entries per workgroup
   uint32_t vocab;
-  int32_t shift, bits;    // the digit of this pass
+  int32_t low_bits;       // of the first pass's digit
+  int32_t high_bits;      // of the second's, 0: one pass
   uint64_t* pairs;        // id << 32 | token, between the passes
   int32_t* keys;          // sorted ids and their tokens
   int32_t* perm;
   uint32_t* counts;       // [chunks][1 << bits]
   int32_t* valid;         // tokens of each rank inside the vocabulary
-  uint8_t* present;       // [ranks][vocab] whether a token occurs
+  uint8_t* present;       // [ranks][present_row] whether a token occurs
+  uint32_t present_row;   // bytes, a multiple of 16
   int32_t* long_rows;     // count, then the runs where rows of many runs begin
 };
 
@@ -100,9 +106,20 @@ __device__ __forceinline__ uint64_t sort_entry(const SortArgs<P>& a, int rank, i
   }
 }
 
+// A digit of the id: `bits` bits from bit `shift` on.
+struct Digit {
+  int32_t shift, bits;
+  __device__ __forceinline__ uint32_t of(uint64_t entry) const {
+    return static_cast<uint32_t>(entry >> (32 + shift)) & ((1u << bits) - 1);
+  }
+};
+
+// Clears part `mine` of `parts` of the rank's map of tokens, and the count of long rows.
 template <int P>
-__device__ __forceinline__ uint32_t digit_of(const SortArgs<P>& a, uint64_t entry) {
-  return static_cast<uint32_t>(entry >> (32 + a.shift)) & ((1u << a.bits) - 1);
+__device__ __forceinline__ void clear_marks(const SortArgs<P>& a, int rank, uint32_t mine, uint32_t parts) {
+  u32x4* map = reinterpret_cast<u32x4*>(a.present + static_cast<uint64_t>(rank) * a.present_row);
+  for (uint32_t v = mine * kSortThreads + threadIdx.x; v < a.present_row / 16; v += parts * kSortThreads) map[v] = u32x4{0, 0, 0, 0};
+  if (rank == 0 && mine == 0 && threadIdx.x == 0) a.long_rows[0] = 0;
 }
 
 // Digit counts of one chunk.
@@ -113,18 +130,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   const int rank = rank_of<P>(a.tile0, a.N, block);
   const int64_t n = FIRST ? a.tok[rank] : a.valid[rank];
   const int64_t first = static_cast<int64_t>(block - a.tile0[rank]) * a.chunk;
-  const int bins = 1 << a.bits;
-  if constexpr (FIRST) {  // the rank's map is cleared here and set by the placing kernel behind
-    const int32_t mine = block - a.tile0[rank], chunks = a.tile0[rank + 1] - a.tile0[rank];
-    uint8_t* map = a.present + static_cast<uint64_t>(rank) * a.vocab;
-    for (uint32_t v = mine * kSortThreads + threadIdx.x; v < a.vocab; v += chunks * kSortThreads) map[v] = 0;
-    if (block == 0 && threadIdx.x == 0) a.long_rows[0] = 0;
-  }
+  const Digit digit = FIRST ? Digit{0, a.low_bits} : Digit{a.low_bits, a.high_bits};
+  const int bins = 1 << digit.bits;
+  if constexpr (FIRST) clear_marks(a, rank, block - a.tile0[rank], a.tile0[rank + 1] - a.tile0[rank]);
   for (int d = threadIdx.x; d < bins; d += kSortThreads) hist[d] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < a.chunk; i += kSortThreads) {
     const uint64_t e = sort_entry<FIRST>(a, rank, first + i, n);
-    if (e != ~uint64_t(0)) atomicAdd(&hist[digit_of(a, e)], 1u);
+    if (e != ~uint64_t(0)) atomicAdd(&hist[digit.of(e)], 1u);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += kSortThreads) a.counts[static_cast<uint64_t>(block) * bins + d] = hist[d];
@@ -151,40 +164,43 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t x, uint32_t* lds, u
   return before + s - x;
 }
 
-// Places one chunk's entries: behind all entries of smaller digits, those of the
-// same digit in earlier chunks, and those of earlier wavefronts and lanes.
-template <bool FIRST, bool LAST, int P>
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs<P> a) {
-  extern __shared__ uint32_t next[];   // [wavefront][digit]: entries counted, then the place of the next one
-  __shared__ uint32_t sums[kSortWaves];
-  const int32_t block = a.block0 + blockIdx.x;
-  const int rank = rank_of<P>(a.tile0, a.N, block);
-  const int64_t n = FIRST ? a.tok[rank] : a.valid[rank];
-  const int32_t mine = block - a.tile0[rank], chunks = a.tile0[rank + 1] - a.tile0[rank];
-  const int bins = 1 << a.bits, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+// Places chunk `mine` of the rank's n entries: behind all entries of smaller digits,
+// those of the same digit in earlier chunks, and those of earlier wavefronts and
+// lanes.  ALONE: the rank has this chunk only, whose counts need not be looked up.
+// Returns the number of entries of all chunks.
+template <bool FIRST, bool LAST, bool ALONE, int P>
+__device__ __forceinline__ uint32_t place_chunk(const SortArgs<P>& a, int rank, int64_t n, int32_t mine, int32_t chunks,
+                                                uint32_t* next, uint32_t* sums) {
+  const Digit digit = FIRST ? Digit{0, a.low_bits} : Digit{a.low_bits, a.high_bits};
+  const int bins = 1 << digit.bits, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int per = a.chunk / kSortWaves;
   const int64_t first = static_cast<int64_t>(mine) * a.chunk + wave * per;
-  uint32_t* my = next + wave * bins;
+  uint32_t* my = next + wave * bins;   // [wavefront][digit]: entries counted, then the place of the next one
   for (int d = threadIdx.x; d < kSortWaves * bins; d += kSortThreads) next[d] = 0;
   __syncthreads();
   for (int i = lane; i < per; i += kWave) {
     const uint64_t e = sort_entry<FIRST>(a, rank, first + i, n);
-    if (e != ~uint64_t(0)) atomicAdd(&my[digit_of(a, e)], 1u);
+    if (e != ~uint64_t(0)) atomicAdd(&my[digit.of(e)], 1u);
   }
   __syncthreads();
   // digits in order, up to four of them per thread: entries of all chunks, and of those before this one
   const int run = (bins + kSortThreads - 1) / kSortThreads;
-  const uint32_t* counts = a.counts + static_cast<uint64_t>(a.tile0[rank]) * bins;
+  const uint32_t* counts = ALONE ? nullptr : a.counts + static_cast<uint64_t>(a.tile0[rank]) * bins;
   const int d0 = threadIdx.x * run;
   uint32_t all[kSortRun] = {}, before[kSortRun] = {}, sum = 0;
 #pragma unroll
   for (int k = 0; k < kSortRun; ++k) {
     if (k >= run || d0 + k >= bins) break;
+    if constexpr (ALONE) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) all[k] += next[w * bins + d0 + k];
+    } else {
 #pragma unroll 8
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t t = counts[static_cast<uint64_t>(c) * bins + d0 + k];
-      all[k] += t;
-      before[k] += c < mine ? t : 0;
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t t = counts[static_cast<uint64_t>(c) * bins + d0 + k];
+        all[k] += t;
+        before[k] += c < mine ? t : 0;
+      }
     }
     sum += all[k];
   }
@@ -203,26 +219,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
     }
     at += all[k];
   }
-  if (FIRST && mine == 0 && threadIdx.x == 0) a.valid[rank] = static_cast<int32_t>(total);
   __syncthreads();
   for (int i = 0; i < per; i += kWave) {
     const uint64_t e = sort_entry<FIRST>(a, rank, first + i + lane, i + lane < per ? n : 0);
     const bool ok = e != ~uint64_t(0);
-    const uint32_t d = ok ? digit_of(a, e) : 0;
+    const uint32_t d = ok ? digit.of(e) : 0;
     uint64_t peers = __ballot(ok);
-    for (int b = 0; b < a.bits; ++b) {
+    for (int b = 0; b < digit.bits; ++b) {
       const uint64_t ones = __ballot(d >> b & 1);
       peers &= d >> b & 1 ? ones : ~ones;
     }
-    const int before = __popcll(peers & ((uint64_t(1) << lane) - 1));
-    const uint32_t place = ok ? my[d] + before : 0;
+    const int ahead = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    const uint32_t place = ok ? my[d] + ahead : 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (ok && before == 0) my[d] += __popcll(peers);
+    if (ok && ahead == 0) my[d] += __popcll(peers);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (ok) {
-      if constexpr (FIRST) a.present[static_cast<uint64_t>(rank) * a.vocab + (e >> 32)] = 1;
+      if constexpr (FIRST) a.present[static_cast<uint64_t>(rank) * a.present_row + (e >> 32)] = 1;
       if constexpr (LAST) {
         a.keys[a.at[rank] + place] = static_cast<int32_t>(e >> 32);
         a.perm[a.at[rank] + place] = static_cast<int32_t>(e);
@@ -231,6 +246,40 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
       }
     }
   }
+  return total;
+}
+
+template <bool FIRST, bool LAST, int P>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs<P> a) {
+  extern __shared__ uint32_t next[];
+  __shared__ uint32_t sums[kSortWaves];
+  const int32_t block = a.block0 + blockIdx.x;
+  const int rank = rank_of<P>(a.tile0, a.N, block);
+  const int32_t mine = block - a.tile0[rank];
+  const uint32_t total = place_chunk<FIRST, LAST, false>(a, rank, FIRST ? a.tok[rank] : a.valid[rank], mine,
+                                                         a.tile0[rank + 1] - a.tile0[rank], next, sums);
+  if (FIRST && mine == 0 && threadIdx.x == 0) a.valid[rank] = static_cast<int32_t>(total);
+}
+
+// The whole sort of ranks of few tokens, one workgroup each.
+template <int P>
+__global__ void __launch_bounds__(kSortThreads) sort_alone_kernel(const SortArgs<P> a) {
+  extern __shared__ uint32_t next[];
+  __shared__ uint32_t sums[kSortWaves];
+  const int rank = blockIdx.x;
+  clear_marks(a, rank, 0, 1);
+  __threadfence_block();
+  __syncthreads();
+  uint32_t n;
+  if (a.high_bits == 0) {
+    n = place_chunk<true, true, true>(a, rank, a.tok[rank], 0, 1, next, sums);
+  } else {
+    n = place_chunk<true, false, true>(a, rank, a.tok[rank], 0, 1, next, sums);
+    __threadfence_block();
+    __syncthreads();
+    place_chunk<false, true, true>(a, rank, n, 0, 1, next, sums);
+  }
+  if (threadIdx.x == 0) a.valid[rank] = static_cast<int32_t>(n);
 }
 
 // ------------------------------------------------------------- sums of sorted rows
@@ -241,7 +290,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
 // are left as partial sums, the first of them the tail of the run where the row
 // begins, the others the heads of the runs behind, and a second launch adds them up.
 
-constexpr int kAhead = 4;      // rows whose loads are in flight together
+constexpr int kClearAhead = 4;   // rows that are looked up together before the empty ones are cleared
 
 template <int P>
 struct RowSumArgs {
@@ -253,16 +302,18 @@ struct RowSumArgs {
   int32_t N;
   uint32_t vocab;
   uint64_t H;
-  uint64_t units;
+  uint64_t units;        // per row
   uint64_t pitch;        // floats of a partial row
   uint64_t sum_blocks;   // workgroups of the runs; those behind clear rows
   uint32_t slices;       // of a row, NV << lanes_log2 units each
   int32_t lanes_log2;
+  bool through;          // every row written starts on a line
   uint32_t clear_rows;   // rows per clearing workgroup
   const int32_t* keys;
   const int32_t* perm;
   const int32_t* valid;
   const uint8_t* present;
+  uint32_t present_row;
   int32_t* long_rows;    // count, then the runs where rows of many runs begin
   float* partial;        // [runs][head, tail][pitch]
   int32_t run;           // sorted tokens per run
@@ -280,15 +331,30 @@ __device__ __forceinline__ int past(const int2* entries, int lo, int hi, int32_t
   return lo;
 }
 
-// VE sums of unit u times scale, to a row of H elements of OutT, on top of what is there where `add`.
-template <class OutT, int VE>
-__device__ __forceinline__ void put_sums(char* row, uint64_t H, uint64_t u, const float (&acc)[VE], float scale, bool add) {
+// VE sums times scale to a row of n elements: those from element `off` of its unit u (of UNIT elements) on.  With `add`
+// they go on top of what is there, each element from one lane alone: the row's last unit may overlap the one before and
+// leaves it those elements.
+template <class OutT, int VE, int UNIT>
+__device__ __forceinline__ void put_sums(char* row, uint32_t n, uint32_t u, uint32_t off, const float (&acc)[VE], float scale,
+                                         bool add, bool through) {
   typedef AnyUnit<OutT, VE> W;
-  float v[VE], old[VE];
-  if (add) W::widen(W::load(row, H, u), old);
+  const uint32_t s = AnyUnit<OutT, UNIT>::start(n, u) + off;
+  const uint32_t here = n >= UNIT ? VE : n > off ? min(n - off, static_cast<uint32_t>(VE)) : 0;   // elements in the row
+  char* p = row + static_cast<uint64_t>(s) * OutT::ES;
+  float v[VE];
 #pragma unroll
-  for (int e = 0; e < VE; ++e) v[e] = add ? acc[e] * scale + old[e] : acc[e] * scale;
-  W::store(row, H, u, W::narrow(v));
+  for (int e = 0; e < VE; ++e) v[e] = acc[e] * scale;
+  if (!add) {
+    W::store(p, here, 0, W::narrow(v), through);
+    return;
+  }
+  float old[VE];
+  W::widen(W::load(p, here, 0), old);
+#pragma unroll
+  for (int e = 0; e < VE; ++e) v[e] += old[e];
+  const uint32_t own = u * UNIT + off;   // the first element that is this unit's
+  if (s == own) W::store(p, here, 0, W::narrow(v), through);
+  else W::store_some(p, min(own - s, static_cast<uint32_t>(VE)), VE, W::narrow(v));
 }
 
 // Elements of a unit that is at most 16 bytes in either type, so that every store of a wavefront is one run of memory.
@@ -298,20 +364,31 @@ constexpr int sum_unit() { return In::VE < OutT::VE ? In::VE : OutT::VE; }
 template <class In, class OutT, int NV, int P>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a) {
   constexpr int VE = sum_unit<In, OutT>();
+  constexpr int AHEAD = NV > 2 ? 2 : 4;   // rows whose loads are in flight together
   typedef AnyUnit<In, VE> U;
   extern __shared__ int2 entries[];   // (id, token) of each group's run and the next one
   const uint64_t block = a.block0 + blockIdx.x;
   if (block >= a.sum_blocks) {
     // rows without a token: a group of lanes takes clear_rows of them
-    const uint64_t first = ((block - a.sum_blocks) * kThreads + threadIdx.x >> a.lanes_log2) * a.clear_rows;
-    const uint64_t last = min(first + a.clear_rows, static_cast<uint64_t>(a.N) * a.vocab);
-    typedef AnyUnit<OutT> W;
-    const uint64_t units = (a.H + W::VE - 1) / W::VE;
-    const uint32_t lanes = 1u << a.lanes_log2;
-    for (uint64_t r = first; r < last; ++r) {
-      if (a.present[r]) continue;
-      char* row = a.dw[r / a.vocab] + r % a.vocab * a.H * OutT::ES;
-      for (uint64_t u = threadIdx.x & (lanes - 1); u < units; u += lanes) W::store(row, a.H, u, u32x4{0, 0, 0, 0});
+    const uint32_t rows = a.N * a.vocab, lanes = 1u << a.lanes_log2;
+    const uint64_t group = (block - a.sum_blocks) * kThreads + threadIdx.x >> a.lanes_log2;
+    const uint32_t first = static_cast<uint32_t>(min<uint64_t>(group * a.clear_rows, rows)), last = min(first + a.clear_rows, rows);
+    typedef AnyUnit<OutT, VE> W;
+    const typename W::T zero = {};
+    for (uint32_t r0 = first; r0 < last; r0 += kClearAhead) {
+      char* row[kClearAhead];
+#pragma unroll
+      for (int k = 0; k < kClearAhead; ++k) {
+        const uint32_t r = min(r0 + k, last - 1), rank = r / a.vocab, v = r - rank * a.vocab;
+        const bool empty = r0 + k < last && !a.present[static_cast<uint64_t>(rank) * a.present_row + v];
+        row[k] = empty ? a.dw[rank] + v * (a.H * OutT::ES) : nullptr;
+      }
+#pragma unroll
+      for (int k = 0; k < kClearAhead; ++k) {
+        if (!row[k]) continue;
+        const uint32_t H = static_cast<uint32_t>(a.H);
+        for (uint32_t u = threadIdx.x & (lanes - 1); u < a.units; u += lanes) W::store(row[k], H, W::start(H, u), zero, a.through);
+      }
     }
     return;
   }
@@ -350,19 +427,25 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
     count = past(mine, count, staged, last_key);
     ended = true;
   }
-  const uint64_t u0 = (q - static_cast<uint64_t>(run) * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2) + lane;
+  const uint32_t u0 = static_cast<uint32_t>((q - static_cast<uint64_t>(run) * a.slices) * (static_cast<uint64_t>(NV) << a.lanes_log2)) + lane;
   const char* dout = a.dout[rank];
-  const uint64_t row_bytes = a.H * In::ES;
+  char* dw = a.dw[rank];
+  const uint64_t row_bytes = a.H * In::ES, dw_bytes = a.H * OutT::ES;
+  const uint32_t H = static_cast<uint32_t>(a.H);
+  uint32_t s[NV];   // first element of each unit; lanes past the row's end read its last one
+#pragma unroll
+  for (int j = 0; j < NV; ++j) s[j] = U::start(H, u0 + (j << a.lanes_log2));
   float acc[NV][VE] = {};
   const auto flush = [&](bool whole) {
+    char* row = dw + cur * dw_bytes;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint64_t u = u0 + (static_cast<uint64_t>(j) << a.lanes_log2);
+      const uint32_t u = u0 + (j << a.lanes_log2);
       if (u >= a.units) continue;
       if (began && whole) {
-        put_sums<OutT, VE>(a.dw[rank] + static_cast<uint64_t>(cur) * a.H * OutT::ES, a.H, u, acc[j], a.scale, a.accumulate);
+        put_sums<OutT, VE, VE>(row, H, u, 0, acc[j], a.scale, a.accumulate, a.through);
       } else {
-        float* p = a.partial + (2 * static_cast<uint64_t>(run) + (began ? 1 : 0)) * a.pitch + u * VE;
+        float* p = a.partial + (2 * static_cast<uint64_t>(run) + (began ? 1 : 0)) * a.pitch + static_cast<uint64_t>(u) * VE;
 #pragma unroll
         for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(p + e) = float4{acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]};
       }
@@ -370,16 +453,18 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
       for (int e = 0; e < VE; ++e) acc[j][e] = 0.0f;
     }
   };
-  for (int i = i0; i < count; i += kAhead) {
-    typename U::T x[kAhead][NV];
+  // the next rows' loads are in flight while these are added
+  const auto fetch = [&](typename U::T (&x)[AHEAD][NV], int i) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const char* row = dout + static_cast<uint64_t>(static_cast<uint32_t>(mine[min(i + k, count - 1)].y)) * row_bytes;
+    for (int k = 0; k < AHEAD; ++k) {
+      const char* row = dout + static_cast<uint32_t>(mine[min(i + k, count - 1)].y) * row_bytes;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) x[k][j] = U::load(row, a.H, u0 + (static_cast<uint64_t>(j) << a.lanes_log2));
+      for (int j = 0; j < NV; ++j) x[k][j] = U::load(row, H, s[j]);
     }
+  };
+  const auto take = [&](const typename U::T (&x)[AHEAD][NV], int i) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       if (i + k >= count) break;
       const int32_t key = mine[i + k].x;
       if (key != cur) {
@@ -395,6 +480,14 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
         for (int e = 0; e < VE; ++e) acc[j][e] += v[e];
       }
     }
+  };
+  typename U::T xa[AHEAD][NV], xb[AHEAD][NV];
+  fetch(xa, i0);
+  for (int i = i0; i < count; i += 2 * AHEAD) {
+    if (i + AHEAD < count) fetch(xb, i + AHEAD);
+    take(xa, i);
+    if (i + 2 * AHEAD < count) fetch(xa, i + 2 * AHEAD);
+    take(xb, i + AHEAD);
   }
   flush(ended);
   if (began && !ended && u0 == 0) a.long_rows[1 + atomicAdd(&a.long_rows[0], 1)] = static_cast<int32_t>(run);
@@ -406,7 +499,7 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const RowSumArgs<P> a
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinGroups = kJoinThreads / 256;
 
-template <class OutT, int P>
+template <class OutT, int VE, int P>
 __global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs<P> a) {
   __shared__ float4 sums[kJoinGroups - 1][256];
   const int group = threadIdx.x / 256, lane = threadIdx.x % 256;
@@ -425,7 +518,7 @@ __global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs
     }
     const uint64_t u = (item - slot * a.slices) * 256 + lane;
     float4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-    if (u * 4 < a.pitch) {
+    if (u * 4 < a.units * VE) {
       const float* p = a.partial + 2 * static_cast<uint64_t>(run) * a.pitch + u * 4;
 #pragma unroll 8
       for (int64_t i = group; i < parts; i += kJoinGroups) {
@@ -438,7 +531,7 @@ __global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs
     }
     if (group > 0) sums[group - 1][lane] = acc;
     __syncthreads();
-    if (group == 0 && u * 4 < a.H) {
+    if (group == 0 && u * 4 < a.units * VE) {
       float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
       for (int g = 0; g < kJoinGroups - 1; ++g) {
@@ -448,7 +541,9 @@ __global__ void __launch_bounds__(kJoinThreads) row_join_kernel(const RowSumArgs
         v[2] += t.z;
         v[3] += t.w;
       }
-      put_sums<OutT, 4>(a.dw[rank] + static_cast<uint64_t>(key) * a.H * OutT::ES, a.H, u, v, a.scale, a.accumulate);
+      char* row = a.dw[rank] + static_cast<uint64_t>(key) * a.H * OutT::ES;
+      const uint32_t i = static_cast<uint32_t>(u) * 4;   // partial rows: unit after unit
+      put_sums<OutT, 4, VE>(row, static_cast<uint32_t>(a.H), i / VE, i % VE, v, a.scale, a.accumulate, a.through);
     }
     __syncthreads();
   }
@@ -477,15 +572,22 @@ gc_status embedding_typed(const gci::EmbeddingCall& c) {
   a.N = c.nranks;
   a.vocab = static_cast<uint32_t>(c.vocab);
   a.H = c.hidden;
+  uint64_t m = c.hidden * In::ES;
+  for (int s = 0; s < c.nranks; ++s) m |= c.tokens[s] ? reinterpret_cast<uint64_t>(c.out[s]) : 0;
+  a.through = m % kLine == 0;
   a.units = (c.hidden + In::VE - 1) / In::VE;
   a.scale = c.scale;
   while (a.lanes_log2 < 6 && (uint64_t(1) << a.lanes_log2) < a.units) ++a.lanes_log2;
-  return a.units > kWave ? embedding_impl<In, 4, P>(c, a) : embedding_impl<In, 1, P>(c, a);
+  // units per lane: as many as spread a row evenly over slices of at most four
+  const uint64_t waves = (a.units + kWave - 1) / kWave, slices = (waves + 3) / 4, nv = (waves + slices - 1) / slices;
+  if (nv <= 1) return embedding_impl<In, 1, P>(c, a);
+  if (nv == 2) return embedding_impl<In, 2, P>(c, a);
+  return nv == 3 ? embedding_impl<In, 3, P>(c, a) : embedding_impl<In, 4, P>(c, a);
 }
 
 template <bool FIRST, bool LAST, int P>
 gc_status sort_pass(SortArgs<P>& a, const gci::EmbeddingGeom& g, hipStream_t stream) {
-  const size_t bins = size_t(1) << a.bits;
+  const size_t bins = size_t(1) << (FIRST ? a.low_bits : a.high_bits);
   void* params[] = {&a};
   const auto go = [&](const void* kernel, size_t lds) {
     return gci::in_launches(g.chunks, kSortThreads, [&](uint32_t first, uint32_t n) {
@@ -503,8 +605,8 @@ gc_status row_sums(RowSumArgs<P>& r, bool long_rows, hipStream_t stream) {
   r.slices = static_cast<uint32_t>((r.units + per - 1) / per);
   r.sum_blocks = ((runs * r.slices << r.lanes_log2) + kThreads - 1) / kThreads;
   const uint64_t row = r.H * OutT::ES, rows = static_cast<uint64_t>(r.N) * r.vocab;
-  const uint64_t lane_bytes = row >> r.lanes_log2;   // about 256 bytes per lane of a clearing group
-  r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, 256 / std::max<uint64_t>(1, lane_bytes)));
+  const uint64_t lane_bytes = row >> r.lanes_log2;   // about 64 bytes per lane of a clearing group
+  r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, 64 / std::max<uint64_t>(1, lane_bytes)));
   const uint64_t groups = (rows + r.clear_rows - 1) / r.clear_rows;
   const uint64_t clear = r.accumulate ? 0 : ((groups << r.lanes_log2) + kThreads - 1) / kThreads;
   void* params[] = {&r};
@@ -517,7 +619,7 @@ gc_status row_sums(RowSumArgs<P>& r, bool long_rows, hipStream_t stream) {
   if (st != GC_OK || !long_rows) return st;
   r.slices = static_cast<uint32_t>((r.pitch / 4 + 255) / 256);
   const uint64_t most = std::min<uint64_t>(runs * r.slices, 1024);   // workgroups; two fit a CU
-  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(row_join_kernel<OutT, P>), dim3(static_cast<uint32_t>(most)),
+  return gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(row_join_kernel<OutT, sum_unit<In, OutT>(), P>), dim3(static_cast<uint32_t>(most)),
                                          dim3(kJoinThreads), params, 0, stream));
 }
 
@@ -553,28 +655,38 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   r.present = s.present = reinterpret_cast<uint8_t*>(scratch + g.present);
   r.long_rows = s.long_rows = reinterpret_cast<int32_t*>(scratch + g.long_rows);
   r.partial = reinterpret_cast<float*>(scratch + g.partial);
-  s.bits = g.low_bits;
+  r.present_row = s.present_row = static_cast<uint32_t>(g.present_row);
+  s.low_bits = g.low_bits;
+  s.high_bits = g.bits - g.low_bits;
   gc_status st;
-  if (g.low_bits == g.bits) {
+  if (g.chunks == c.nranks) {
+    void* params[] = {&s};
+    const size_t lds = size_t(kSortWaves) * 4 << std::max(s.low_bits, s.high_bits);
+    st = gci::hip_status(hipLaunchKernel(reinterpret_cast<const void*>(sort_alone_kernel<P>), dim3(c.nranks), dim3(kSortThreads), params,
+                                         lds, c.stream));
+  } else if (s.high_bits == 0) {
     st = sort_pass<true, true, P>(s, g, c.stream);
   } else {
     st = sort_pass<true, false, P>(s, g, c.stream);
     if (st != GC_OK) return st;
-    s.shift = g.low_bits;
-    s.bits = g.bits - g.low_bits;
     st = sort_pass<false, true, P>(s, g, c.stream);
   }
   if (st != GC_OK) return st;
   r.H = c.hidden;
   constexpr int VE = sum_unit<In, OutT>();
+  uint64_t m = c.hidden * OutT::ES;
+  for (int k = 0; k < c.nranks; ++k) m |= reinterpret_cast<uint64_t>(c.dw[k]);
+  r.through = m % kLine == 0;
   r.units = (c.hidden + VE - 1) / VE;
   r.pitch = gci::embedding_pitch(c.hidden);
   r.scale = c.scale;
   r.accumulate = c.accumulate;
   r.lanes_log2 = 3;
   while (r.lanes_log2 < 8 && (uint64_t(1) << r.lanes_log2) < r.units) ++r.lanes_log2;
-  return r.units > kThreads ? row_sums<In, OutT, 2, P>(r, long_rows, c.stream)
-                            : row_sums<In, OutT, 1, P>(r, long_rows, c.stream);
+  // units per lane: one, two, or three where that leaves less of the last slice empty (rows a little over 512 units)
+  if (r.units <= kThreads) return row_sums<In, OutT, 1, P>(r, long_rows, c.stream);
+  const uint64_t by2 = (r.units + 2 * kThreads - 1) / (2 * kThreads) * 2, by3 = (r.units + 3 * kThreads - 1) / (3 * kThreads) * 3;
+  return by2 <= by3 ? row_sums<In, OutT, 2, P>(r, long_rows, c.stream) : row_sums<In, OutT, 3, P>(r, long_rows, c.stream);
 }
 
 template <class In, class OutT>

@@ -322,10 +322,10 @@ struct EmbeddingGeom {
   int32_t bits = 0;     // of an id
   int32_t low_bits = 0;
   int32_t run = 0;      // sorted tokens that one group of lanes sums
-  uint64_t pairs = 0, keys = 0, perm = 0, counts = 0, valid = 0, present = 0, long_rows = 0, partial = 0, bytes = 0;
+  uint64_t pairs = 0, keys = 0, perm = 0, counts = 0, valid = 0, present = 0, present_row = 0, long_rows = 0, partial = 0, bytes = 0;
 };
 constexpr int kEmbeddingDigit = 11;   // most bits of a digit
-// Floats of a partial row: hidden rounded up to a unit of either type.
+// Floats of a partial row: whole units of either type.
 inline uint64_t embedding_pitch(uint64_t hidden) { return (hidden + 7) / 8 * 8; }
 EmbeddingGeom embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden);
 

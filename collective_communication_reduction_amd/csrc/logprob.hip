@@ -44,6 +44,19 @@ struct LogprobArgs {
 // Natural exponential; below e^-87 it flushes to 0.
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2E); }
 
+// Unit u of a row of n logits, -inf past its end.
+template <class In>
+__device__ __forceinline__ u32x4 load_own(const char* row, uint64_t n, uint64_t u) {
+  typedef AnyUnit<In> U;
+  const uint32_t left = static_cast<uint32_t>(min<uint64_t>(U::VE, n > u * U::VE ? n - u * U::VE : 0));
+  return U::load(row + u * 16, left, 0, In::ES == 2 ? 0xFF80u : 0xFF800000u);
+}
+template <class In>
+__device__ __forceinline__ void store_own(char* row, uint64_t n, uint64_t u, u32x4 v) {
+  typedef AnyUnit<In> U;
+  U::store(row + u * 16, static_cast<uint32_t>(min<uint64_t>(U::VE, n - u * U::VE)), 0, v, n * In::ES % kLine == 0);
+}
+
 // Sums of a set of logits relative to its maximum.
 struct Stat {
   float m, s, u;
@@ -139,17 +152,16 @@ template <class In, bool ENT>
 __device__ __forceinline__ void put_grads(const RowGrad& g, const char* row, char* out, uint64_t V, uint64_t stride) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;
   const uint64_t units = (stride + VE - 1) / VE;
   for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
     float x[VE];
-    U::widen(U::load(row, V, u, kFill), x);
+    U::widen(load_own<In>(row, V, u), x);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const uint64_t i = u * VE + e;
       x[e] = i < V ? grad_of<ENT>(g, g.scale * (x[e] - g.m), static_cast<int64_t>(i) == g.target) : 0.0f;
     }
-    U::store(out, stride, u, U::narrow(x));
+    store_own<In>(out, stride, u, U::narrow(x));
   }
 }
 
@@ -157,7 +169,6 @@ template <class In, int P>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs<P> a) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;   // -inf
   __shared__ Stat stats[kThreads / kWave];
   __shared__ uint64_t best[kThreads / kWave];
   const int32_t block = a.block0 + blockIdx.x;
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs<P> 
   Stat c{kNegInf, 0.0f, 0.0f};
   for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
     float x[VE];
-    U::widen(U::load(row, a.V, u, kFill), x);
+    U::widen(load_own<In>(row, a.V, u), x);
     add<VE>(c, x, a.scale);
   }
   c = block_stat(c, a.scale, stats);
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs<P> 
     uint64_t b = 0;
     for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
       float x[VE];
-      U::widen(U::load(row, a.V, u, kFill), x);
+      U::widen(load_own<In>(row, a.V, u), x);
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const uint64_t i = u * VE + e, key = i < a.V ? order_key(x[e], static_cast<uint32_t>(i)) : 0;
@@ -226,20 +237,19 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const Logpro
             ENT ? a.dentropy[rank][r] : 0.0f, a.scale, target, lse == kNegInf};
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  constexpr uint32_t kFill = In::ES == 2 ? 0xFF80u : 0xFF800000u;
   const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
   const char* row = a.logits[rank] + off;
   char* out = a.dlogits[rank] + off;
   const uint64_t units = (a.stride + VE - 1) / VE;
   for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
     float x[VE];
-    U::widen(U::load(row, a.V, u, kFill), x);
+    U::widen(load_own<In>(row, a.V, u), x);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const uint64_t i = u * VE + e;
       x[e] = i < a.V ? grad_of<ENT>(g, fmaf(a.scale, x[e], -lse), static_cast<int64_t>(i) == target) : 0.0f;
     }
-    U::store(out, a.stride, u, U::narrow(x));
+    store_own<In>(out, a.stride, u, U::narrow(x));
   }
 }
 

@@ -1,12 +1,14 @@
-// Units of a row at any element alignment: up to 16 bytes in one access, which the
-// hardware takes at every address of the element's size, and the row's last unit
-// element by element where it is short.  One path therefore serves every row
-// length and offset (rows of 31999 bf16 logits read at 94 % of 32000's rate).
+// Units of a row at any element alignment.  A unit is up to 16 bytes in one access,
+// which the hardware takes at every address of the element's size, so one path
+// serves every row length and offset.  The last unit of a row that is no multiple of
+// it is moved inside the row and overlaps the one before: whole accesses only.
 #pragma once
 
 #include "rows.h"
 
 namespace gcdev {
+
+constexpr uint64_t kLine = 128;
 
 template <class In, int N = In::VE>
 struct AnyUnit {
@@ -17,42 +19,48 @@ struct AnyUnit {
   typedef typename std::conditional<In::ES == 2, OutBf16, OutF32>::type Out;
   typedef typename std::conditional<In::ES == 2, uint16_t, uint32_t>::type E;
 
-  // Elements VE u and on of a row of n; `fill` (an element's bits) past its end, where nothing is read.
+  // First element of unit u in a row of n.  Rows shorter than a unit have one at 0.
+  __device__ static __forceinline__ uint32_t start(uint32_t n, uint32_t u) { return n < VE ? 0 : min(u * VE, n - VE); }
+  // VE elements from s on, in a row of n; in a row shorter than that all of it, and `fill` (an element's bits) behind.
   // KEEP: read again soon, may stay in the caches.
   template <bool KEEP = false>
-  __device__ static __forceinline__ T load(const char* row, uint64_t n, uint64_t u, uint32_t fill = 0) {
-    const char* p = row + u * (VE * In::ES);
-    if ((u + 1) * VE <= n) {
-      if constexpr (KEEP) return *reinterpret_cast<const TAny*>(p);
-      else return __builtin_nontemporal_load(reinterpret_cast<const TAny*>(p));
-    }
-    const int k = u * VE < n ? static_cast<int>(n - u * VE) : 0;
-    const E* e = reinterpret_cast<const E*>(p);
+  __device__ static __forceinline__ T load(const char* row, uint32_t n, uint32_t s, uint32_t fill = 0) {
+    const char* p = row + static_cast<uint64_t>(s) * In::ES;
+    if (n < VE) return load_some(p, n, fill);
+    if constexpr (KEEP) return *reinterpret_cast<const TAny*>(p);
+    else return __builtin_nontemporal_load(reinterpret_cast<const TAny*>(p));
+  }
+  // The first k < VE elements at p.
+  __device__ static __forceinline__ T load_some(const char* p, uint32_t k, uint32_t fill) {
     T v;
 #pragma unroll
     for (int i = 0; i < NW; ++i) v[i] = In::ES == 2 ? fill << 16 | fill : fill;
+    const E* e = reinterpret_cast<const E*>(p);
 #pragma unroll
-    for (int i = 0; i < VE - 1; ++i)
+    for (uint32_t i = 0; i < VE - 1; ++i)
       if (i < k) {
         if constexpr (In::ES == 4) v[i] = e[i];
         else v[i / 2] = i % 2 ? (v[i / 2] & 0xFFFFu) | static_cast<uint32_t>(e[i]) << 16 : (v[i / 2] & 0xFFFF0000u) | e[i];
       }
     return v;
   }
-  // Stores what the row holds of the unit.  On a boundary of its size a unit goes through to memory; elsewhere
-  // neighbouring units share lines, and those are left to meet in the L2.
-  __device__ static __forceinline__ void store(char* row, uint64_t n, uint64_t u, T v) {
-    char* p = row + u * (VE * In::ES);
-    if ((u + 1) * VE <= n) {
-      if (reinterpret_cast<uintptr_t>(p) % sizeof(T)) *reinterpret_cast<TAny*>(p) = v;
-      else if constexpr (NW == 4) st16p<gci::kStoreDevNT>(p, v);
-      else __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
-      return;
-    }
+  // VE elements from s on, or all of a shorter row.  through: to memory, past the L2; for rows that all start on a
+  // line of memory (kLine).  Others share lines with their neighbours and are left to meet there.  Rows of 4092 fp32,
+  // whole units but not lines, take 5 % less time so; and a line that is written both ways takes a multiple (rows of
+  // 4095 bf16: 0.8 TB/s where the units on a 16-byte boundary went through, 5.4 where none did).
+  __device__ static __forceinline__ void store(char* row, uint32_t n, uint32_t s, T v, bool through) {
+    char* p = row + static_cast<uint64_t>(s) * In::ES;
+    if (n < VE) store_some(p, 0, n, v);
+    else if (!through) *reinterpret_cast<TAny*>(p) = v;
+    else if constexpr (NW == 4) st16p<gci::kStoreDevNT>(p, v);
+    else __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
+  }
+  // Elements lo .. hi - 1 of a unit at p.
+  __device__ static __forceinline__ void store_some(char* p, uint32_t lo, uint32_t hi, T v) {
     E* e = reinterpret_cast<E*>(p);
 #pragma unroll
-    for (int i = 0; i < VE - 1; ++i)
-      if (u * VE + i < n) e[i] = static_cast<E>(In::ES == 4 ? v[i] : v[i / 2] >> 16 * (i % 2));
+    for (uint32_t i = 0; i < VE; ++i)
+      if (i >= lo && i < hi) e[i] = static_cast<E>(In::ES == 4 ? v[i] : v[i / 2] >> 16 * (i % 2));
   }
   __device__ static __forceinline__ void widen(const T& v, float (&x)[VE]) {
 #pragma unroll
