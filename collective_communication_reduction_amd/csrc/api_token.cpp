@@ -13,6 +13,7 @@ using namespace gca;
 
 constexpr size_t kMaxVocab = size_t(1) << 22;   // of an embedding: two digits of gci::kEmbeddingDigit bits
 constexpr int kMaxTop = 64;
+constexpr float kMaxScale = 0x1p64f;            // of logits: times log2(e) it stays a number
 
 gc_status check_row_type(gc_dtype t) {
   if (t != GC_MX8 && !valid_dtype(t)) return GC_ERR_INVALID_ARG;
@@ -149,7 +150,7 @@ gc_status logprob_sizes(const int64_t* ntokens, int nranks, size_t vocab, int to
 
 // What both directions check.
 gc_status logprob_check(const gci::LogprobCall& c, Buffers& b) {
-  if (c.stride < c.vocab || !std::isfinite(c.scale) || !(c.scale > 0.0f)) return GC_ERR_INVALID_ARG;
+  if (c.stride < c.vocab || !(c.scale > 0.0f && c.scale <= kMaxScale)) return GC_ERR_INVALID_ARG;
   if (c.stride > kMaxRow) return GC_ERR_UNSUPPORTED;
   GC_TRY(check_row_type(c.t));
   const size_t es = elem_bytes(c.t);

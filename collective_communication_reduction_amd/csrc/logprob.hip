@@ -1,12 +1,15 @@
 // Log probabilities of given tokens, the entropy of their distribution, its most
 // likely tokens, and the gradient of the logits, for gfx950.
 //
-//   z = scale * x,  m = max x,  d = scale * (x - m),  S = sum e^d,  U = sum d e^d
-//   lse = scale * m + log S,  log p = d - log S,  entropy = log S - U / S
-//   dx = scale * (dlogprob * ([target] - p) - dentropy * p * (log p + entropy))
+//   t = x scale log2(e) - r,  S = sum 2^t,  U = sum t 2^t      (r: the largest x times scale log2(e))
+//   lse = ln2 (r + log2 S),  log p = ln2 (t - log2 S),  entropy = ln2 (log2 S - U / S)
+//   dx = scale (dlogprob ([target] - p) - dentropy p (log p + entropy))
 //
-// One pass over a row keeps the running maximum m and rescales S and U when it
-// grows; sums are fp32.
+// One pass: a group of lanes (a wavefront or a workgroup) holds a row in registers,
+// each lane takes its own values' maximum and sums relative to it, and the lanes'
+// sums are joined at the end.  Longer rows go through the registers in tiles, and
+// only their gradient reads them again.  HBM bytes bound it: about ten vector
+// operations a value, four of them the exponential's quarter rate.
 
 #include <type_traits>
 
@@ -17,8 +20,11 @@ namespace {
 using namespace gcdev;
 
 constexpr float kLog2E = 1.44269504088896340736f;
-constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_huge_valf();
 constexpr float kFarBelow = -1e30f;   // in place of -inf where it meets a factor of 0
+
+enum Mode { kStats, kTop, kGrad };    // what a kernel does besides the sums
 
 template <int P>
 struct LogprobArgs {
@@ -32,230 +38,377 @@ struct LogprobArgs {
   const float* dlogprob[P];
   const float* dentropy[P];
   char* dlogits[P];
+  int64_t rows[P];
   int32_t tile0[P + 1];
   uint32_t block0;
   int32_t N;
   int32_t top;
   float scale;
-  uint64_t V;
-  uint64_t stride;
+  uint32_t V;
+  uint32_t stride;
+  bool through;   // every row of dlogits starts on a line
 };
 
-// Natural exponential; below e^-87 it flushes to 0.
-__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2E); }
+__device__ __forceinline__ float exp2_of(float t) { return __builtin_amdgcn_exp2f(t); }  // below 2^-126: 0
 
 // Unit u of a row of n logits, -inf past its end.
 template <class In>
-__device__ __forceinline__ u32x4 load_own(const char* row, uint64_t n, uint64_t u) {
+__device__ __forceinline__ u32x4 load_logits(const char* row, uint32_t n, uint32_t u) {
   typedef AnyUnit<In> U;
-  const uint32_t left = static_cast<uint32_t>(min<uint64_t>(U::VE, n > u * U::VE ? n - u * U::VE : 0));
-  return U::load(row + u * 16, left, 0, In::ES == 2 ? 0xFF80u : 0xFF800000u);
-}
-template <class In>
-__device__ __forceinline__ void store_own(char* row, uint64_t n, uint64_t u, u32x4 v) {
-  typedef AnyUnit<In> U;
-  U::store(row + u * 16, static_cast<uint32_t>(min<uint64_t>(U::VE, n - u * U::VE)), 0, v, n * In::ES % kLine == 0);
+  const uint32_t at = u * U::VE, left = n > at ? min(n - at, static_cast<uint32_t>(U::VE)) : 0;
+  return U::load(row + static_cast<uint64_t>(u) * 16, left, 0, In::ES == 2 ? 0xFF80u : 0xFF800000u);
 }
 
-// Sums of a set of logits relative to its maximum.
+// Sums of a set of logits relative to r; r is -inf for a set without a finite one.
 struct Stat {
-  float m, s, u;
+  float r, s, u;
 };
 
-// c.s and c.u of values at maximum c.m, taken to a maximum of m.
-__device__ __forceinline__ void raise(Stat& c, float m, float scale) {
-  const float d = c.m == m ? 0.0f : fmaxf(scale * (c.m - m), kFarBelow);
-  const float f = exp_of(d);
+// c's sums relative to r.
+__device__ __forceinline__ void raise(Stat& c, float r) {
+  const float d = c.r == r ? 0.0f : fmaxf(c.r - r, kFarBelow), f = exp2_of(d);
   c.u = f * fmaf(c.s, d, c.u);
   c.s *= f;
-  c.m = m;
+  c.r = r;
 }
 
-__device__ __forceinline__ Stat join(Stat a, Stat b, float scale) {
-  const float m = fmaxf(a.m, b.m);
-  raise(a, m, scale);
-  raise(b, m, scale);
-  return Stat{m, a.s + b.s, a.u + b.u};
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+  const float r = fmaxf(a.r, b.r);
+  raise(a, r);
+  raise(b, r);
+  return Stat{r, a.s + b.s, a.u + b.u};
 }
 
+// Sum of VE values in a tree.
 template <int VE>
-__device__ __forceinline__ void add(Stat& c, const float (&x)[VE], float scale) {
-  float m = c.m;
-#pragma unroll
-  for (int e = 0; e < VE; ++e) m = fmaxf(m, x[e]);
-  if (m > c.m) raise(c, m, scale);
-  const float base = m == kNegInf ? 0.0f : m;
-#pragma unroll
-  for (int e = 0; e < VE; ++e) {
-    const float d = scale * (x[e] - base), p = exp_of(d);
-    c.s += p;
-    c.u = fmaf(p, fmaxf(d, kFarBelow), c.u);
-  }
+__device__ __forceinline__ float tree(const float (&x)[VE]) {
+  if constexpr (VE == 8) return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  else return (x[0] + x[1]) + (x[2] + x[3]);
 }
 
-// The workgroup's Stat; every lane gets it.
-__device__ __forceinline__ Stat block_stat(Stat c, float scale, Stat* lds) {
+// Adds NV units to a lane's sums; c2 = scale log2(e).  Returns the units' maximum (NaN left out).
+template <class In, int NV>
+__device__ __forceinline__ float add(Stat& c, const u32x4 (&x)[NV], float c2) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE;
+  float m = -kInf;
 #pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1)
-    c = join(c, Stat{__shfl_xor(c.m, o), __shfl_xor(c.s, o), __shfl_xor(c.u, o)}, scale);
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = c;
-  __syncthreads();
-  c = lds[0];
-  for (int w = 1; w < kThreads / kWave; ++w) c = join(c, lds[w], scale);
-  __syncthreads();
+  for (int j = 0; j < NV; ++j) {
+    float v[VE];
+    U::widen(x[j], v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) m = fmaxf(m, v[e]);
+  }
+  const float r = m * c2;
+  if (r > c.r) raise(c, r);
+  const float base = c.r == -kInf ? 0.0f : c.r;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float v[VE], p[VE];
+    U::widen(x[j], v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float t = fmaf(v[e], c2, -base);
+      p[e] = exp2_of(t);
+      v[e] = p[e] * fmaxf(t, kFarBelow);
+    }
+    c.s += tree<VE>(p);
+    c.u += tree<VE>(v);
+  }
+  return m;
+}
+
+// The group's Stat; every lane gets it.  lds: one per wavefront.
+template <int LANES>
+__device__ __forceinline__ Stat group_stat(Stat c, Stat* lds) {
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) c = join(c, Stat{__shfl_xor(c.r, o), __shfl_xor(c.s, o), __shfl_xor(c.u, o)});
+  if constexpr (LANES > kWave) {
+    constexpr int W = LANES / kWave;
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = c;
+    __syncthreads();
+    c = lds[threadIdx.x % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) c = join(c, Stat{__shfl_xor(c.r, o), __shfl_xor(c.s, o), __shfl_xor(c.u, o)});
+  }
   return c;
 }
 
-// Order of the alternatives: by value, then the lowest token first; 0 is below every value.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t id) {
-  const uint32_t b = __float_as_uint(x + 0.0f);   // -0 counts as 0
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return x != x ? 0 : static_cast<uint64_t>(k) << 32 | (0xFFFFFFFFu - id);
-}
-
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int o) {
-  const uint32_t lo = __shfl_xor(static_cast<uint32_t>(x), o), hi = __shfl_xor(static_cast<uint32_t>(x >> 32), o);
-  return static_cast<uint64_t>(hi) << 32 | lo;
-}
-
-__device__ __forceinline__ uint64_t block_max(uint64_t x, uint64_t* lds) {
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) {
-    const uint64_t y = shfl_xor64(x, o);
-    x = x > y ? x : y;
-  }
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
-  __syncthreads();
-  x = lds[0];
-  for (int w = 1; w < kThreads / kWave; ++w) x = x > lds[w] ? x : lds[w];
-  __syncthreads();
-  return x;
-}
-
-// What the gradient of one row needs.
-struct RowGrad {
-  float m, log_s, inv_s, entropy, dlp, dent, scale;
-  int32_t target;
-  bool empty;
+// ------------------------------------------------------------- alternatives
+//
+// A wavefront keeps its best candidates in order, one per lane.  Value v of token
+// id comes before another if it is larger, or equal and of a lower id; a lane
+// without a candidate holds (-inf, ~0), behind every real one.  NaN is never one.
+struct Best {
+  float v;
+  uint32_t id;
 };
 
-// log p of one logit and its gradient.
-template <bool ENT>
-__device__ __forceinline__ float grad_of(const RowGrad& g, float d, bool target) {
-  const float p = exp_of(d) * g.inv_s;
-  float v = g.dlp * ((target ? 1.0f : 0.0f) - p);
-  if constexpr (ENT) v -= g.dent * (p * (fmaxf(d - g.log_s, kFarBelow) + g.entropy));
-  return g.empty ? 0.0f : v * g.scale;
+__device__ __forceinline__ bool before(float v, uint32_t id, const Best& b) { return v > b.v || (v == b.v && id < b.id); }
+
+// Inserts the same (v, id) on every lane.
+__device__ __forceinline__ void insert(Best& list, float v, uint32_t id) {
+  const int at = __popcll(__ballot(before(list.v, list.id, Best{v, id})));
+  const int lane = threadIdx.x % kWave;
+  // the list one lane further up
+  const float pv = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(list.v), 0x138, 0xF, 0xF, false));
+  const uint32_t pid = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(list.id), 0x138, 0xF, 0xF, false));
+  if (lane == at) list = Best{v, id};
+  else if (lane > at) list = Best{pv, pid};
 }
 
-template <class In, bool ENT>
-__device__ __forceinline__ void put_grads(const RowGrad& g, const char* row, char* out, uint64_t V, uint64_t stride) {
+__device__ __forceinline__ Best last_of(const Best& list, int k) {
+  return Best{__int_as_float(__builtin_amdgcn_readlane(__float_as_int(list.v), k - 1)),
+              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(list.id), k - 1))};
+}
+
+// Offers each lane's (v, id) where ok; tail: the list's k-th.
+__device__ __forceinline__ void offer(Best& list, Best& tail, int k, bool ok, float v, uint32_t id) {
+  uint64_t todo = __ballot(ok && before(v, id, tail));
+  while (todo) {
+    const int l = __ffsll(static_cast<unsigned long long>(todo)) - 1;
+    const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+    const uint32_t i = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(id), l));
+    insert(list, x, i);
+    tail = last_of(list, k);
+    todo &= todo - 1;
+    todo &= __ballot(ok && before(v, id, tail));
+  }
+}
+
+// A value that at least q of the wavefront's m reach.
+__device__ __forceinline__ float qth_largest(float m, int q) {
+  float t = kInf;
+  for (int i = 0; i < q; ++i) {
+    t = m;
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor(t, o));
+    const uint64_t at = __ballot(m == t);
+    if (at && static_cast<int>(threadIdx.x % kWave) == __ffsll(static_cast<unsigned long long>(at)) - 1) m = -kInf;
+  }
+  return t;
+}
+
+// Offers the tile's values to the wavefront's list.  m: the lane's largest.  Of every wavefront at least
+// ceil(k / wavefronts) lanes reach the threshold, so k values of the tile do, and few others.
+template <class In, int LANES, int NV>
+__device__ __forceinline__ void offer_tile(Best& list, int k, const u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* lds) {
   typedef AnyUnit<In> U;
-  constexpr int VE = U::VE;
-  const uint64_t units = (stride + VE - 1) / VE;
-  for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
-    float x[VE];
-    U::widen(load_own<In>(row, V, u), x);
+  constexpr int VE = U::VE, W = LANES / kWave;
+  float t = qth_largest(m, (k + W - 1) / W);
+  if constexpr (W > 1) {
+    __syncthreads();   // the tile before may still be reading
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = t;
+    __syncthreads();
+    t = lds[threadIdx.x % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor(t, o));
+  }
+  Best tail = last_of(list, k);
+  t = fmaxf(t, tail.v);
+  if (!__any(m >= t)) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float v[VE];
+    U::widen(x[j], v);
+    float most = v[0];
+#pragma unroll
+    for (int e = 1; e < VE; ++e) most = fmaxf(most, v[e]);
+    if (!__any(most >= t)) continue;
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const uint64_t i = u * VE + e;
-      x[e] = i < V ? grad_of<ENT>(g, g.scale * (x[e] - g.m), static_cast<int64_t>(i) == g.target) : 0.0f;
+      const uint32_t id = (u0 + j * LANES) * VE + e;
+      offer(list, tail, k, v[e] >= t && id < V, v[e], id);
     }
-    store_own<In>(out, stride, u, U::narrow(x));
   }
+}
+
+// The group's list from the wavefronts'; whole on the first wavefront.
+template <int LANES>
+__device__ __forceinline__ void join_lists(Best& list, int k, Best (*lds)[kWave]) {
+  if constexpr (LANES > kWave) {
+    constexpr int W = LANES / kWave;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    lds[wave][lane] = list;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+      __syncthreads();
+      if (wave % (2 * o) == 0) {
+        Best tail = last_of(list, k);
+        const Best other = lds[wave + o][lane];
+        offer(list, tail, k, lane < k && other.id != ~0u, other.v, other.id);
+        lds[wave][lane] = list;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- gradient
+
+// dx of one logit is -p (a + b t), and `hit` more at the target.  Behind the sums t = x c - r and p = 2^t k with
+// k = 1 / S; from a saved lse t = x scale - lse in natural units and p = e^t: the factor log2(e) is then taken after
+// the difference, which it would round.
+struct RowGrad {
+  float c, r, k, a, b, hit;
+  uint32_t target;   // ~0: none
+};
+
+// Gradients of unit u from its logits, stored; zeros in columns V .. stride - 1.
+template <class In, bool SAVED>
+__device__ __forceinline__ void put_grads(const RowGrad& g, const u32x4& x, char* out, uint32_t u, uint32_t V, uint32_t stride,
+                                          bool through) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE;
+  const uint32_t at = u * VE;
+  if (at >= stride) return;
+  float v[VE];
+  U::widen(x, v);
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    const float t = fmaf(v[e], g.c, -g.r);
+    v[e] = -(exp2_of(SAVED ? t * kLog2E : t) * g.k) * fmaf(g.b, fmaxf(t, kFarBelow), g.a);
+  }
+  if (g.target - at < VE)
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (g.target == at + e) v[e] += g.hit;
+  if (at + VE > V)
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (at + e >= V) v[e] = 0.0f;
+  U::store(out + static_cast<uint64_t>(u) * 16, min(stride - at, static_cast<uint32_t>(VE)), 0, U::narrow(v), through);
+}
+
+// The row's target, ~0 for none.
+template <int P>
+__device__ __forceinline__ uint32_t target_of(const LogprobArgs<P>& a, int rank, int64_t r) {
+  const uint32_t t = a.targets[rank] ? static_cast<uint32_t>(a.targets[rank][r]) : ~0u;
+  return t < a.V ? t : ~0u;
+}
+
+// ------------------------------------------------------------- kernels
+
+// Row of this group, or false past the rank's last.
+template <int LANES, int P>
+__device__ __forceinline__ bool row_of(const LogprobArgs<P>& a, int& rank, int64_t& r) {
+  const int32_t block = a.block0 + blockIdx.x;
+  rank = rank_of<P>(a.tile0, a.N, block);
+  constexpr int GROUPS = LANES == kWave ? kThreads / kWave : 1;
+  r = static_cast<int64_t>(block - a.tile0[rank]) * GROUPS + (GROUPS > 1 ? threadIdx.x / kWave : 0);
+  return r < a.rows[rank];
+}
+
+template <class In, int LANES, int NV, int MODE, int P>
+__global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_kernel(const LogprobArgs<P> a) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE, W = LANES / kWave;
+  __shared__ Stat stats[W];
+  __shared__ float marks[W];
+  __shared__ Best lists[MODE == kTop ? W : 1][kWave];
+  int rank;
+  int64_t r;
+  if (!row_of<LANES, P>(a, rank, r)) return;
+  const int lane = threadIdx.x % LANES;
+  const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
+  const char* row = a.logits[rank] + off;
+  const uint32_t units = (a.V + VE - 1) / VE;
+  const float c2 = a.scale * kLog2E;
+  const uint32_t target = target_of(a, rank, r);
+  const float given = target == ~0u ? 0.0f : In::one(row, target);   // before dlogits may overwrite it
+  Stat c{-kInf, 0.0f, 0.0f};
+  Best list{-kInf, ~0u};
+  u32x4 x[NV];
+  for (uint32_t u0 = lane; u0 - lane < units; u0 += NV * LANES) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
+    const float m = add<In, NV>(c, x, c2);
+    if constexpr (MODE == kTop) offer_tile<In, LANES, NV>(list, a.top, x, m, u0, a.V, marks);
+  }
+  c = group_stat<LANES>(c, stats);
+  const bool empty = c.s == 0.0f && c.r != kInf;
+  if (c.r == kInf) c.s = c.r - c.r;                       // +inf, or a scaled logit past the type's range: NaN
+  const float log2_s = empty ? 0.0f : __log2f(c.s), base = empty ? 0.0f : c.r;
+  const float entropy = empty ? 0.0f : kLn2 * (log2_s - c.u / c.s);
+  const auto log_p = [&](float v) { return empty ? -kInf : kLn2 * (fmaf(v, c2, -base) - log2_s); };
+  if (lane == 0) {
+    if (a.lse[rank]) a.lse[rank][r] = empty ? -kInf : kLn2 * (base + log2_s);
+    if (a.entropy[rank]) a.entropy[rank][r] = entropy;
+    if (a.logprob[rank]) a.logprob[rank][r] = target == ~0u ? 0.0f : log_p(given);
+  }
+  if constexpr (MODE == kTop) {
+    join_lists<LANES>(list, a.top, lists);
+    if (lane < a.top) {
+      a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(list.id);
+      a.top_logprob[rank][r * a.top + lane] = log_p(list.v);
+    }
+  }
+  if constexpr (MODE == kGrad) {
+    const float dlp = target == ~0u || empty ? 0.0f : a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
+    // dlogprob p + dentropy p (ln2 (t - log2 S) + entropy)
+    const float b = a.scale * dent * kLn2;
+    const RowGrad g{c2, base, empty ? 0.0f : 1.0f / c.s, a.scale * (dlp + dent * entropy) - b * log2_s, b, a.scale * dlp, target};
+    char* out = a.dlogits[rank] + off;
+    const uint32_t all = (a.stride + VE - 1) / VE;
+    for (uint32_t u0 = lane; u0 - lane < all; u0 += NV * LANES) {
+      if (all > NV * LANES)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) put_grads<In, false>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
+    }
+  }
+}
+
+// The gradient from the saved lse and entropy.
+template <class In, int LANES, int P>
+__global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const LogprobArgs<P> a) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE, NV = 4;
+  int rank;
+  int64_t r;
+  if (!row_of<LANES, P>(a, rank, r)) return;
+  const int lane = threadIdx.x % LANES;
+  const uint32_t target = target_of(a, rank, r);
+  const float lse = a.lse[rank][r];
+  const bool empty = lse == -kInf;
+  const float dlp = target == ~0u || empty ? 0.0f : a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
+  const float entropy = a.entropy[rank] ? a.entropy[rank][r] : 0.0f;
+  const RowGrad g{a.scale, empty ? 0.0f : lse, empty ? 0.0f : 1.0f, a.scale * (dlp + dent * entropy), a.scale * dent, a.scale * dlp, target};
+  const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
+  const uint32_t units = (a.stride + VE - 1) / VE;
+  for (uint32_t u0 = lane; u0 - lane < units; u0 += NV * LANES) {
+    u32x4 x[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(a.logits[rank] + off, a.V, u0 + j * LANES);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) put_grads<In, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+template <class In, int LANES, int NV, int P>
+gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
+  constexpr int threads = LANES == kWave ? kThreads : LANES;
+  fill_blocks<P>(a.tile0, c.tokens, c.nranks, threads / LANES);
+  const int32_t g = a.tile0[c.nranks];
+  if (c.top) return launch_blocks(logprob_kernel<In, LANES, NV, kTop, P>, a, g, threads, c.stream);
+  return c.dlogits ? launch_blocks(logprob_kernel<In, LANES, NV, kGrad, P>, a, g, threads, c.stream)
+                   : launch_blocks(logprob_kernel<In, LANES, NV, kStats, P>, a, g, threads, c.stream);
 }
 
 template <class In, int P>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs<P> a) {
-  typedef AnyUnit<In> U;
-  constexpr int VE = U::VE;
-  __shared__ Stat stats[kThreads / kWave];
-  __shared__ uint64_t best[kThreads / kWave];
-  const int32_t block = a.block0 + blockIdx.x;
-  const int rank = rank_of<P>(a.tile0, a.N, block);
-  const int64_t r = block - a.tile0[rank];
-  const char* row = a.logits[rank] + static_cast<uint64_t>(r) * a.stride * In::ES;
-  const uint64_t units = (a.V + VE - 1) / VE;
-  Stat c{kNegInf, 0.0f, 0.0f};
-  for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
-    float x[VE];
-    U::widen(load_own<In>(row, a.V, u), x);
-    add<VE>(c, x, a.scale);
-  }
-  c = block_stat(c, a.scale, stats);
-  const bool empty = c.s == 0.0f;
-  const float log_s = empty ? 0.0f : logf(c.s);
-  const float m = empty ? 0.0f : c.m;
-  const float entropy = empty ? 0.0f : log_s - c.u / c.s;
-  int32_t target = a.targets[rank] ? a.targets[rank][r] : -1;
-  if (static_cast<uint32_t>(target) >= a.V) target = -1;
-  if (threadIdx.x == 0) {
-    if (a.lse[rank]) a.lse[rank][r] = empty ? kNegInf : a.scale * m + log_s;
-    if (a.entropy[rank]) a.entropy[rank][r] = entropy;
-    if (a.logprob[rank])
-      a.logprob[rank][r] = target < 0 ? 0.0f : empty ? kNegInf : a.scale * (In::one(row, target) - m) - log_s;
-  }
-  uint64_t prev = ~uint64_t(0);
-  for (int k = 0; k < a.top; ++k) {
-    uint64_t b = 0;
-    for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
-      float x[VE];
-      U::widen(load_own<In>(row, a.V, u), x);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const uint64_t i = u * VE + e, key = i < a.V ? order_key(x[e], static_cast<uint32_t>(i)) : 0;
-        if (key < prev && key > b) b = key;
-      }
-    }
-    prev = block_max(b, best);
-    if (threadIdx.x == 0) {
-      const int64_t at = r * a.top + k;
-      const int32_t id = prev ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(prev)) : -1;
-      a.top_ids[rank][at] = id;
-      a.top_logprob[rank][at] = id < 0 || empty ? (c.s != c.s ? c.s : kNegInf) : a.scale * (In::one(row, id) - m) - log_s;
-    }
-  }
-  if (!a.dlogits[rank]) return;
-  __syncthreads();   // dlogits may be logits: single values of the row were read above
-  const RowGrad g{m, log_s, 1.0f / c.s, entropy, target < 0 ? 0.0f : a.dlogprob[rank][r],
-                  a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f, a.scale, target, empty};
-  char* out = a.dlogits[rank] + static_cast<uint64_t>(r) * a.stride * In::ES;
-  if (a.dentropy[rank]) put_grads<In, true>(g, row, out, a.V, a.stride);
-  else put_grads<In, false>(g, row, out, a.V, a.stride);
-}
-
-// The gradient from the saved lse and entropy: p = e^(z - lse).
-template <class In, bool ENT, int P>
-__global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const LogprobArgs<P> a) {
-  const int32_t block = a.block0 + blockIdx.x;
-  const int rank = rank_of<P>(a.tile0, a.N, block);
-  const int64_t r = block - a.tile0[rank];
-  const float lse = a.lse[rank][r];
-  int32_t target = a.targets[rank][r];
-  if (static_cast<uint32_t>(target) >= a.V) target = -1;
-  const RowGrad g{0.0f, 0.0f, 1.0f, ENT ? a.entropy[rank][r] : 0.0f, target < 0 ? 0.0f : a.dlogprob[rank][r],
-            ENT ? a.dentropy[rank][r] : 0.0f, a.scale, target, lse == kNegInf};
-  typedef AnyUnit<In> U;
-  constexpr int VE = U::VE;
-  const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
-  const char* row = a.logits[rank] + off;
-  char* out = a.dlogits[rank] + off;
-  const uint64_t units = (a.stride + VE - 1) / VE;
-  for (uint64_t u = threadIdx.x; u < units; u += kThreads) {
-    float x[VE];
-    U::widen(load_own<In>(row, a.V, u), x);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const uint64_t i = u * VE + e;
-      x[e] = i < a.V ? grad_of<ENT>(g, fmaf(a.scale, x[e], -lse), static_cast<int64_t>(i) == target) : 0.0f;
-    }
-    store_own<In>(out, a.stride, u, U::narrow(x));
-  }
+gc_status backward_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
+  const bool wave = c.stride <= 4 * kWave * In::VE;   // a wavefront's four units a lane hold a row
+  fill_blocks<P>(a.tile0, c.tokens, c.nranks, wave ? kThreads / kWave : 1);
+  return wave ? launch_blocks(logprob_backward_kernel<In, kWave, P>, a, a.tile0[c.nranks], kThreads, c.stream)
+              : launch_blocks(logprob_backward_kernel<In, kThreads, P>, a, a.tile0[c.nranks], kThreads, c.stream);
 }
 
 template <class In, int P>
 gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   LogprobArgs<P> a{};
+  uint64_t m = c.stride * In::ES;
   for (int s = 0; s < c.nranks; ++s) {
     a.logits[s] = static_cast<const char*>(c.logits[s]);
     if (c.targets) a.targets[s] = c.targets[s];
@@ -267,17 +420,27 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
     if (c.dlogprob) a.dlogprob[s] = c.dlogprob[s];
     if (c.dentropy) a.dentropy[s] = c.dentropy[s];
     if (c.dlogits) a.dlogits[s] = static_cast<char*>(c.dlogits[s]);
+    if (c.dlogits && c.tokens[s]) m |= reinterpret_cast<uint64_t>(c.dlogits[s]);
+    a.rows[s] = c.tokens[s];
   }
-  fill_blocks<P>(a.tile0, c.tokens, c.nranks, 1);
   a.N = c.nranks;
   a.top = c.top;
   a.scale = c.scale;
-  a.V = c.vocab;
-  a.stride = c.stride;
-  const int32_t g = a.tile0[c.nranks];
-  if (!backward) return launch_blocks(logprob_kernel<In, P>, a, g, kThreads, c.stream);
-  return c.dentropy ? launch_blocks(logprob_backward_kernel<In, true, P>, a, g, kThreads, c.stream)
-                    : launch_blocks(logprob_backward_kernel<In, false, P>, a, g, kThreads, c.stream);
+  a.V = static_cast<uint32_t>(c.vocab);
+  a.stride = static_cast<uint32_t>(c.stride);
+  a.through = m % kLine == 0;
+  if (backward) return backward_rows<In, P>(a, c);
+  const uint64_t units = ((c.dlogits ? c.stride : c.vocab) + In::VE - 1) / In::VE;
+  if constexpr (P <= 8) {
+    if (units <= 1 * kWave) return launch_rows<In, kWave, 1, P>(a, c);
+    if (units <= 4 * kWave) return launch_rows<In, kWave, 4, P>(a, c);
+    if (units <= 4 * 256) return launch_rows<In, 256, 4, P>(a, c);
+    if (units <= 4 * 512) return launch_rows<In, 512, 4, P>(a, c);
+    if (units <= 8 * 512) return launch_rows<In, 512, 8, P>(a, c);
+    return launch_rows<In, 1024, 8, P>(a, c);
+  } else {
+    return launch_rows<In, 512, 8, P>(a, c);
+  }
 }
 
 gc_status logprob_any(const gci::LogprobCall& c, bool backward) {
@@ -289,7 +452,18 @@ gc_status logprob_any(const gci::LogprobCall& c, bool backward) {
 
 namespace gci {
 
-gc_status launch_token_logprob(const LogprobCall& c) { return logprob_any(c, false); }
 gc_status launch_token_logprob_backward(const LogprobCall& c) { return logprob_any(c, true); }
+
+gc_status launch_token_logprob(const LogprobCall& c) {
+  if (!c.top || !c.dlogits) return logprob_any(c, false);
+  // both at once are rare: the alternatives first, then the pass with the gradient, which may overwrite the logits
+  LogprobCall part = c;
+  part.dlogits = nullptr;
+  const gc_status st = logprob_any(part, false);
+  if (st != GC_OK) return st;
+  part = c;
+  part.top = 0;
+  return logprob_any(part, false);
+}
 
 }  // namespace gci

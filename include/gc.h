@@ -544,7 +544,7 @@ size_t gc_token_logprob_scratch_bytes(const int64_t* ntokens, int nranks, size_t
 
 /*
  * Log probabilities of given tokens.  Per row, with z = scale * logits (scale a
- * temperature's inverse, > 0):
+ * temperature's inverse, above 0 and at most 2^64):
  *   lse = log(sum of e^z),  p = e^(z - lse),
  *   logprob = z[target] - lse,  entropy = -sum of p * log(p),
  *   and the `top` largest logits: their tokens and log probabilities, in
@@ -565,7 +565,7 @@ size_t gc_token_logprob_scratch_bytes(const int64_t* ntokens, int nranks, size_t
  *               dentropy may be NULL.  All NULL: no gradient.
  *   scratch     DEVICE, 256-byte aligned, gc_token_logprob_scratch_bytes(); calls
  *               that may run at once need one each.
- * Logits of -inf have probability 0.  A row of nothing else has lse and log
+ * Logits of -inf have probability 0; z beyond 2^127 in magnitude counts as infinite.  A row of nothing else has lse and log
  * probabilities of -inf (its target's too), entropy 0 and a zero gradient.  A NaN
  * or +inf makes the row's numbers NaN; NaN logits are never alternatives, and
  * where too few others are left the remaining ids are -1.  Rows of all ranks
