@@ -79,6 +79,13 @@ __device__ __forceinline__ Stat join(Stat a, Stat b) {
   return Stat{r, a.s + b.s, a.u + b.u};
 }
 
+// Keeps the compiler from carrying the widened values of one pass over the registers to the next, at twice their size.
+template <int NV>
+__device__ __forceinline__ void forget(u32x4 (&x)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) asm volatile("" : "+v"(x[j]));
+}
+
 // Sum of VE values in a tree.
 template <int VE>
 __device__ __forceinline__ float tree(const float (&x)[VE]) {
@@ -86,14 +93,18 @@ __device__ __forceinline__ float tree(const float (&x)[VE]) {
   else return (x[0] + x[1]) + (x[2] + x[3]);
 }
 
-// Adds NV units to a lane's sums; c2 = scale log2(e).  Returns the units' maximum (NaN left out).
-template <class In, int NV>
-__device__ __forceinline__ float add(Stat& c, const u32x4 (&x)[NV], float c2) {
+// Adds NV units, those of them that start before unit `units` counted from u0 (the group's first) in steps of LANES, to
+// a lane's sums; c2 = scale log2(e).  Returns their maximum (NaN left out); far is set where an x is -inf.  Such an x
+// makes 0 * -inf of t 2^t: units where that shows are added again with a limit on t, which is one operation in ten that
+// the others save.
+template <class In, int LANES, int NV>
+__device__ __forceinline__ float add(Stat& c, u32x4 (&x)[NV], uint32_t u0, uint32_t units, float c2, bool& far) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
   float m = -kInf;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    if (u0 + j * LANES >= units) break;
     float v[VE];
     U::widen(x[j], v);
 #pragma unroll
@@ -102,19 +113,34 @@ __device__ __forceinline__ float add(Stat& c, const u32x4 (&x)[NV], float c2) {
   const float r = m * c2;
   if (r > c.r) raise(c, r);
   const float base = c.r == -kInf ? 0.0f : c.r;
+  forget(x);
+  float s = 0.0f, u = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    if (u0 + j * LANES >= units) break;
     float v[VE], p[VE];
     U::widen(x[j], v);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float t = fmaf(v[e], c2, -base);
-      p[e] = exp2_of(t);
-      v[e] = p[e] * fmaxf(t, kFarBelow);
+      v[e] = fmaf(v[e], c2, -base);
+      p[e] = exp2_of(v[e]);
+      v[e] *= p[e];
     }
-    c.s += tree<VE>(p);
-    c.u += tree<VE>(v);
+    s += tree<VE>(p);
+    float tu = tree<VE>(v);
+    if (tu != tu) {
+      far = true;
+      asm volatile("" : "+v"(x[j]));
+      U::widen(x[j], v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) v[e] = p[e] * fmaxf(fmaf(v[e], c2, -base), kFarBelow);
+      tu = tree<VE>(v);
+    }
+    u += tu;
   }
+  forget(x);
+  c.s += s;
+  c.u += u;
   return m;
 }
 
@@ -136,9 +162,16 @@ __device__ __forceinline__ Stat group_stat(Stat c, Stat* lds) {
 
 // ------------------------------------------------------------- alternatives
 //
-// A wavefront keeps its best candidates in order, one per lane.  Value v of token
-// id comes before another if it is larger, or equal and of a lower id; a lane
-// without a candidate holds (-inf, ~0), behind every real one.  NaN is never one.
+// Value v of token id comes before another if it is larger, or equal and of a lower
+// id; NaN never counts.  Of every wavefront at least ceil(k / wavefronts) lanes hold
+// a value that reaches the threshold the lanes' maxima give, so k values of a tile do,
+// and few others: these are listed in LDS, and a value's place is the number of
+// listed ones before it.  Where more reach it than the list holds (equal values,
+// rows with few tokens left), the tile's k first are found one after the other.
+
+constexpr int kListed = 512;
+constexpr int kKept = 128;     // listed values that the next tile starts with at most; with the k first of it they fit
+
 struct Best {
   float v;
   uint32_t id;
@@ -146,115 +179,172 @@ struct Best {
 
 __device__ __forceinline__ bool before(float v, uint32_t id, const Best& b) { return v > b.v || (v == b.v && id < b.id); }
 
-// Inserts the same (v, id) on every lane.
-__device__ __forceinline__ void insert(Best& list, float v, uint32_t id) {
-  const int at = __popcll(__ballot(before(list.v, list.id, Best{v, id})));
-  const int lane = threadIdx.x % kWave;
-  // the list one lane further up
-  const float pv = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(list.v), 0x138, 0xF, 0xF, false));
-  const uint32_t pid = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(list.id), 0x138, 0xF, 0xF, false));
-  if (lane == at) list = Best{v, id};
-  else if (lane > at) list = Best{pv, pid};
+struct TopList {
+  Best e[kListed];
+  int n;       // listed, or more than kListed where some found no room
+  float floor; // the threshold that the tiles so far give
+};
+
+// The largest of a wavefront's values, NaN left out; every lane gets it.
+__device__ __forceinline__ float wave_max(float x) {
+  // each step's lanes without a partner keep their own value
+#define GC_STEP(ctrl, rows) \
+  x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), ctrl, rows, 0xF, false)))
+  GC_STEP(0x111, 0xF);   // one lane down the row of 16, two, four, eight
+  GC_STEP(0x112, 0xF);
+  GC_STEP(0x114, 0xF);
+  GC_STEP(0x118, 0xF);
+  GC_STEP(0x142, 0xA);   // row 0 into 1, 2 into 3
+  GC_STEP(0x143, 0xC);   // row 1 into 2 and 3
+#undef GC_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kWave - 1));
 }
 
-__device__ __forceinline__ Best last_of(const Best& list, int k) {
-  return Best{__int_as_float(__builtin_amdgcn_readlane(__float_as_int(list.v), k - 1)),
-              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(list.id), k - 1))};
-}
-
-// Offers each lane's (v, id) where ok; tail: the list's k-th.
-__device__ __forceinline__ void offer(Best& list, Best& tail, int k, bool ok, float v, uint32_t id) {
-  uint64_t todo = __ballot(ok && before(v, id, tail));
-  while (todo) {
-    const int l = __ffsll(static_cast<unsigned long long>(todo)) - 1;
-    const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
-    const uint32_t i = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(id), l));
-    insert(list, x, i);
-    tail = last_of(list, k);
-    todo &= todo - 1;
-    todo &= __ballot(ok && before(v, id, tail));
-  }
-}
-
-// A value that at least q of the wavefront's m reach.
+// A value that at least q lanes' m reach.
 __device__ __forceinline__ float qth_largest(float m, int q) {
   float t = kInf;
   for (int i = 0; i < q; ++i) {
-    t = m;
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor(t, o));
+    t = wave_max(m);
     const uint64_t at = __ballot(m == t);
     if (at && static_cast<int>(threadIdx.x % kWave) == __ffsll(static_cast<unsigned long long>(at)) - 1) m = -kInf;
   }
   return t;
 }
 
-// Offers the tile's values to the wavefront's list.  m: the lane's largest.  Of every wavefront at least
-// ceil(k / wavefronts) lanes reach the threshold, so k values of the tile do, and few others.
+// All lanes of a group have come here, and see each other's LDS.
+template <int LANES>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (LANES > kWave) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Keeps the k first of the listed, in order, and the last of them as the floor.
+template <int LANES>
+__device__ __forceinline__ void keep_first(TopList& list, int k) {
+  const int lane = threadIdx.x % LANES, n = list.n;
+  constexpr int EACH = (kListed + LANES - 1) / LANES;
+  Best b[EACH];
+  int place[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    place[i] = k;
+    if (lane + i * LANES >= n) continue;
+    b[i] = list.e[lane + i * LANES];
+    place[i] = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) place[i] += before(list.e[j].v, list.e[j].id, b[i]);
+  }
+  group_sync<LANES>();
+#pragma unroll
+  for (int i = 0; i < EACH; ++i)
+    if (place[i] < k) list.e[place[i]] = b[i];
+  group_sync<LANES>();
+  if (lane == 0) {
+    list.n = min(n, k);
+    if (n >= k) list.floor = fmaxf(list.floor, list.e[k - 1].v);
+  }
+  group_sync<LANES>();
+}
+
+// The first of the group's (v, id); every lane gets it.
+template <int LANES>
+__device__ __forceinline__ Best group_first(Best b, Best* lds) {
+  const auto take = [&](float v, uint32_t id) {
+    if (before(v, id, b)) b = Best{v, id};
+  };
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) take(__shfl_xor(b.v, o), __shfl_xor(b.id, o));
+  if constexpr (LANES > kWave) {
+    constexpr int W = LANES / kWave;
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = b;
+    __syncthreads();
+    b = lds[threadIdx.x % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) take(__shfl_xor(b.v, o), __shfl_xor(b.id, o));
+    __syncthreads();
+  }
+  return b;
+}
+
+// Lists what the tile holds of the row's k first.  m: the lane's largest value, u0 its first unit.
 template <class In, int LANES, int NV>
-__device__ __forceinline__ void offer_tile(Best& list, int k, const u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* lds) {
+__device__ __forceinline__ void list_tile(TopList& list, int k, u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* marks,
+                                          Best* firsts) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE, W = LANES / kWave;
   float t = qth_largest(m, (k + W - 1) / W);
   if constexpr (W > 1) {
-    __syncthreads();   // the tile before may still be reading
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = t;
+    if (threadIdx.x % kWave == 0) marks[threadIdx.x / kWave] = t;
     __syncthreads();
-    t = lds[threadIdx.x % W];
+    t = marks[threadIdx.x % W];
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor(t, o));
   }
-  Best tail = last_of(list, k);
-  t = fmaxf(t, tail.v);
-  if (!__any(m >= t)) return;
+  t = fmaxf(t, list.floor);
+  const int had = list.n;
+  group_sync<LANES>();
+  if (m >= t) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float v[VE];
-    U::widen(x[j], v);
-    float most = v[0];
+    for (int j = 0; j < NV; ++j) {
+      float v[VE];
+      U::widen(x[j], v);
 #pragma unroll
-    for (int e = 1; e < VE; ++e) most = fmaxf(most, v[e]);
-    if (!__any(most >= t)) continue;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const uint32_t id = (u0 + j * LANES) * VE + e;
-      offer(list, tail, k, v[e] >= t && id < V, v[e], id);
-    }
-  }
-}
-
-// The group's list from the wavefronts'; whole on the first wavefront.
-template <int LANES>
-__device__ __forceinline__ void join_lists(Best& list, int k, Best (*lds)[kWave]) {
-  if constexpr (LANES > kWave) {
-    constexpr int W = LANES / kWave;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    lds[wave][lane] = list;
-#pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-      __syncthreads();
-      if (wave % (2 * o) == 0) {
-        Best tail = last_of(list, k);
-        const Best other = lds[wave + o][lane];
-        offer(list, tail, k, lane < k && other.id != ~0u, other.v, other.id);
-        lds[wave][lane] = list;
+      for (int e = 0; e < VE; ++e) {
+        const uint32_t id = (u0 + j * LANES) * VE + e;
+        if (v[e] >= t && id < V) {
+          const int at = atomicAdd(&list.n, 1);
+          if (at < kListed) list.e[at] = Best{v[e], id};
+        }
       }
     }
   }
+  group_sync<LANES>();
+  forget(x);
+  if (list.n > kListed) {
+    Best last{kInf, 0};
+    bool any = false;      // the first round takes any value
+    for (int i = 0; i < k; ++i) {
+      Best b{-kInf, ~0u};
+      forget(x);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        uint32_t id0 = (u0 + j * LANES) * VE;
+        asm volatile("" : "+v"(id0));   // else every id of the tile is kept in a register over the rounds
+        float v[VE];
+        U::widen(x[j], v);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const uint32_t id = id0 + e;
+          if (id < V && before(v[e], id, b) && (!any || before(last.v, last.id, Best{v[e], id}))) b = Best{v[e], id};
+        }
+      }
+      last = group_first<LANES>(b, firsts);
+      any = true;
+      if (threadIdx.x % LANES == 0) list.e[had + i] = last;
+    }
+    if (threadIdx.x % LANES == 0) list.n = had + k;
+    group_sync<LANES>();
+  }
+  if (threadIdx.x % LANES == 0) list.floor = t;
+  group_sync<LANES>();
 }
 
 // ------------------------------------------------------------- gradient
 
-// dx of one logit is -p (a + b t), and `hit` more at the target.  Behind the sums t = x c - r and p = 2^t k with
-// k = 1 / S; from a saved lse t = x scale - lse in natural units and p = e^t: the factor log2(e) is then taken after
-// the difference, which it would round.
+// dx of one logit is -p (a + b t), and `hit` more at the target.  Behind the sums t = x c - r and p = 2^t k: k = 1 / S,
+// or 1 for bf16 results, whose r holds log2 S too.  SAVED: from a saved lse t = x scale - lse and p = e^t, so that the
+// factor log2(e) does not round before the difference is taken.  FAR: an x may be -inf.
 struct RowGrad {
   float c, r, k, a, b, hit;
   uint32_t target;   // ~0: none
 };
 
 // Gradients of unit u from its logits, stored; zeros in columns V .. stride - 1.
-template <class In, bool SAVED>
+template <class In, bool SAVED, bool FAR>
 __device__ __forceinline__ void put_grads(const RowGrad& g, const u32x4& x, char* out, uint32_t u, uint32_t V, uint32_t stride,
                                           bool through) {
   typedef AnyUnit<In> U;
@@ -266,7 +356,9 @@ __device__ __forceinline__ void put_grads(const RowGrad& g, const u32x4& x, char
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
     const float t = fmaf(v[e], g.c, -g.r);
-    v[e] = -(exp2_of(SAVED ? t * kLog2E : t) * g.k) * fmaf(g.b, fmaxf(t, kFarBelow), g.a);
+    float p = exp2_of(SAVED ? t * kLog2E : t);
+    if (!SAVED && In::ES == 4) p *= g.k;
+    v[e] = -p * fmaf(g.b, FAR ? fmaxf(t, kFarBelow) : t, g.a);
   }
   if (g.target - at < VE)
 #pragma unroll
@@ -303,8 +395,9 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE, W = LANES / kWave;
   __shared__ Stat stats[W];
-  __shared__ float marks[W];
-  __shared__ Best lists[MODE == kTop ? W : 1][kWave];
+  __shared__ float marks[MODE == kTop ? W : 1];
+  __shared__ Best firsts[MODE == kTop ? W : 1];
+  __shared__ TopList lists[MODE != kTop ? 1 : LANES == kWave ? kThreads / kWave : 1];
   int rank;
   int64_t r;
   if (!row_of<LANES, P>(a, rank, r)) return;
@@ -316,13 +409,24 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
   const uint32_t target = target_of(a, rank, r);
   const float given = target == ~0u ? 0.0f : In::one(row, target);   // before dlogits may overwrite it
   Stat c{-kInf, 0.0f, 0.0f};
-  Best list{-kInf, ~0u};
+  TopList& list = lists[MODE == kTop && LANES == kWave ? threadIdx.x / kWave : 0];
+  if constexpr (MODE == kTop) {
+    if (lane == 0) {
+      list.n = 0;
+      list.floor = -kInf;
+    }
+    group_sync<LANES>();
+  }
   u32x4 x[NV];
+  bool far = false;
   for (uint32_t u0 = lane; u0 - lane < units; u0 += NV * LANES) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
-    const float m = add<In, NV>(c, x, c2);
-    if constexpr (MODE == kTop) offer_tile<In, LANES, NV>(list, a.top, x, m, u0, a.V, marks);
+    const float m = add<In, LANES, NV>(c, x, u0 - lane, units, c2, far);
+    if constexpr (MODE == kTop) {
+      if (list.n > kKept) keep_first<LANES>(list, a.top);   // between tiles, for a higher floor
+      list_tile<In, LANES, NV>(list, a.top, x, m, u0, a.V, marks, firsts);
+    }
   }
   c = group_stat<LANES>(c, stats);
   const bool empty = c.s == 0.0f && c.r != kInf;
@@ -336,25 +440,34 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
     if (a.logprob[rank]) a.logprob[rank][r] = target == ~0u ? 0.0f : log_p(given);
   }
   if constexpr (MODE == kTop) {
-    join_lists<LANES>(list, a.top, lists);
+    if (list.n > a.top || a.top > 1) keep_first<LANES>(list, a.top);
     if (lane < a.top) {
-      a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(list.id);
-      a.top_logprob[rank][r * a.top + lane] = log_p(list.v);
+      const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
+      a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(b.id);
+      a.top_logprob[rank][r * a.top + lane] = log_p(b.v);
     }
   }
   if constexpr (MODE == kGrad) {
     const float dlp = target == ~0u || empty ? 0.0f : a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
-    // dlogprob p + dentropy p (ln2 (t - log2 S) + entropy)
-    const float b = a.scale * dent * kLn2;
-    const RowGrad g{c2, base, empty ? 0.0f : 1.0f / c.s, a.scale * (dlp + dent * entropy) - b * log2_s, b, a.scale * dlp, target};
+    // dlogprob p + dentropy p (log p + entropy), log p = ln2 t or ln2 (t - log2 S)
+    const float b = a.scale * dent * kLn2, norm = In::ES == 2 ? log2_s : 0.0f;
+    const RowGrad g{c2, base + norm, empty ? 0.0f : 1.0f / c.s, a.scale * (dlp + dent * entropy) - b * (log2_s - norm), b,
+                    a.scale * dlp, target};
     char* out = a.dlogits[rank] + off;
     const uint32_t all = (a.stride + VE - 1) / VE;
+    // a wavefront takes the limits on t where one of its lanes met a -inf; columns past V are filled with it
+    const bool limits = __any(far) || a.V < all * VE;
     for (uint32_t u0 = lane; u0 - lane < all; u0 += NV * LANES) {
       if (all > NV * LANES)
 #pragma unroll
         for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
+      if (limits) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) put_grads<In, false>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
+        for (int j = 0; j < NV; ++j) put_grads<In, false, true>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) put_grads<In, false, false>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
+      }
     }
   }
 }
@@ -381,7 +494,7 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const Logpro
 #pragma unroll
     for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(a.logits[rank] + off, a.V, u0 + j * LANES);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) put_grads<In, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
+    for (int j = 0; j < NV; ++j) put_grads<In, true, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
   }
 }
 
@@ -434,7 +547,8 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   if constexpr (P <= 8) {
     if (units <= 1 * kWave) return launch_rows<In, kWave, 1, P>(a, c);
     if (units <= 4 * kWave) return launch_rows<In, kWave, 4, P>(a, c);
-    if (units <= 4 * 256) return launch_rows<In, 256, 4, P>(a, c);
+    if (c.top) return units <= 8 * 1024 ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 1024, 8, P>(a, c);
+    if (units <= 4 * 256 || !c.dlogits) return launch_rows<In, 256, 4, P>(a, c);
     if (units <= 4 * 512) return launch_rows<In, 512, 4, P>(a, c);
     if (units <= 8 * 512) return launch_rows<In, 512, 8, P>(a, c);
     return launch_rows<In, 1024, 8, P>(a, c);
