@@ -169,9 +169,25 @@ gc_status logprob_check(const gci::LogprobCall& c, Buffers& b) {
 
 }  // namespace
 
+namespace {
+
+// A workgroup per row leaves most of the chip idle where there are few rows.  Few long ones are cut into parts of 8192
+// logits or more, 256 parts in all, for a second launch to join; one row of 32000 takes as long whole.
+int logprob_parts(const int64_t* ntokens, int nranks, size_t vocab) {
+  int64_t rows = 0;
+  for (int r = 0; r < nranks; ++r) rows += ntokens[r];
+  if (rows == 0 || vocab < 65536) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({gci::kLogprobParts, 256 / rows, static_cast<int64_t>(vocab / 8192)})));
+}
+
+}  // namespace
+
 extern "C" size_t gc_token_logprob_scratch_bytes(const int64_t* ntokens, int nranks, size_t vocab, int top) {
   if (logprob_sizes(ntokens, nranks, vocab, top) != GC_OK) return 0;
-  return 256;
+  const int parts = logprob_parts(ntokens, nranks, vocab);
+  uint64_t rows = 0;
+  for (int r = 0; r < nranks; ++r) rows += ntokens[r];
+  return up256(std::max<uint64_t>(1, parts > 1 ? rows * parts * (16 + 8 * static_cast<uint64_t>(top)) : 0));
 }
 
 extern "C" gc_status gc_token_logprob(const void* const* logits, const int32_t* const* targets, const int64_t* ntokens,
@@ -184,7 +200,7 @@ extern "C" gc_status gc_token_logprob(const void* const* logits, const int32_t* 
   if (!targets != !logprob || !dlogits != !dlogprob || (dentropy && !dlogits) || (dlogits && !targets))
     return GC_ERR_INVALID_ARG;
   const gci::LogprobCall c{logits, targets, ntokens, nranks, vocab, stride, scale, t, logprob, entropy, lse, top,
-                           top_ids, top_logprob, dlogprob, dentropy, dlogits, scratch, stream};
+                           top_ids, top_logprob, dlogprob, dentropy, dlogits, scratch, stream, logprob_parts(ntokens, nranks, vocab)};
   Buffers b;
   GC_TRY(logprob_check(c, b));
   const auto rows = [&](uint64_t bytes) { return [=](int r) { return static_cast<uint64_t>(ntokens[r]) * bytes; }; };

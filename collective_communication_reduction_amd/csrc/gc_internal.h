@@ -386,7 +386,9 @@ struct LogprobCall {
   void* const* dlogits;
   void* scratch;
   hipStream_t stream;
+  int parts = 1;   // of a row where there are few (not with a gradient)
 };
+constexpr int kLogprobParts = 32;   // at most
 gc_status launch_token_logprob(const LogprobCall& call);
 gc_status launch_token_logprob_backward(const LogprobCall& call);
 

@@ -24,7 +24,14 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFarBelow = -1e30f;   // in place of -inf where it meets a factor of 0
 
+constexpr int kMostParts = gci::kLogprobParts;
+
 enum Mode { kStats, kTop, kGrad };    // what a kernel does besides the sums
+
+// What a part of a row leaves for the kernel that joins them.
+struct Part {
+  float r, s, u, pad;
+};
 
 template <int P>
 struct LogprobArgs {
@@ -47,6 +54,9 @@ struct LogprobArgs {
   uint32_t V;
   uint32_t stride;
   bool through;   // every row of dlogits starts on a line
+  int32_t parts;  // of a row, a workgroup each; 1: rows whole
+  Part* part;     // [rows of all ranks][parts]
+  uint64_t* best; // [rows of all ranks][parts][top]: value bits << 32 | id
 };
 
 __device__ __forceinline__ float exp2_of(float t) { return __builtin_amdgcn_exp2f(t); }  // below 2^-126: 0
@@ -72,11 +82,36 @@ __device__ __forceinline__ void raise(Stat& c, float r) {
   c.r = r;
 }
 
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float r = fmaxf(a.r, b.r);
-  raise(a, r);
-  raise(b, r);
-  return Stat{r, a.s + b.s, a.u + b.u};
+// One step of a reduction over a wavefront: lanes read the lane that `ctrl` names, `none` where there is none or
+// their row of 16 is not in `rows`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float x, float none) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(x), CTRL, ROWS, 0xF, false));
+}
+
+// Reduces a wavefront's values with f: one, two, four and eight lanes down each row of 16, then row 0 into 1 and 2 into
+// 3, then 1 into 2 and 3, and the last lane has it all.  About 60 cycles, a tenth of what exchanges through LDS take.
+template <class F>
+__device__ __forceinline__ float wave_reduce(float x, float none, F f) {
+  x = f(x, dpp<0x111, 0xF>(x, none));
+  x = f(x, dpp<0x112, 0xF>(x, none));
+  x = f(x, dpp<0x114, 0xF>(x, none));
+  x = f(x, dpp<0x118, 0xF>(x, none));
+  x = f(x, dpp<0x142, 0xA>(x, none));
+  x = f(x, dpp<0x143, 0xC>(x, none));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kWave - 1));
+}
+
+// The largest of a wavefront's values, NaN left out; every lane gets it, as with the rest.
+__device__ __forceinline__ float wave_max(float x) {
+  return wave_reduce(x, -kInf, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_add(float x) {
+  return wave_reduce(x, 0.0f, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ Stat wave_stat(Stat c) {
+  raise(c, wave_max(c.r));
+  return Stat{c.r, wave_add(c.s), wave_add(c.u)};
 }
 
 // Keeps the compiler from carrying the widened values of one pass over the registers to the next, at twice their size.
@@ -147,15 +182,14 @@ __device__ __forceinline__ float add(Stat& c, u32x4 (&x)[NV], uint32_t u0, uint3
 // The group's Stat; every lane gets it.  lds: one per wavefront.
 template <int LANES>
 __device__ __forceinline__ Stat group_stat(Stat c, Stat* lds) {
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) c = join(c, Stat{__shfl_xor(c.r, o), __shfl_xor(c.s, o), __shfl_xor(c.u, o)});
+  c = wave_stat(c);
   if constexpr (LANES > kWave) {
     constexpr int W = LANES / kWave;
     if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = c;
     __syncthreads();
-    c = lds[threadIdx.x % W];
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) c = join(c, Stat{__shfl_xor(c.r, o), __shfl_xor(c.s, o), __shfl_xor(c.u, o)});
+    c = Stat{-kInf, 0.0f, 0.0f};
+    if (threadIdx.x % kWave < W) c = lds[threadIdx.x % kWave];
+    c = wave_stat(c);
   }
   return c;
 }
@@ -184,21 +218,6 @@ struct TopList {
   int n;       // listed, or more than kListed where some found no room
   float floor; // the threshold that the tiles so far give
 };
-
-// The largest of a wavefront's values, NaN left out; every lane gets it.
-__device__ __forceinline__ float wave_max(float x) {
-  // each step's lanes without a partner keep their own value
-#define GC_STEP(ctrl, rows) \
-  x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), ctrl, rows, 0xF, false)))
-  GC_STEP(0x111, 0xF);   // one lane down the row of 16, two, four, eight
-  GC_STEP(0x112, 0xF);
-  GC_STEP(0x114, 0xF);
-  GC_STEP(0x118, 0xF);
-  GC_STEP(0x142, 0xA);   // row 0 into 1, 2 into 3
-  GC_STEP(0x143, 0xC);   // row 1 into 2 and 3
-#undef GC_STEP
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kWave - 1));
-}
 
 // A value that at least q lanes' m reach.
 __device__ __forceinline__ float qth_largest(float m, int q) {
@@ -270,58 +289,37 @@ __device__ __forceinline__ Best group_first(Best b, Best* lds) {
   return b;
 }
 
-// Lists what the tile holds of the row's k first.  m: the lane's largest value, u0 its first unit.
-template <class In, int LANES, int NV>
-__device__ __forceinline__ void list_tile(TopList& list, int k, u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* marks,
-                                          Best* firsts) {
-  typedef AnyUnit<In> U;
-  constexpr int VE = U::VE, W = LANES / kWave;
+// Lists what a tile holds of the row's k first.  m: the largest of the lane's values; each(f) calls f(v, id) for all of
+// them.
+template <int LANES, class Each>
+__device__ __forceinline__ void list_tile(TopList& list, int k, float m, float* marks, Best* firsts, Each each) {
+  constexpr int W = LANES / kWave;
   float t = qth_largest(m, (k + W - 1) / W);
   if constexpr (W > 1) {
     if (threadIdx.x % kWave == 0) marks[threadIdx.x / kWave] = t;
     __syncthreads();
-    t = marks[threadIdx.x % W];
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor(t, o));
+    for (int w = 0; w < W; ++w) t = fminf(t, marks[w]);
   }
   t = fmaxf(t, list.floor);
   const int had = list.n;
   group_sync<LANES>();
-  if (m >= t) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float v[VE];
-      U::widen(x[j], v);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const uint32_t id = (u0 + j * LANES) * VE + e;
-        if (v[e] >= t && id < V) {
-          const int at = atomicAdd(&list.n, 1);
-          if (at < kListed) list.e[at] = Best{v[e], id};
-        }
+  if (m >= t)
+    each([&](float v, uint32_t id) {
+      if (v >= t) {
+        const int at = atomicAdd(&list.n, 1);
+        if (at < kListed) list.e[at] = Best{v, id};
       }
-    }
-  }
+    });
   group_sync<LANES>();
-  forget(x);
   if (list.n > kListed) {
     Best last{kInf, 0};
     bool any = false;      // the first round takes any value
     for (int i = 0; i < k; ++i) {
       Best b{-kInf, ~0u};
-      forget(x);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        uint32_t id0 = (u0 + j * LANES) * VE;
-        asm volatile("" : "+v"(id0));   // else every id of the tile is kept in a register over the rounds
-        float v[VE];
-        U::widen(x[j], v);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const uint32_t id = id0 + e;
-          if (id < V && before(v[e], id, b) && (!any || before(last.v, last.id, Best{v[e], id}))) b = Best{v[e], id};
-        }
-      }
+      each([&](float v, uint32_t id) {
+        if (before(v, id, b) && (!any || before(last.v, last.id, Best{v, id}))) b = Best{v, id};
+      });
       last = group_first<LANES>(b, firsts);
       any = true;
       if (threadIdx.x % LANES == 0) list.e[had + i] = last;
@@ -331,6 +329,27 @@ __device__ __forceinline__ void list_tile(TopList& list, int k, u32x4 (&x)[NV], 
   }
   if (threadIdx.x % LANES == 0) list.floor = t;
   group_sync<LANES>();
+}
+
+// The same for a tile of logits, u0 the lane's first unit.
+template <class In, int LANES, int NV>
+__device__ __forceinline__ void list_logits(TopList& list, int k, u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* marks,
+                                            Best* firsts) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE;
+  list_tile<LANES>(list, k, m, marks, firsts, [&](auto take) {
+    forget(x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint32_t id = (u0 + j * LANES) * VE;
+      asm volatile("" : "+v"(id));   // else the tile's ids are kept in as many registers from one round to the next
+      float v[VE];
+      U::widen(x[j], v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (id + e < V) take(v[e], id + e);
+    }
+  });
 }
 
 // ------------------------------------------------------------- gradient
@@ -382,15 +401,48 @@ __device__ __forceinline__ uint32_t target_of(const LogprobArgs<P>& a, int rank,
 
 // Row of this group, or false past the rank's last.
 template <int LANES, int P>
-__device__ __forceinline__ bool row_of(const LogprobArgs<P>& a, int& rank, int64_t& r) {
-  const int32_t block = a.block0 + blockIdx.x;
+__device__ __forceinline__ bool row_of(const LogprobArgs<P>& a, int32_t block, int& rank, int64_t& r) {
   rank = rank_of<P>(a.tile0, a.N, block);
   constexpr int GROUPS = LANES == kWave ? kThreads / kWave : 1;
-  r = static_cast<int64_t>(block - a.tile0[rank]) * GROUPS + (GROUPS > 1 ? threadIdx.x / kWave : 0);
+  r = static_cast<int64_t>(block - a.tile0[rank]) * GROUPS + (GROUPS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : 0);
   return r < a.rows[rank];
 }
 
-template <class In, int LANES, int NV, int MODE, int P>
+// A row's numbers from its sums.
+struct RowSums {
+  float c2, base, log2_s, inv_s, entropy;
+  bool empty;
+  __device__ __forceinline__ RowSums(Stat c, float scale) : c2(scale * kLog2E), empty(c.s == 0.0f && c.r != kInf) {
+    if (c.r == kInf) c.s = c.r - c.r;   // +inf, or a scaled logit past the type's range: NaN
+    base = empty ? 0.0f : c.r;
+    log2_s = empty ? 0.0f : __log2f(c.s);
+    inv_s = empty ? 0.0f : 1.0f / c.s;
+    entropy = empty ? 0.0f : kLn2 * (log2_s - c.u * inv_s);
+  }
+  __device__ __forceinline__ float log_p(float x) const { return empty ? -kInf : kLn2 * (fmaf(x, c2, -base) - log2_s); }
+};
+
+// Stores a row's numbers (from one lane); target ~0: none, else its logit is given.
+template <int P>
+__device__ __forceinline__ void put_row(const LogprobArgs<P>& a, int rank, int64_t r, const RowSums& n, uint32_t target, float given) {
+  if (a.lse[rank]) a.lse[rank][r] = n.empty ? -kInf : kLn2 * (n.base + n.log2_s);
+  if (a.entropy[rank]) a.entropy[rank][r] = n.entropy;
+  if (a.logprob[rank]) a.logprob[rank][r] = target == ~0u ? 0.0f : n.log_p(given);
+}
+
+// Stores the alternatives, one per lane.
+template <int LANES, int P>
+__device__ __forceinline__ void put_top(const LogprobArgs<P>& a, int rank, int64_t r, const RowSums& n, TopList& list) {
+  keep_first<LANES>(list, a.top);
+  const int lane = threadIdx.x % LANES;
+  if (lane < a.top) {
+    const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
+    a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(b.id);
+    a.top_logprob[rank][r * a.top + lane] = n.log_p(b.v);
+  }
+}
+
+template <class In, int LANES, int NV, int MODE, bool SPLIT, int P>
 __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_kernel(const LogprobArgs<P> a) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE, W = LANES / kWave;
@@ -400,14 +452,17 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
   __shared__ TopList lists[MODE != kTop ? 1 : LANES == kWave ? kThreads / kWave : 1];
   int rank;
   int64_t r;
-  if (!row_of<LANES, P>(a, rank, r)) return;
+  const int32_t block = a.block0 + blockIdx.x;
+  if (!row_of<LANES, P>(a, SPLIT ? block / a.parts : block, rank, r)) return;
   const int lane = threadIdx.x % LANES;
   const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
   const char* row = a.logits[rank] + off;
-  const uint32_t units = (a.V + VE - 1) / VE;
+  const uint32_t all = (a.V + VE - 1) / VE, share = SPLIT ? (all + a.parts - 1) / a.parts : all;
+  const uint32_t first = SPLIT ? min(block % a.parts * share, all) : 0, units = min(first + share, all);
   const float c2 = a.scale * kLog2E;
-  const uint32_t target = target_of(a, rank, r);
-  const float given = target == ~0u ? 0.0f : In::one(row, target);   // before dlogits may overwrite it
+  const uint32_t target = SPLIT ? ~0u : target_of(a, rank, r);
+  const float dlp = MODE == kGrad && target != ~0u ? a.dlogprob[rank][r] : 0.0f;
+  const float dent = MODE == kGrad && a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
   Stat c{-kInf, 0.0f, 0.0f};
   TopList& list = lists[MODE == kTop && LANES == kWave ? threadIdx.x / kWave : 0];
   if constexpr (MODE == kTop) {
@@ -418,57 +473,106 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
     group_sync<LANES>();
   }
   u32x4 x[NV];
-  bool far = false;
-  for (uint32_t u0 = lane; u0 - lane < units; u0 += NV * LANES) {
+  const uint32_t V = SPLIT ? min(a.V, units * VE) : a.V;             // the logits from there on are the next part's
+  const auto fetch = [&](uint32_t u0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
+    for (int j = 0; j < NV; ++j)
+      x[j] = u0 - lane + j * LANES < units ? load_logits<In>(row, V, u0 + j * LANES) : u32x4{0, 0, 0, 0};
+  };
+  bool far = false;
+  float given = 0.0f;
+  for (uint32_t u0 = first + lane; u0 - lane < units; u0 += NV * LANES) {
+    if constexpr (MODE == kTop)
+      if (list.n > kKept) keep_first<LANES>(list, a.top);            // for a higher floor
+    fetch(u0);
+    if (u0 - lane == first && target != ~0u) given = In::one(row, target);   // before dlogits may overwrite it
     const float m = add<In, LANES, NV>(c, x, u0 - lane, units, c2, far);
-    if constexpr (MODE == kTop) {
-      if (list.n > kKept) keep_first<LANES>(list, a.top);   // between tiles, for a higher floor
-      list_tile<In, LANES, NV>(list, a.top, x, m, u0, a.V, marks, firsts);
-    }
+    if constexpr (MODE == kTop) list_logits<In, LANES, NV>(list, a.top, x, m, u0, V, marks, firsts);
   }
   c = group_stat<LANES>(c, stats);
-  const bool empty = c.s == 0.0f && c.r != kInf;
-  if (c.r == kInf) c.s = c.r - c.r;                       // +inf, or a scaled logit past the type's range: NaN
-  const float log2_s = empty ? 0.0f : __log2f(c.s), base = empty ? 0.0f : c.r;
-  const float entropy = empty ? 0.0f : kLn2 * (log2_s - c.u / c.s);
-  const auto log_p = [&](float v) { return empty ? -kInf : kLn2 * (fmaf(v, c2, -base) - log2_s); };
-  if (lane == 0) {
-    if (a.lse[rank]) a.lse[rank][r] = empty ? -kInf : kLn2 * (base + log2_s);
-    if (a.entropy[rank]) a.entropy[rank][r] = entropy;
-    if (a.logprob[rank]) a.logprob[rank][r] = target == ~0u ? 0.0f : log_p(given);
-  }
-  if constexpr (MODE == kTop) {
-    if (list.n > a.top || a.top > 1) keep_first<LANES>(list, a.top);
-    if (lane < a.top) {
-      const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
-      a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(b.id);
-      a.top_logprob[rank][r * a.top + lane] = log_p(b.v);
-    }
-  }
-  if constexpr (MODE == kGrad) {
-    const float dlp = target == ~0u || empty ? 0.0f : a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
-    // dlogprob p + dentropy p (log p + entropy), log p = ln2 t or ln2 (t - log2 S)
-    const float b = a.scale * dent * kLn2, norm = In::ES == 2 ? log2_s : 0.0f;
-    const RowGrad g{c2, base + norm, empty ? 0.0f : 1.0f / c.s, a.scale * (dlp + dent * entropy) - b * (log2_s - norm), b,
-                    a.scale * dlp, target};
-    char* out = a.dlogits[rank] + off;
-    const uint32_t all = (a.stride + VE - 1) / VE;
-    // a wavefront takes the limits on t where one of its lanes met a -inf; columns past V are filled with it
-    const bool limits = __any(far) || a.V < all * VE;
-    for (uint32_t u0 = lane; u0 - lane < all; u0 += NV * LANES) {
-      if (all > NV * LANES)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u0 + j * LANES);
-      if (limits) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) put_grads<In, false, true>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) put_grads<In, false, false>(g, x[j], out, u0 + j * LANES, a.V, a.stride, a.through);
+  if constexpr (SPLIT) {
+    uint64_t at = block;                                             // rows of all ranks are numbered as their parts are
+    if (lane == 0) a.part[at] = Part{c.r, c.s, c.u, 0.0f};
+    if constexpr (MODE == kTop) {
+      keep_first<LANES>(list, a.top);
+      if (lane < a.top) {
+        const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
+        a.best[at * a.top + lane] = static_cast<uint64_t>(__float_as_uint(b.v)) << 32 | b.id;
       }
     }
+    return;
+  }
+  const RowSums n(c, a.scale);
+  if (lane == 0) put_row(a, rank, r, n, target, given);
+  if constexpr (MODE == kTop) put_top<LANES>(a, rank, r, n, list);
+  if constexpr (MODE == kGrad) {
+    const float hit = n.empty ? 0.0f : a.scale * dlp;
+    // dlogprob p + dentropy p (log p + entropy), log p = ln2 t or ln2 (t - log2 S)
+    const float b = a.scale * dent * kLn2, norm = In::ES == 2 ? n.log2_s : 0.0f;
+    const RowGrad g{c2, n.base + norm, n.inv_s, hit + a.scale * dent * n.entropy - b * (n.log2_s - norm), b, hit, target};
+    char* out = a.dlogits[rank] + off;
+    const uint32_t wide = (a.stride + VE - 1) / VE;
+    // a wavefront takes the limits on t where one of its lanes met a -inf; columns past V are filled with it
+    const bool limits = __any(far) || a.V < wide * VE;
+    for (uint32_t u1 = lane; u1 - lane < wide; u1 += NV * LANES) {
+      if (wide > NV * LANES)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(row, a.V, u1 + j * LANES);
+      if (limits) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) put_grads<In, false, true>(g, x[j], out, u1 + j * LANES, a.V, a.stride, a.through);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) put_grads<In, false, false>(g, x[j], out, u1 + j * LANES, a.V, a.stride, a.through);
+      }
+    }
+  }
+}
+
+// Joins the parts of a row, at most kWave of them.
+template <class In, bool TOP, int P>
+__global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArgs<P> a) {
+  __shared__ float marks[kThreads / kWave];
+  __shared__ Best firsts[kThreads / kWave];
+  __shared__ TopList list;
+  int rank;
+  int64_t r;
+  const int32_t block = a.block0 + blockIdx.x;
+  row_of<kThreads, P>(a, block, rank, r);
+  const uint32_t target = target_of(a, rank, r);
+  const float given = target == ~0u ? 0.0f : In::one(a.logits[rank] + static_cast<uint64_t>(r) * a.stride * In::ES, target);
+  Stat c{-kInf, 0.0f, 0.0f};
+  const int lane = threadIdx.x % kWave;
+  if (lane < a.parts) {
+    const Part p = a.part[static_cast<uint64_t>(block) * a.parts + lane];
+    c = Stat{p.r, p.s, p.u};
+  }
+  c = group_stat<kWave>(c, nullptr);
+  const RowSums n(c, a.scale);
+  if (threadIdx.x == 0) put_row(a, rank, r, n, target, given);
+  if constexpr (TOP) {
+    constexpr int EACH = kMostParts * kWave / kThreads;
+    const int count = a.parts * a.top;
+    const uint64_t* best = a.best + static_cast<uint64_t>(block) * count;
+    uint64_t x[EACH];
+    float m = -kInf;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      x[j] = i < count ? best[i] : 0xFF800000FFFFFFFFull;   // nothing
+      m = fmaxf(m, __uint_as_float(static_cast<uint32_t>(x[j] >> 32)));
+    }
+    if (threadIdx.x == 0) {
+      list.n = 0;
+      list.floor = -kInf;
+    }
+    __syncthreads();
+    list_tile<kThreads>(list, a.top, m, marks, firsts, [&](auto take) {
+#pragma unroll
+      for (int j = 0; j < EACH; ++j)
+        if (static_cast<uint32_t>(x[j]) != ~0u) take(__uint_as_float(static_cast<uint32_t>(x[j] >> 32)), static_cast<uint32_t>(x[j]));
+    });
+    put_top<kThreads>(a, rank, r, n, list);
   }
 }
 
@@ -479,7 +583,7 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const Logpro
   constexpr int VE = U::VE, NV = 4;
   int rank;
   int64_t r;
-  if (!row_of<LANES, P>(a, rank, r)) return;
+  if (!row_of<LANES, P>(a, a.block0 + blockIdx.x, rank, r)) return;
   const int lane = threadIdx.x % LANES;
   const uint32_t target = target_of(a, rank, r);
   const float lse = a.lse[rank][r];
@@ -505,9 +609,23 @@ gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   constexpr int threads = LANES == kWave ? kThreads : LANES;
   fill_blocks<P>(a.tile0, c.tokens, c.nranks, threads / LANES);
   const int32_t g = a.tile0[c.nranks];
-  if (c.top) return launch_blocks(logprob_kernel<In, LANES, NV, kTop, P>, a, g, threads, c.stream);
-  return c.dlogits ? launch_blocks(logprob_kernel<In, LANES, NV, kGrad, P>, a, g, threads, c.stream)
-                   : launch_blocks(logprob_kernel<In, LANES, NV, kStats, P>, a, g, threads, c.stream);
+  if (c.top) return launch_blocks(logprob_kernel<In, LANES, NV, kTop, false, P>, a, g, threads, c.stream);
+  return c.dlogits ? launch_blocks(logprob_kernel<In, LANES, NV, kGrad, false, P>, a, g, threads, c.stream)
+                   : launch_blocks(logprob_kernel<In, LANES, NV, kStats, false, P>, a, g, threads, c.stream);
+}
+
+// Few rows: a workgroup per part, and one per row that joins them.
+template <class In, int P>
+gc_status launch_parts(LogprobArgs<P>& a, const gci::LogprobCall& c) {
+  fill_blocks<P>(a.tile0, c.tokens, c.nranks, 1);
+  const int32_t rows = a.tile0[c.nranks];
+  a.part = static_cast<Part*>(c.scratch);
+  a.best = reinterpret_cast<uint64_t*>(a.part + static_cast<uint64_t>(rows) * a.parts);
+  const gc_status st = c.top ? launch_blocks(logprob_kernel<In, 256, 4, kTop, true, P>, a, rows * a.parts, 256, c.stream)
+                             : launch_blocks(logprob_kernel<In, 256, 4, kStats, true, P>, a, rows * a.parts, 256, c.stream);
+  if (st != GC_OK) return st;
+  return c.top ? launch_blocks(logprob_join_kernel<In, true, P>, a, rows, kThreads, c.stream)
+               : launch_blocks(logprob_join_kernel<In, false, P>, a, rows, kThreads, c.stream);
 }
 
 template <class In, int P>
@@ -543,6 +661,8 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   a.stride = static_cast<uint32_t>(c.stride);
   a.through = m % kLine == 0;
   if (backward) return backward_rows<In, P>(a, c);
+  a.parts = c.dlogits ? 1 : c.parts;
+  if (a.parts > 1) return launch_parts<In, P>(a, c);
   const uint64_t units = ((c.dlogits ? c.stride : c.vocab) + In::VE - 1) / In::VE;
   if constexpr (P <= 8) {
     if (units <= 1 * kWave) return launch_rows<In, kWave, 1, P>(a, c);
