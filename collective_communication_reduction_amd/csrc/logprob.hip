@@ -55,6 +55,7 @@ struct LogprobArgs {
   uint32_t stride;
   bool through;   // every row of dlogits starts on a line
   int32_t parts;  // of a row, a workgroup each; 1: rows whole
+  uint32_t slices;  // of a row in the gradient, a workgroup each
   Part* part;     // [rows of all ranks][parts]
   uint64_t* best; // [rows of all ranks][parts][top]: value bits << 32 | id
 };
@@ -355,8 +356,9 @@ __device__ __forceinline__ void list_logits(TopList& list, int k, u32x4 (&x)[NV]
 // ------------------------------------------------------------- gradient
 
 // dx of one logit is -p (a + b t), and `hit` more at the target.  Behind the sums t = x c - r and p = 2^t k: k = 1 / S,
-// or 1 for bf16 results, whose r holds log2 S too.  SAVED: from a saved lse t = x scale - lse and p = e^t, so that the
-// factor log2(e) does not round before the difference is taken.  FAR: an x may be -inf.
+// or 1 for bf16 results, whose r holds log2 S too.  SAVED: from a saved lse, t = x scale - lse and p = e^t: the factor
+// log2(e) would round lse before the difference is taken, and 1 - p of a sure target is what that leaves.  FAR: an x
+// may be -inf.
 struct RowGrad {
   float c, r, k, a, b, hit;
   uint32_t target;   // ~0: none
@@ -376,7 +378,7 @@ __device__ __forceinline__ void put_grads(const RowGrad& g, const u32x4& x, char
   for (int e = 0; e < VE; ++e) {
     const float t = fmaf(v[e], g.c, -g.r);
     float p = exp2_of(SAVED ? t * kLog2E : t);
-    if (!SAVED && In::ES == 4) p *= g.k;
+    if (!SAVED && In::ES == 4) p *= g.k;   // bf16: r holds log2 S
     v[e] = -p * fmaf(g.b, FAR ? fmaxf(t, kFarBelow) : t, g.a);
   }
   if (g.target - at < VE)
@@ -576,30 +578,34 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
   }
 }
 
-// The gradient from the saved lse and entropy.
+// The gradient from the saved lse and entropy, kSlice units of a row per lane group: workgroups that run side by side
+// then read and write memory side by side.
+constexpr int kSlice = 4;   // units per lane
+
 template <class In, int LANES, int P>
 __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const LogprobArgs<P> a) {
   typedef AnyUnit<In> U;
-  constexpr int VE = U::VE, NV = 4;
+  constexpr int VE = U::VE;
   int rank;
   int64_t r;
-  if (!row_of<LANES, P>(a, a.block0 + blockIdx.x, rank, r)) return;
+  const uint64_t block = a.block0 + static_cast<uint64_t>(blockIdx.x);
+  const uint32_t line = static_cast<uint32_t>(block / a.slices), slice = static_cast<uint32_t>(block - static_cast<uint64_t>(line) * a.slices);
+  if (!row_of<LANES, P>(a, static_cast<int32_t>(line), rank, r)) return;
   const int lane = threadIdx.x % LANES;
   const uint32_t target = target_of(a, rank, r);
   const float lse = a.lse[rank][r];
-  const bool empty = lse == -kInf;
-  const float dlp = target == ~0u || empty ? 0.0f : a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
+  const float dlp = a.dlogprob[rank][r], dent = a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
   const float entropy = a.entropy[rank] ? a.entropy[rank][r] : 0.0f;
-  const RowGrad g{a.scale, empty ? 0.0f : lse, empty ? 0.0f : 1.0f, a.scale * (dlp + dent * entropy), a.scale * dent, a.scale * dlp, target};
   const uint64_t off = static_cast<uint64_t>(r) * a.stride * In::ES;
-  const uint32_t units = (a.stride + VE - 1) / VE;
-  for (uint32_t u0 = lane; u0 - lane < units; u0 += NV * LANES) {
-    u32x4 x[NV];
+  const uint32_t u0 = slice * (kSlice * LANES) + lane;
+  u32x4 x[kSlice];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = load_logits<In>(a.logits[rank] + off, a.V, u0 + j * LANES);
+  for (int j = 0; j < kSlice; ++j) x[j] = load_logits<In>(a.logits[rank] + off, a.V, u0 + j * LANES);
+  const bool empty = lse == -kInf;
+  const float hit = target == ~0u || empty ? 0.0f : a.scale * dlp;
+  const RowGrad g{a.scale, empty ? 0.0f : lse, 1.0f, hit + a.scale * dent * entropy, a.scale * dent, hit, target};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) put_grads<In, true, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
-  }
+  for (int j = 0; j < kSlice; ++j) put_grads<In, true, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
 }
 
 // ------------------------------------------------------------- host side
@@ -630,10 +636,13 @@ gc_status launch_parts(LogprobArgs<P>& a, const gci::LogprobCall& c) {
 
 template <class In, int P>
 gc_status backward_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
-  const bool wave = c.stride <= 4 * kWave * In::VE;   // a wavefront's four units a lane hold a row
+  const uint64_t units = (c.stride + In::VE - 1) / In::VE;
+  const bool wave = units <= kSlice * kWave;   // a wavefront holds a row
   fill_blocks<P>(a.tile0, c.tokens, c.nranks, wave ? kThreads / kWave : 1);
-  return wave ? launch_blocks(logprob_backward_kernel<In, kWave, P>, a, a.tile0[c.nranks], kThreads, c.stream)
-              : launch_blocks(logprob_backward_kernel<In, kThreads, P>, a, a.tile0[c.nranks], kThreads, c.stream);
+  a.slices = wave ? 1 : static_cast<uint32_t>((units + kSlice * kThreads - 1) / (kSlice * kThreads));
+  const uint64_t blocks = static_cast<uint64_t>(a.tile0[c.nranks]) * a.slices;
+  return wave ? launch_blocks(logprob_backward_kernel<In, kWave, P>, a, blocks, kThreads, c.stream)
+              : launch_blocks(logprob_backward_kernel<In, kThreads, P>, a, blocks, kThreads, c.stream);
 }
 
 template <class In, int P>
@@ -667,7 +676,9 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   if constexpr (P <= 8) {
     if (units <= 1 * kWave) return launch_rows<In, kWave, 1, P>(a, c);
     if (units <= 4 * kWave) return launch_rows<In, kWave, 4, P>(a, c);
-    if (c.top) return units <= 8 * 1024 ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 1024, 8, P>(a, c);
+    int64_t rows = 0;
+    for (int s = 0; s < c.nranks; ++s) rows += c.tokens[s];
+    if (c.top) return units <= 8 * 1024 || rows >= 512 ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 1024, 8, P>(a, c);
     if (units <= 4 * 256 || !c.dlogits) return launch_rows<In, 256, 4, P>(a, c);
     if (units <= 4 * 512) return launch_rows<In, 512, 4, P>(a, c);
     if (units <= 8 * 512) return launch_rows<In, 512, 8, P>(a, c);
