@@ -57,7 +57,7 @@ struct LogprobArgs {
   int32_t parts;  // of a row, a workgroup each; 1: rows whole
   uint32_t slices;  // of a row in the gradient, a workgroup each
   Part* part;     // [rows of all ranks][parts]
-  uint64_t* best; // [rows of all ranks][parts][top]: value bits << 32 | id
+  uint64_t* best; // [rows of all ranks][parts][top] keys of the alternatives
 };
 
 __device__ __forceinline__ float exp2_of(float t) { return __builtin_amdgcn_exp2f(t); }  // below 2^-126: 0
@@ -207,15 +207,19 @@ __device__ __forceinline__ Stat group_stat(Stat c, Stat* lds) {
 constexpr int kListed = 512;
 constexpr int kKept = 128;     // listed values that the next tile starts with at most; with the k first of it they fit
 
-struct Best {
-  float v;
-  uint32_t id;
-};
-
-__device__ __forceinline__ bool before(float v, uint32_t id, const Best& b) { return v > b.v || (v == b.v && id < b.id); }
+// A value of a token as one number, larger for what comes first; 0 for nothing.  -0 counts as 0.
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t id) {
+  const uint32_t b = __float_as_uint(v + 0.0f), k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return static_cast<uint64_t>(k) << 32 | ~id;
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t k = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint32_t id_of(uint64_t key) { return ~static_cast<uint32_t>(key); }
 
 struct TopList {
-  Best e[kListed];
+  alignas(16) uint64_t e[kListed];
   int n;       // listed, or more than kListed where some found no room
   float floor; // the threshold that the tiles so far give
 };
@@ -242,58 +246,74 @@ __device__ __forceinline__ void group_sync() {
   }
 }
 
-// Keeps the k first of the listed, in order, and the last of them as the floor.
-template <int LANES>
-__device__ __forceinline__ void keep_first(TopList& list, int k) {
-  const int lane = threadIdx.x % LANES, n = list.n;
-  constexpr int EACH = (kListed + LANES - 1) / LANES;
-  Best b[EACH];
+// Puts the k first of the n listed in order, EACH of them at most per lane.
+template <int LANES, int EACH>
+__device__ __forceinline__ void order_list(TopList& list, int n, int k) {
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x % LANES;
+  uint64_t mine[EACH];
   int place[EACH];
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
-    place[i] = k;
-    if (lane + i * LANES >= n) continue;
-    b[i] = list.e[lane + i * LANES];
+    mine[i] = lane + i * LANES < n ? list.e[lane + i * LANES] : 0;
     place[i] = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) place[i] += before(list.e[j].v, list.e[j].id, b[i]);
+  }
+  for (int j = 0; j < n; j += AHEAD) {
+    uint64_t other[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) other[q] = list.e[j + q];   // kListed is a multiple of AHEAD
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (i * LANES >= n) break;
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) place[i] += j + q < n && other[q] > mine[i];
+    }
   }
   group_sync<LANES>();
 #pragma unroll
   for (int i = 0; i < EACH; ++i)
-    if (place[i] < k) list.e[place[i]] = b[i];
+    if (lane + i * LANES < n && place[i] < k) list.e[place[i]] = mine[i];
+}
+
+// Keeps the k first of the listed, in order, and the last of them as the floor.
+template <int LANES>
+__device__ __forceinline__ void keep_first(TopList& list, int k) {
+  const int lane = threadIdx.x % LANES, n = list.n;
+  if (n <= LANES) order_list<LANES, 1>(list, n, k);
+  else order_list<LANES, (kListed + LANES - 1) / LANES>(list, n, k);
   group_sync<LANES>();
   if (lane == 0) {
     list.n = min(n, k);
-    if (n >= k) list.floor = fmaxf(list.floor, list.e[k - 1].v);
+    if (n >= k) list.floor = fmaxf(list.floor, value_of(list.e[k - 1]));
   }
   group_sync<LANES>();
 }
 
-// The first of the group's (v, id); every lane gets it.
+// The largest of the group's keys; every lane gets it.
 template <int LANES>
-__device__ __forceinline__ Best group_first(Best b, Best* lds) {
-  const auto take = [&](float v, uint32_t id) {
-    if (before(v, id, b)) b = Best{v, id};
+__device__ __forceinline__ uint64_t group_first(uint64_t x, uint64_t* lds) {
+  const auto take = [&](int o) {
+    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(x), o), hi = __shfl_xor(static_cast<uint32_t>(x >> 32), o);
+    x = max(x, static_cast<uint64_t>(hi) << 32 | lo);
   };
 #pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) take(__shfl_xor(b.v, o), __shfl_xor(b.id, o));
+  for (int o = kWave / 2; o > 0; o >>= 1) take(o);
   if constexpr (LANES > kWave) {
     constexpr int W = LANES / kWave;
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = b;
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
     __syncthreads();
-    b = lds[threadIdx.x % W];
+    x = lds[threadIdx.x % W];
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) take(__shfl_xor(b.v, o), __shfl_xor(b.id, o));
+    for (int o = W / 2; o > 0; o >>= 1) take(o);
     __syncthreads();
   }
-  return b;
+  return x;
 }
 
-// Lists what a tile holds of the row's k first.  m: the largest of the lane's values; each(f) calls f(v, id) for all of
-// them.
+// Lists what a tile holds of the row's k first.  m: the largest of the lane's values; each(t, f) calls f(v, id) for those
+// of them that reach t.
 template <int LANES, class Each>
-__device__ __forceinline__ void list_tile(TopList& list, int k, float m, float* marks, Best* firsts, Each each) {
+__device__ __forceinline__ void list_tile(TopList& list, int k, float m, float* marks, uint64_t* firsts, Each each) {
   constexpr int W = LANES / kWave;
   float t = qth_largest(m, (k + W - 1) / W);
   if constexpr (W > 1) {
@@ -306,23 +326,20 @@ __device__ __forceinline__ void list_tile(TopList& list, int k, float m, float* 
   const int had = list.n;
   group_sync<LANES>();
   if (m >= t)
-    each([&](float v, uint32_t id) {
-      if (v >= t) {
-        const int at = atomicAdd(&list.n, 1);
-        if (at < kListed) list.e[at] = Best{v, id};
-      }
+    each(t, [&](float v, uint32_t id) {
+      const int at = atomicAdd(&list.n, 1);
+      if (at < kListed) list.e[at] = key_of(v, id);
     });
   group_sync<LANES>();
   if (list.n > kListed) {
-    Best last{kInf, 0};
-    bool any = false;      // the first round takes any value
+    uint64_t last = ~uint64_t(0);
     for (int i = 0; i < k; ++i) {
-      Best b{-kInf, ~0u};
-      each([&](float v, uint32_t id) {
-        if (before(v, id, b) && (!any || before(last.v, last.id, Best{v, id}))) b = Best{v, id};
+      uint64_t b = 0;
+      each(-kInf, [&](float v, uint32_t id) {
+        const uint64_t key = key_of(v, id);
+        if (key < last) b = max(b, key);
       });
       last = group_first<LANES>(b, firsts);
-      any = true;
       if (threadIdx.x % LANES == 0) list.e[had + i] = last;
     }
     if (threadIdx.x % LANES == 0) list.n = had + k;
@@ -335,20 +352,23 @@ __device__ __forceinline__ void list_tile(TopList& list, int k, float m, float* 
 // The same for a tile of logits, u0 the lane's first unit.
 template <class In, int LANES, int NV>
 __device__ __forceinline__ void list_logits(TopList& list, int k, u32x4 (&x)[NV], float m, uint32_t u0, uint32_t V, float* marks,
-                                            Best* firsts) {
+                                            uint64_t* firsts) {
   typedef AnyUnit<In> U;
   constexpr int VE = U::VE;
-  list_tile<LANES>(list, k, m, marks, firsts, [&](auto take) {
+  list_tile<LANES>(list, k, m, marks, firsts, [&](float t, auto take) {
     forget(x);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      uint32_t id = (u0 + j * LANES) * VE;
-      asm volatile("" : "+v"(id));   // else the tile's ids are kept in as many registers from one round to the next
-      float v[VE];
+      float v[VE], most = -kInf;
       U::widen(x[j], v);
 #pragma unroll
+      for (int e = 0; e < VE; ++e) most = fmaxf(most, v[e]);
+      if (!(most >= t)) continue;
+      uint32_t id = (u0 + j * LANES) * VE;
+      asm volatile("" : "+v"(id));   // else the tile's ids are kept in as many registers from one round to the next
+#pragma unroll
       for (int e = 0; e < VE; ++e)
-        if (id + e < V) take(v[e], id + e);
+        if (v[e] >= t && id + e < V) take(v[e], id + e);
     }
   });
 }
@@ -438,9 +458,9 @@ __device__ __forceinline__ void put_top(const LogprobArgs<P>& a, int rank, int64
   keep_first<LANES>(list, a.top);
   const int lane = threadIdx.x % LANES;
   if (lane < a.top) {
-    const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
-    a.top_ids[rank][r * a.top + lane] = static_cast<int32_t>(b.id);
-    a.top_logprob[rank][r * a.top + lane] = n.log_p(b.v);
+    const bool some = lane < list.n;
+    a.top_ids[rank][r * a.top + lane] = some ? static_cast<int32_t>(id_of(list.e[lane])) : -1;
+    a.top_logprob[rank][r * a.top + lane] = n.log_p(some ? value_of(list.e[lane]) : -kInf);
   }
 }
 
@@ -450,7 +470,7 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
   constexpr int VE = U::VE, W = LANES / kWave;
   __shared__ Stat stats[W];
   __shared__ float marks[MODE == kTop ? W : 1];
-  __shared__ Best firsts[MODE == kTop ? W : 1];
+  __shared__ uint64_t firsts[MODE == kTop ? W : 1];
   __shared__ TopList lists[MODE != kTop ? 1 : LANES == kWave ? kThreads / kWave : 1];
   int rank;
   int64_t r;
@@ -497,10 +517,7 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
     if (lane == 0) a.part[at] = Part{c.r, c.s, c.u, 0.0f};
     if constexpr (MODE == kTop) {
       keep_first<LANES>(list, a.top);
-      if (lane < a.top) {
-        const Best b = lane < list.n ? list.e[lane] : Best{-kInf, ~0u};
-        a.best[at * a.top + lane] = static_cast<uint64_t>(__float_as_uint(b.v)) << 32 | b.id;
-      }
+      if (lane < a.top) a.best[at * a.top + lane] = lane < list.n ? list.e[lane] : 0;
     }
     return;
   }
@@ -535,7 +552,7 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
 template <class In, bool TOP, int P>
 __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArgs<P> a) {
   __shared__ float marks[kThreads / kWave];
-  __shared__ Best firsts[kThreads / kWave];
+  __shared__ uint64_t firsts[kThreads / kWave];
   __shared__ TopList list;
   int rank;
   int64_t r;
@@ -561,18 +578,18 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
       const int i = threadIdx.x + j * kThreads;
-      x[j] = i < count ? best[i] : 0xFF800000FFFFFFFFull;   // nothing
-      m = fmaxf(m, __uint_as_float(static_cast<uint32_t>(x[j] >> 32)));
+      x[j] = i < count ? best[i] : 0;
+      if (x[j]) m = fmaxf(m, value_of(x[j]));
     }
     if (threadIdx.x == 0) {
       list.n = 0;
       list.floor = -kInf;
     }
     __syncthreads();
-    list_tile<kThreads>(list, a.top, m, marks, firsts, [&](auto take) {
+    list_tile<kThreads>(list, a.top, m, marks, firsts, [&](float t, auto take) {
 #pragma unroll
       for (int j = 0; j < EACH; ++j)
-        if (static_cast<uint32_t>(x[j]) != ~0u) take(__uint_as_float(static_cast<uint32_t>(x[j] >> 32)), static_cast<uint32_t>(x[j]));
+        if (x[j] && value_of(x[j]) >= t) take(value_of(x[j]), id_of(x[j]));
     });
     put_top<kThreads>(a, rank, r, n, list);
   }
@@ -674,12 +691,14 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   if (a.parts > 1) return launch_parts<In, P>(a, c);
   const uint64_t units = ((c.dlogits ? c.stride : c.vocab) + In::VE - 1) / In::VE;
   if constexpr (P <= 8) {
-    if (units <= 1 * kWave) return launch_rows<In, kWave, 1, P>(a, c);
     if (units <= 4 * kWave) return launch_rows<In, kWave, 4, P>(a, c);
     int64_t rows = 0;
     for (int s = 0; s < c.nranks; ++s) rows += c.tokens[s];
-    if (c.top) return units <= 8 * 1024 || rows >= 512 ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 1024, 8, P>(a, c);
-    if (units <= 4 * 256 || !c.dlogits) return launch_rows<In, 256, 4, P>(a, c);
+    if (!c.dlogits) {
+      if (rows < 512 && units > 2 * 1024) return launch_rows<In, 1024, 8, P>(a, c);
+      return c.top ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 256, 4, P>(a, c);
+    }
+    if (units <= 4 * 256) return launch_rows<In, 256, 4, P>(a, c);
     if (units <= 4 * 512) return launch_rows<In, 512, 4, P>(a, c);
     if (units <= 8 * 512) return launch_rows<In, 512, 8, P>(a, c);
     return launch_rows<In, 1024, 8, P>(a, c);
