@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, the entropy of their distribution, its most
 // likely tokens, and the gradient of the logits, for gfx950.
 //
-//   t = x scale log2(e) - r,  S = sum 2^t,  U = sum t 2^t      (r: the largest x times scale log2(e))
+//   t = x scale log2(e) - r,  S = sum 2^t,  U = sum t 2^t      (r: the largest x times scale log2(e), rounded)
 //   lse = ln2 (r + log2 S),  log p = ln2 (t - log2 S),  entropy = ln2 (log2 S - U / S)
 //   dx = scale (dlogprob ([target] - p) - dentropy p (log p + entropy))
 //
@@ -23,6 +23,7 @@ constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFarBelow = -1e30f;   // in place of -inf where it meets a factor of 0
+constexpr float kLargest = 0x1p14f;   // of r: its rounding moves t by 2^-11 at most, p by less than half of bf16's rounding
 
 constexpr int kMostParts = gci::kLogprobParts;
 
@@ -70,14 +71,16 @@ __device__ __forceinline__ u32x4 load_logits(const char* row, uint32_t n, uint32
   return U::load(row + static_cast<uint64_t>(u) * 16, left, 0, In::ES == 2 ? 0xFF80u : 0xFF800000u);
 }
 
-// Sums of a set of logits relative to r; r is -inf for a set without a finite one.
+// Sums of a set of logits relative to r, which is -kLargest for what is lower: sums of 0 beside any other logit.  Where
+// the largest r of a row is that, or kLargest and more, its sums are made again from differences of logits.
 struct Stat {
   float r, s, u;
 };
+constexpr Stat kNothing{-kLargest, 0.0f, 0.0f};
 
 // c's sums relative to r.
 __device__ __forceinline__ void raise(Stat& c, float r) {
-  const float d = c.r == r ? 0.0f : fmaxf(c.r - r, kFarBelow), f = exp2_of(d);
+  const float d = c.r - r, f = exp2_of(d);
   c.u = f * fmaf(c.s, d, c.u);
   c.s *= f;
   c.r = r;
@@ -148,7 +151,7 @@ __device__ __forceinline__ float add(Stat& c, u32x4 (&x)[NV], uint32_t u0, uint3
   }
   const float r = m * c2;
   if (r > c.r) raise(c, r);
-  const float base = c.r == -kInf ? 0.0f : c.r;
+  const float base = c.r;
   forget(x);
   float s = 0.0f, u = 0.0f;
 #pragma unroll
@@ -188,11 +191,50 @@ __device__ __forceinline__ Stat group_stat(Stat c, Stat* lds) {
     constexpr int W = LANES / kWave;
     if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = c;
     __syncthreads();
-    c = Stat{-kInf, 0.0f, 0.0f};
+    c = kNothing;
     if (threadIdx.x % kWave < W) c = lds[threadIdx.x % kWave];
     c = wave_stat(c);
   }
   return c;
+}
+
+// The sums of a row whose logits are too large for r, relative to its largest logit m (0 where there is none): t = (x - m)
+// scale log2(e), which is exact where it counts.  lds: one per wavefront, from a group_stat.
+template <class In, int LANES>
+__device__ __forceinline__ Stat sums_from(const char* row, uint32_t V, float c2, Stat* lds, float& m) {
+  typedef AnyUnit<In> U;
+  constexpr int VE = U::VE, W = LANES / kWave;
+  const uint32_t units = (V + VE - 1) / VE, lane = threadIdx.x % LANES;
+  float v[VE];
+  m = -kInf;
+#pragma unroll 1
+  for (uint32_t u = lane; u < units; u += LANES) {
+    U::widen(load_logits<In>(row, V, u), v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) m = fmaxf(m, v[e]);
+  }
+  m = wave_max(m);
+  if constexpr (W > 1) {
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave].r = m;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) m = fmaxf(m, lds[w].r);
+    __syncthreads();
+  }
+  Stat c = kNothing;
+  if (m == kInf) c.s = m - m;   // NaN
+  if (fabsf(m) == kInf) m = 0.0f;
+#pragma unroll 1
+  for (uint32_t u = lane; u < units; u += LANES) {
+    U::widen(load_logits<In>(row, V, u), v);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float t = (v[e] - m) * c2, p = exp2_of(t);
+      c.s += p;
+      c.u += p * fmaxf(t, kFarBelow);
+    }
+  }
+  return group_stat<LANES>(c, lds);
 }
 
 // ------------------------------------------------------------- alternatives
@@ -377,10 +419,10 @@ __device__ __forceinline__ void list_logits(TopList& list, int k, u32x4 (&x)[NV]
 
 // dx of one logit is -p (a + b t), and `hit` more at the target.  Behind the sums t = x c - r and p = 2^t k: k = 1 / S,
 // or 1 for bf16 results, whose r holds log2 S too.  SAVED: from a saved lse, t = x scale - lse and p = e^t: the factor
-// log2(e) would round lse before the difference is taken, and 1 - p of a sure target is what that leaves.  FAR: an x
-// may be -inf.
+// log2(e) would round lse before the difference is taken, and 1 - p of a sure target is what that leaves; t above 0 is
+// lse's own rounding.  FAR: an x may be -inf, and t = (x - m) c - r.
 struct RowGrad {
-  float c, r, k, a, b, hit;
+  float m, c, r, k, a, b, hit;
   uint32_t target;   // ~0: none
 };
 
@@ -396,7 +438,8 @@ __device__ __forceinline__ void put_grads(const RowGrad& g, const u32x4& x, char
   U::widen(x, v);
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
-    const float t = fmaf(v[e], g.c, -g.r);
+    float t = fmaf(FAR && !SAVED ? v[e] - g.m : v[e], g.c, -g.r);
+    if (SAVED) t = t > 0.0f ? 0.0f : t;
     float p = exp2_of(SAVED ? t * kLog2E : t);
     if (!SAVED && In::ES == 4) p *= g.k;   // bf16: r holds log2 S
     v[e] = -p * fmaf(g.b, FAR ? fmaxf(t, kFarBelow) : t, g.a);
@@ -432,22 +475,26 @@ __device__ __forceinline__ bool row_of(const LogprobArgs<P>& a, int32_t block, i
 
 // A row's numbers from its sums.
 struct RowSums {
-  float c2, base, log2_s, inv_s, entropy;
-  bool empty;
-  __device__ __forceinline__ RowSums(Stat c, float scale) : c2(scale * kLog2E), empty(c.s == 0.0f && c.r != kInf) {
-    if (c.r == kInf) c.s = c.r - c.r;   // +inf, or a scaled logit past the type's range: NaN
-    base = empty ? 0.0f : c.r;
+  float c2, m = 0.0f, base, log2_s, inv_s, entropy, lse;
+  bool large, empty;   // large: sums relative to the logit m
+  // c: the sums of the group's lanes; again(m) makes them anew from the row's logits.
+  template <class Again>
+  __device__ __forceinline__ RowSums(Stat c, float scale, Again again) : c2(scale * kLog2E), large(!(fabsf(c.r) < kLargest)) {
+    if (large) c = again(c2, m);
+    empty = c.s == 0.0f;
+    base = large ? 0.0f : c.r;
     log2_s = empty ? 0.0f : __log2f(c.s);
     inv_s = empty ? 0.0f : 1.0f / c.s;
     entropy = empty ? 0.0f : kLn2 * (log2_s - c.u * inv_s);
+    lse = empty ? -kInf : fmaf(scale, m, kLn2 * (base + log2_s));
   }
-  __device__ __forceinline__ float log_p(float x) const { return empty ? -kInf : kLn2 * (fmaf(x, c2, -base) - log2_s); }
+  __device__ __forceinline__ float log_p(float x) const { return empty ? -kInf : kLn2 * (fmaf(x - m, c2, -base) - log2_s); }
 };
 
 // Stores a row's numbers (from one lane); target ~0: none, else its logit is given.
 template <int P>
 __device__ __forceinline__ void put_row(const LogprobArgs<P>& a, int rank, int64_t r, const RowSums& n, uint32_t target, float given) {
-  if (a.lse[rank]) a.lse[rank][r] = n.empty ? -kInf : kLn2 * (n.base + n.log2_s);
+  if (a.lse[rank]) a.lse[rank][r] = n.lse;
   if (a.entropy[rank]) a.entropy[rank][r] = n.entropy;
   if (a.logprob[rank]) a.logprob[rank][r] = target == ~0u ? 0.0f : n.log_p(given);
 }
@@ -485,7 +532,7 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
   const uint32_t target = SPLIT ? ~0u : target_of(a, rank, r);
   const float dlp = MODE == kGrad && target != ~0u ? a.dlogprob[rank][r] : 0.0f;
   const float dent = MODE == kGrad && a.dentropy[rank] ? a.dentropy[rank][r] : 0.0f;
-  Stat c{-kInf, 0.0f, 0.0f};
+  Stat c = kNothing;
   TopList& list = lists[MODE == kTop && LANES == kWave ? threadIdx.x / kWave : 0];
   if constexpr (MODE == kTop) {
     if (lane == 0) {
@@ -521,18 +568,18 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
     }
     return;
   }
-  const RowSums n(c, a.scale);
+  const RowSums n(c, a.scale, [&](float c2, float& m) { return sums_from<In, LANES>(row, a.V, c2, stats, m); });
   if (lane == 0) put_row(a, rank, r, n, target, given);
   if constexpr (MODE == kTop) put_top<LANES>(a, rank, r, n, list);
   if constexpr (MODE == kGrad) {
     const float hit = n.empty ? 0.0f : a.scale * dlp;
     // dlogprob p + dentropy p (log p + entropy), log p = ln2 t or ln2 (t - log2 S)
     const float b = a.scale * dent * kLn2, norm = In::ES == 2 ? n.log2_s : 0.0f;
-    const RowGrad g{c2, n.base + norm, n.inv_s, hit + a.scale * dent * n.entropy - b * (n.log2_s - norm), b, hit, target};
+    const RowGrad g{n.m, c2, n.base + norm, n.inv_s, hit + a.scale * dent * n.entropy - b * (n.log2_s - norm), b, hit, target};
     char* out = a.dlogits[rank] + off;
     const uint32_t wide = (a.stride + VE - 1) / VE;
     // a wavefront takes the limits on t where one of its lanes met a -inf; columns past V are filled with it
-    const bool limits = __any(far) || a.V < wide * VE;
+    const bool limits = __any(far) || n.large || a.V < wide * VE;
     for (uint32_t u1 = lane; u1 - lane < wide; u1 += NV * LANES) {
       if (wide > NV * LANES)
 #pragma unroll
@@ -551,6 +598,7 @@ __global__ void __launch_bounds__(LANES == kWave ? kThreads : LANES) logprob_ker
 // Joins the parts of a row, at most kWave of them.
 template <class In, bool TOP, int P>
 __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArgs<P> a) {
+  __shared__ Stat stats[kThreads / kWave];
   __shared__ float marks[kThreads / kWave];
   __shared__ uint64_t firsts[kThreads / kWave];
   __shared__ TopList list;
@@ -559,16 +607,16 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
   const int32_t block = a.block0 + blockIdx.x;
   row_of<kThreads, P>(a, block, rank, r);
   const uint32_t target = target_of(a, rank, r);
-  const float given = target == ~0u ? 0.0f : In::one(a.logits[rank] + static_cast<uint64_t>(r) * a.stride * In::ES, target);
-  Stat c{-kInf, 0.0f, 0.0f};
+  Stat c = kNothing;
   const int lane = threadIdx.x % kWave;
   if (lane < a.parts) {
     const Part p = a.part[static_cast<uint64_t>(block) * a.parts + lane];
     c = Stat{p.r, p.s, p.u};
   }
   c = group_stat<kWave>(c, nullptr);
-  const RowSums n(c, a.scale);
-  if (threadIdx.x == 0) put_row(a, rank, r, n, target, given);
+  const char* row = a.logits[rank] + static_cast<uint64_t>(r) * a.stride * In::ES;
+  const RowSums n(c, a.scale, [&](float c2, float& m) { return sums_from<In, kThreads>(row, a.V, c2, stats, m); });
+  if (threadIdx.x == 0) put_row(a, rank, r, n, target, target == ~0u ? 0.0f : In::one(row, target));
   if constexpr (TOP) {
     constexpr int EACH = kMostParts * kWave / kThreads;
     const int count = a.parts * a.top;
@@ -620,21 +668,45 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(const Logpro
   for (int j = 0; j < kSlice; ++j) x[j] = load_logits<In>(a.logits[rank] + off, a.V, u0 + j * LANES);
   const bool empty = lse == -kInf;
   const float hit = target == ~0u || empty ? 0.0f : a.scale * dlp;
-  const RowGrad g{a.scale, empty ? 0.0f : lse, 1.0f, hit + a.scale * dent * entropy, a.scale * dent, hit, target};
+  const RowGrad g{0.0f, a.scale, empty ? 0.0f : lse, 1.0f, hit + a.scale * dent * entropy, a.scale * dent, hit, target};
 #pragma unroll
   for (int j = 0; j < kSlice; ++j) put_grads<In, true, true>(g, x[j], a.dlogits[rank] + off, u0 + j * LANES, a.V, a.stride, a.through);
 }
 
 // ------------------------------------------------------------- host side
 
-template <class In, int LANES, int NV, int P>
+template <class In, int MODE, int LANES, int NV, int P>
 gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   constexpr int threads = LANES == kWave ? kThreads : LANES;
   fill_blocks<P>(a.tile0, c.tokens, c.nranks, threads / LANES);
-  const int32_t g = a.tile0[c.nranks];
-  if (c.top) return launch_blocks(logprob_kernel<In, LANES, NV, kTop, false, P>, a, g, threads, c.stream);
-  return c.dlogits ? launch_blocks(logprob_kernel<In, LANES, NV, kGrad, false, P>, a, g, threads, c.stream)
-                   : launch_blocks(logprob_kernel<In, LANES, NV, kStats, false, P>, a, g, threads, c.stream);
+  return launch_blocks(logprob_kernel<In, LANES, NV, MODE, false, P>, a, a.tile0[c.nranks], threads, c.stream);
+}
+
+// Lanes of a row and their units.  A gradient wants the row in registers, and as few of them per lane as the workgroup's
+// 16 wavefronts allow: 32 rows' worth of 16-bit rows of 32000 take 815 us with 512 lanes of 8 units, 830 with 256 of 16
+// (two tiles), 865 with 1024 of 4 (8 x 4096 rows).  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404
+// and 1024 of 4 496; with alternatives 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows), a longer tile's list being
+// worth its registers.  Where rows are too few to fill the chip, more lanes finish one sooner: 64 rows in 20 us with 1024
+// lanes, 26 with 256.
+template <class In, int MODE, int P>
+gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
+  if constexpr (P > 8) {
+    return launch_rows<In, MODE, 512, 8, P>(a, c);   // one form for the many ranks
+  } else {
+    const uint64_t units = ((MODE == kGrad ? c.stride : c.vocab) + In::VE - 1) / In::VE;
+    if (units <= 4 * kWave) return launch_rows<In, MODE, kWave, 4, P>(a, c);
+    if constexpr (MODE == kGrad) {
+      if (units <= 4 * 256) return launch_rows<In, MODE, 256, 4, P>(a, c);
+      if (units <= 4 * 512) return launch_rows<In, MODE, 512, 4, P>(a, c);
+      if (units <= 8 * 512) return launch_rows<In, MODE, 512, 8, P>(a, c);
+      return launch_rows<In, MODE, 1024, 8, P>(a, c);
+    } else {
+      int64_t rows = 0;
+      for (int s = 0; s < c.nranks; ++s) rows += c.tokens[s];
+      if (rows < 512 && units > 2 * 1024) return launch_rows<In, MODE, 1024, 8, P>(a, c);
+      return launch_rows<In, MODE, 256, MODE == kTop ? 8 : 4, P>(a, c);
+    }
+  }
 }
 
 // Few rows: a workgroup per part, and one per row that joins them.
@@ -689,22 +761,8 @@ gc_status logprob_typed(const gci::LogprobCall& c, bool backward) {
   if (backward) return backward_rows<In, P>(a, c);
   a.parts = c.dlogits ? 1 : c.parts;
   if (a.parts > 1) return launch_parts<In, P>(a, c);
-  const uint64_t units = ((c.dlogits ? c.stride : c.vocab) + In::VE - 1) / In::VE;
-  if constexpr (P <= 8) {
-    if (units <= 4 * kWave) return launch_rows<In, kWave, 4, P>(a, c);
-    int64_t rows = 0;
-    for (int s = 0; s < c.nranks; ++s) rows += c.tokens[s];
-    if (!c.dlogits) {
-      if (rows < 512 && units > 2 * 1024) return launch_rows<In, 1024, 8, P>(a, c);
-      return c.top ? launch_rows<In, 256, 8, P>(a, c) : launch_rows<In, 256, 4, P>(a, c);
-    }
-    if (units <= 4 * 256) return launch_rows<In, 256, 4, P>(a, c);
-    if (units <= 4 * 512) return launch_rows<In, 512, 4, P>(a, c);
-    if (units <= 8 * 512) return launch_rows<In, 512, 8, P>(a, c);
-    return launch_rows<In, 1024, 8, P>(a, c);
-  } else {
-    return launch_rows<In, 512, 8, P>(a, c);
-  }
+  if (c.top) return launch_mode<In, kTop, P>(a, c);
+  return c.dlogits ? launch_mode<In, kGrad, P>(a, c) : launch_mode<In, kStats, P>(a, c);
 }
 
 gc_status logprob_any(const gci::LogprobCall& c, bool backward) {

@@ -565,7 +565,9 @@ size_t gc_token_logprob_scratch_bytes(const int64_t* ntokens, int nranks, size_t
  *               dentropy may be NULL.  All NULL: no gradient.
  *   scratch     DEVICE, 256-byte aligned, gc_token_logprob_scratch_bytes(); calls
  *               that may run at once need one each.
- * Logits of -inf have probability 0; z beyond 2^127 in magnitude counts as infinite.  A row of nothing else has lse and log
+ * Logits of -inf have probability 0, and large negative ones that mask beside
+ * others do; a row of one value, whatever its size, is uniform.  A log probability
+ * or lse beyond 2^127 in magnitude counts as infinite.  A row of -inf has lse and log
  * probabilities of -inf (its target's too), entropy 0 and a zero gradient.  A NaN
  * or +inf makes the row's numbers NaN; NaN logits are never alternatives, and
  * where too few others are left the remaining ids are -1.  Rows of all ranks
@@ -583,7 +585,9 @@ gc_status gc_token_logprob(const void* const* logits, const int32_t* const* targ
  *   dlogits = scale * (dlogprob * ([token == target] - p) - dentropy * p * (log(p) + entropy)),
  * fp32, rounded once to t; columns vocab to stride - 1 get zeros.
  *   lse[r], entropy[r], dlogprob[r], dentropy[r]  DEVICE fp32 [ntokens[r]];
- *               dentropy may be NULL, then entropy is not read.
+ *               dentropy may be NULL, then entropy is not read.  p is as exact as
+ *               lse: of one beyond 2^20 in magnitude the fp32 value no longer tells
+ *               p (which stays in 0 .. 1), but the same pass does.
  *   dlogits[r]  DEVICE rows of stride elements of t; may be logits[r] itself.
  */
 gc_status gc_token_logprob_backward(const void* const* logits, const int32_t* const* targets, const float* const* lse,

@@ -73,8 +73,9 @@ def log_softmax(x, scale=1.0):
         m = np.max(z, axis=1, keepdims=True)
         base = np.where(np.isneginf(m), 0.0, m)
         s = np.exp(z - base).sum(1, keepdims=True)
-        lse = base + np.log(s)
-        return np.where(np.isneginf(lse), -np.inf, z - lse), lse[:, 0]
+        log_s = np.log(s)
+        lse = base + log_s
+        return np.where(np.isneginf(lse), -np.inf, z - base - log_s), lse[:, 0]   # lse would round log_s beside a large base
 
 
 def entropy(lp):

@@ -200,6 +200,68 @@ def test_nan_and_infinities(dtype, V):
     assert back[[1, 3]].float().isnan().all() and back[[0, 4]].float().isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e30, "lowest"])
+@pytest.mark.parametrize("V", [9, 1003, 5000, 33000, 140001])
+def test_masks_of_large_values(V, mask, dtype):
+    """Masks that are numbers: beside other logits they weigh nothing, alone they are a row like any other."""
+    rng = np.random.default_rng(V)
+    M = torch.finfo(TYPES[dtype]).min if mask == "lowest" else mask
+    n, top = 7, min(5, V)
+    x = rng.normal(size=(n, V))
+    x[1, rng.random(V) < 0.5] = M
+    few = rng.permutation(V)[:3]
+    x[2, np.setdiff1d(np.arange(V), few)] = M
+    x[3] = M                                                   # nothing left: the same probability for all
+    x[4, few] = -M                                             # as far above
+    x[5] = M * (1 - 0.05 * np.abs(x[5] / 8))                   # all low, of different values
+    x[6, 1:] = M
+    x = torch.from_numpy(x).to(TYPES[dtype])
+    assert x.isfinite().all()
+    x = x.to(DEV)
+    x64 = _f64(x)
+    targets = rng.integers(0, V, n).astype(np.int32)
+    targets[[2, 4]] = few[0]
+    lp, h, lse, tlp = (torch.empty(n, *w, device=DEV) for w in ((), (), (), (top,)))
+    ids, dx, back = torch.empty(n, top, dtype=torch.int32, device=DEV), torch.empty_like(x), torch.empty_like(x)
+    tg, one = torch.from_numpy(targets).to(DEV), torch.ones(n, device=DEV)
+    args = dict(targets=[tg], logprob=[lp], entropy=[h], lse=[lse], top=top, top_ids=[ids], top_logprob=[tlp])
+    scratch = torch.empty(gc.gc_token_logprob_scratch_bytes([n], V, top), dtype=torch.uint8, device=DEV)
+    gc.gc_token_logprob([x], [n], V, scratch, **args)
+    first = [t.clone() for t in (lp, h, lse, ids, tlp)]
+    gc.gc_token_logprob([x], [n], V, scratch, dlogprob=[one], dentropy=[one], dlogits=[dx], **args)
+    gc.gc_token_logprob_backward([x], [n], V, [lse], [tg], [one], [back])
+    want, want_lse = K.log_softmax(x64)
+    rel_s, abs_h = _bounds(x64, want, 1.0, V)
+    # below 2^24 the exponents carry the rounding of the largest logit, above it that of differences
+    big = x64.max(1)
+    big = np.where(np.abs(big) < 2 ** 24, np.abs(big), 0.0)
+    lg = np.log(V)
+
+    def near(got, want, tol):                                  # below -2^127 a number may count as -inf
+        with np.errstate(invalid="ignore"):
+            return ((np.abs(got - want) <= tol) | (np.isneginf(got) & (want < -2.0 ** 127))).all()
+    want_lp, want_h = K.token_logprob(want, targets), K.entropy(want)
+    tol_h = abs_h + 8 * U * (1 + want_h + lg + big)
+    want_ids, want_tlp = K.alternatives(x64, want, top)
+    for lp_, h_, lse_, ids_, tlp_ in (first, (lp, h, lse, ids, tlp)):
+        assert near(_f64(lp_), want_lp, rel_s + 6 * U * (np.abs(want_lp) + lg + big + 1))
+        assert near(_f64(h_), want_h, tol_h)
+        assert near(_f64(lse_), want_lse, rel_s + 4 * U * (np.abs(want_lse) + 2 * big + 1))
+        assert np.array_equal(ids_.cpu().numpy(), want_ids)
+        assert near(_f64(tlp_), want_tlp, (rel_s + 6 * U * (lg + big + 1))[:, None] + 6 * U * np.abs(want_tlp))
+    p, ok = np.exp(want), want > -1e3
+    d = np.where(ok, np.abs(want), 0.0)
+    hit = (np.arange(V) == targets[:, None]) * 1.0
+    dz = hit - p - np.where(ok, p * (want + want_h[:, None]), 0.0)
+    rel_p = rel_s[:, None] + U * (8 + 4 * d + 4 * (lg + big)[:, None])
+    err = p * rel_p + 3 * U * (1 + p) + p * ((d + want_h[:, None]) * (rel_p + 4 * U) + rel_p + tol_h[:, None] + abs_h[:, None])
+    assert (np.abs(_f64(dx) - dz) <= err + (HALF[dtype] + 4 * U) * np.abs(dz) * (1 + 2 ** -8) + 1e-37).all()
+    # a saved lse of a large value is rounded by more than a probability is: the gradient stays within its bounds
+    g = _f64(back)
+    assert (np.abs(g) <= 1).all() and (np.abs(g - (hit - p))[:3] <= (err + (HALF[dtype] + 8 * U) * np.abs(hit - p) * (1 + 2 ** -8) + 1e-37)[:3]).all()
+
+
 @pytest.mark.parametrize("dtype,V", [("bf16", 4099), ("fp32", 33000), ("bf16", 140000)])
 def test_gradient_over_the_logits(dtype, V):
     rng = np.random.default_rng(4)

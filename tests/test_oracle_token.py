@@ -83,3 +83,9 @@ def test_logprob_gradient_against_differences(scale):
         v = rng.normal(size=x.shape)
         h = 1e-6
         assert abs((loss(x + h * v) - loss(x - h * v)) / (2 * h) - (g * v).sum()) < 1e-7
+
+
+def test_log_softmax_of_equal_large_values():
+    for v in (-1e30, 1e30, -1e300):
+        lp, lse = K.log_softmax(np.full((1, 8), v))
+        assert np.allclose(lp, -np.log(8), atol=1e-15) and lse[0] == v
