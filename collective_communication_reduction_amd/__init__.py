@@ -7,8 +7,9 @@ stream, and raises GcError for a non-OK status.  Since the library sees only
 addresses, a tensor is checked here first (a contiguous device tensor that
 holds every byte the call touches, else ValueError; the norm, the 8-bit rows,
 the experts, the combine's gradient, the embedding, dropout and log
-probabilities also check its type, where integer tensors count as raw bits); raw addresses and gc_pointers arrays are the
-caller's responsibility.  Every collective runs in the
+probabilities also check its type, where integer tensors count as raw bits);
+raw addresses and gc_pointers arrays are the caller's responsibility.  Every
+collective runs in the
 HIP kernels of libgc.so; there is no other implementation to fall back to, and
 importing this package fails if the library has not been built
 (python collective_communication_reduction_amd/build.py).

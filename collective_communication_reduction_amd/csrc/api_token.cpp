@@ -55,9 +55,11 @@ extern "C" gc_status gc_embedding(const void* const* weight, const int32_t* cons
   return gci::launch_embedding({weight, tokens, ntokens, nranks, vocab, hidden, scale, t, out, stream});
 }
 
-// Ranks of at most 4096 tokens are sorted by one workgroup each, in one launch; longer ones by a workgroup
-// per 1024 tokens (two of each lane), more where a rank would make over 256 pieces: every piece reads the
-// counts of all the others.
+// Ranks of at most 2048 tokens are sorted by one workgroup each, in one launch (a gradient of 2048 x 256 takes 25 us so,
+// 29 in pieces; 4096 x 256 35 and 30); longer ones by a workgroup per 1024 tokens (two of each lane), more where a rank
+// would make over 256 pieces: every piece reads the counts of all the others.  A group of lanes sums a run of 8 sorted
+// tokens where they are few, for more groups (517 x 1000 fp32: 16 us, 28 with 64), and of up to 64 where those are a
+// thousand, for fewer partial sums (8 x 16384 x 4096 bf16, frequent tokens: 587 us, 604 with 8; none frequent: 635, 608).
 gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden) {
   gci::EmbeddingGeom g;
   int64_t most = 0;
@@ -66,7 +68,7 @@ gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64
     most = std::max(most, tokens[r]);
   }
   const auto up512 = [](int64_t x) { return (std::max<int64_t>(x, 1) + 511) / 512 * 512; };
-  g.chunk = static_cast<int32_t>(most <= 4096 ? up512(most) : std::max<int64_t>(1024, up512(most / 256)));
+  g.chunk = static_cast<int32_t>(most <= 2048 ? up512(most) : std::max<int64_t>(1024, up512(most / 256)));
   for (int r = 0; r < nranks; ++r) g.chunks += static_cast<int32_t>(std::max<int64_t>(1, (tokens[r] + g.chunk - 1) / g.chunk));
   g.bits = 1;
   while (vocab > uint64_t(1) << g.bits) ++g.bits;

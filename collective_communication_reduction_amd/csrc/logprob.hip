@@ -8,8 +8,11 @@
 // One pass: a group of lanes (a wavefront or a workgroup) holds a row in registers,
 // each lane takes its own values' maximum and sums relative to it, and the lanes'
 // sums are joined at the end.  Longer rows go through the registers in tiles, and
-// only their gradient reads them again.  HBM bytes bound it: about ten vector
-// operations a value, four of them the exponential's quarter rate.
+// only their gradient reads them again.  HBM bytes bound it, with about ten vector
+// operations a value, four of them the exponential's quarter rate, close behind:
+// 8 x 4096 rows of 32000 bf16 take 360 us for the sums (5.8 TB/s), 721 with the
+// gradient (5.8 TB/s, read and written); 4 x 2048 rows with five alternatives 110
+// (4.8 TB/s); the gradient from a saved lse of 2 x 1024 x 131072 180 (6.0 TB/s).
 
 #include <type_traits>
 
@@ -644,7 +647,8 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
 }
 
 // The gradient from the saved lse and entropy, kSlice units of a row per lane group: workgroups that run side by side
-// then read and write memory side by side.
+// then read and write memory side by side (sums, then gradient of 2 x 1024 x 131072 bf16: 281 us,
+// 327 with a workgroup per row).
 constexpr int kSlice = 4;   // units per lane
 
 template <class In, int LANES, int P>
@@ -682,12 +686,12 @@ gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   return launch_blocks(logprob_kernel<In, LANES, NV, MODE, false, P>, a, a.tile0[c.nranks], threads, c.stream);
 }
 
-// Lanes of a row and their units.  A gradient wants the row in registers, and as few of them per lane as the workgroup's
-// 16 wavefronts allow: 32 rows' worth of 16-bit rows of 32000 take 815 us with 512 lanes of 8 units, 830 with 256 of 16
-// (two tiles), 865 with 1024 of 4 (8 x 4096 rows).  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404
-// and 1024 of 4 496; with alternatives 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows), a longer tile's list being
-// worth its registers.  Where rows are too few to fill the chip, more lanes finish one sooner: 64 rows in 20 us with 1024
-// lanes, 26 with 256.
+// Lanes of a row and their units.  A wavefront holds a short row: 8 x 16384 rows of 1000 bf16 take 70 us for the sums and
+// 122 with the gradient so, 185 and 275 with 256 lanes (of 2000, the longest: 103 and 215, 187 and 326).  A longer row's
+// gradient wants all of it in registers, in few lanes: of 32000 815 us with 512 lanes of 8 units, 830 with 256 of 16, 865
+// with 1024 of 4 (8 x 4096 rows).  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404 and 1024 of 4 496;
+// with alternatives 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows).  Where rows are too few to fill the chip, more
+// lanes finish one sooner: 64 rows of 32003 fp32 20 us with 1024 lanes, 26 with 256.
 template <class In, int MODE, int P>
 gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   if constexpr (P > 8) {
@@ -709,7 +713,8 @@ gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   }
 }
 
-// Few rows: a workgroup per part, and one per row that joins them.
+// Few rows: a workgroup per part, and one per row that joins them (one row of 131072 bf16 with 20 alternatives: 21 us, 36
+// by one workgroup).
 template <class In, int P>
 gc_status launch_parts(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   fill_blocks<P>(a.tile0, c.tokens, c.nranks, 1);
