@@ -686,12 +686,14 @@ gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   return launch_blocks(logprob_kernel<In, LANES, NV, MODE, false, P>, a, a.tile0[c.nranks], threads, c.stream);
 }
 
-// Lanes of a row and their units.  A wavefront holds a short row: 8 x 16384 rows of 1000 bf16 take 70 us for the sums and
-// 122 with the gradient so, 185 and 275 with 256 lanes (of 2000, the longest: 103 and 215, 187 and 326).  A longer row's
-// gradient wants all of it in registers, in few lanes: of 32000 815 us with 512 lanes of 8 units, 830 with 256 of 16, 865
-// with 1024 of 4 (8 x 4096 rows).  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404 and 1024 of 4 496;
-// with alternatives 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows).  Where rows are too few to fill the chip, more
-// lanes finish one sooner: 64 rows of 32003 fp32 20 us with 1024 lanes, 26 with 256.
+// Lanes of a row and their units.  A wavefront holds a short row: 8 x 16384 rows of 1000 bf16 take 70 us for the sums
+// and 122 with the gradient so, 185 and 275 with 256 lanes (of 2000, the longest: 103 and 215, 187 and 326).  A longer
+// row's gradient wants all of it in registers, in few lanes: of 32000 815 us with 512 lanes of 8 units, 830 with 256 of
+// 16, 865 with 1024 of 4 (8 x 4096 rows); beyond what registers hold tiles of 4 units cost less at the row's end than
+// those of 8: of 69632 266 us and 300, of 131072 273 and 277 (7 x 550 and 2 x 1024 rows), 300 and 296 with 512 of 4 and
+// 256 of 4.  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404 and 1024 of 4 496; with alternatives
+// 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows).  Where rows are too few to fill the chip, more lanes finish one
+// sooner: 64 rows of 32003 fp32 20 us with 1024 lanes, 26 with 256.
 template <class In, int MODE, int P>
 gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   if constexpr (P > 8) {
@@ -703,7 +705,7 @@ gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
       if (units <= 4 * 256) return launch_rows<In, MODE, 256, 4, P>(a, c);
       if (units <= 4 * 512) return launch_rows<In, MODE, 512, 4, P>(a, c);
       if (units <= 8 * 512) return launch_rows<In, MODE, 512, 8, P>(a, c);
-      return launch_rows<In, MODE, 1024, 8, P>(a, c);
+      return units <= 8 * 1024 ? launch_rows<In, MODE, 1024, 8, P>(a, c) : launch_rows<In, MODE, 1024, 4, P>(a, c);
     } else {
       int64_t rows = 0;
       for (int s = 0; s < c.nranks; ++s) rows += c.tokens[s];
