@@ -8,7 +8,7 @@ from oracle import token as K
 
 
 def test_philox_known_answers():
-    """Known answers published with the generator (Random123's kat_vectors, philox4x32 of 10 rounds)."""
+    """Known answers published with the generator (Salmon et al., SC 2011; four 32-bit words, 10 rounds)."""
     ones = 0xFFFFFFFF
     for counter, key, want in (
             ((0, 0, 0, 0), (0, 0), (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)),
