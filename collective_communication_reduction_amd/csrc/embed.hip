@@ -347,14 +347,13 @@ __device__ __forceinline__ int past(const int2* entries, int lo, int hi, int32_t
 }
 
 // VE sums times scale to a row of n elements: those from element `off` of its unit u (of UNIT elements) on.  With `add`
-// they go on top of what is there, each element from one lane alone: the row's last unit may overlap the one before and
-// leaves it those elements.
+// they go on top of what is there, each element from one lane alone: what the row's last unit shares with the one before,
+// which may be more than the first of its pieces, is left to that.
 template <class OutT, int VE, int UNIT>
 __device__ __forceinline__ void put_sums(char* row, uint32_t n, uint32_t u, uint32_t off, const float (&acc)[VE], float scale,
                                          bool add, bool through) {
   typedef AnyUnit<OutT, VE> W;
-  const uint32_t s = AnyUnit<OutT, UNIT>::start(n, u) + off;
-  const uint32_t here = n >= UNIT ? VE : n > off ? min(n - off, static_cast<uint32_t>(VE)) : 0;   // elements in the row
+  const uint32_t s = gci::unit_start(n, UNIT, u) + off, here = gci::unit_held(n, UNIT, off, VE);
   char* p = row + static_cast<uint64_t>(s) * OutT::ES;
   float v[VE];
 #pragma unroll
@@ -367,9 +366,9 @@ __device__ __forceinline__ void put_sums(char* row, uint32_t n, uint32_t u, uint
   W::widen(W::load(p, here, 0), old);
 #pragma unroll
   for (int e = 0; e < VE; ++e) v[e] += old[e];
-  const uint32_t own = u * UNIT + off;   // the first element that is this unit's
-  if (s == own) W::store(p, here, 0, W::narrow(v), through);
-  else W::store_some(p, min(own - s, static_cast<uint32_t>(VE)), VE, W::narrow(v));
+  const uint32_t shared = gci::unit_shared(n, UNIT, u, off, VE);
+  if (shared == 0) W::store(p, here, 0, W::narrow(v), through);
+  else W::store_some(p, shared, VE, W::narrow(v));
 }
 
 // Elements of a unit that is at most 16 bytes in either type, so that every store of a wavefront is one run of memory.

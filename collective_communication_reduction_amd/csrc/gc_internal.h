@@ -167,6 +167,19 @@ gc_status in_launches(uint64_t blocks, uint32_t threads, F one) {
   return GC_OK;
 }
 
+// A row of n elements is taken in units of `unit`; the last unit of one that is no multiple of it is moved inside the row and
+// overlaps the unit before.  A unit may be taken in pieces of `ve` elements, `off` elements into it.
+constexpr uint32_t unit_start(uint32_t n, uint32_t unit, uint32_t u) { return n < unit ? 0 : u * unit < n - unit ? u * unit : n - unit; }
+// Elements of a piece that lie in the row: all of them but in rows shorter than a unit.
+constexpr uint32_t unit_held(uint32_t n, uint32_t unit, uint32_t off, uint32_t ve) {
+  return n >= unit ? ve : n <= off ? 0 : n - off < ve ? n - off : ve;
+}
+// Of these, how many at the piece's front the unit before holds too: whoever adds to the row leaves them to it.
+constexpr uint32_t unit_shared(uint32_t n, uint32_t unit, uint32_t u, uint32_t off, uint32_t ve) {
+  const uint32_t s = unit_start(n, unit, u) + off, own = u * unit;   // own: the first element that only this unit holds
+  return own <= s ? 0 : own - s < ve ? own - s : ve;
+}
+
 // Bytes of an 8-bit row of n values: codes, a scale per 32 values, zeros to a multiple of 16.
 inline uint64_t mx8_row_bytes(uint64_t n) { return (n + (n + 31) / 32 + 15) / 16 * 16; }
 

@@ -20,7 +20,7 @@ struct AnyUnit {
   typedef typename std::conditional<In::ES == 2, uint16_t, uint32_t>::type E;
 
   // First element of unit u in a row of n.  Rows shorter than a unit have one at 0.
-  __device__ static __forceinline__ uint32_t start(uint32_t n, uint32_t u) { return n < VE ? 0 : min(u * VE, n - VE); }
+  __device__ static __forceinline__ uint32_t start(uint32_t n, uint32_t u) { return gci::unit_start(n, VE, u); }
   // VE elements from s on, in a row of n; in a row shorter than that all of it, and `fill` (an element's bits) behind.
   // KEEP: read again soon, may stay in the caches.
   template <bool KEEP = false>
