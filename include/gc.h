@@ -583,7 +583,8 @@ gc_status gc_token_logprob(const void* const* logits, const int32_t* const* targ
 /*
  * Gradient of the logits from the saved lse (and entropy, where dentropy is given):
  *   dlogits = scale * (dlogprob * ([token == target] - p) - dentropy * p * (log(p) + entropy)),
- * fp32, rounded once to t; columns vocab to stride - 1 get zeros.
+ * fp32, rounded once to t; columns vocab to stride - 1 get zeros.  So does, for any finite factors, a token of
+ * probability 0 (in fp32: below 2^-126) that is not the target.
  *   lse[r], entropy[r], dlogprob[r], dentropy[r]  DEVICE fp32 [ntokens[r]];
  *               dentropy may be NULL, then entropy is not read.  p is as exact as
  *               lse: of one beyond 2^20 in magnitude the fp32 value no longer tells
