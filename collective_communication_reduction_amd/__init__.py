@@ -701,7 +701,8 @@ def gc_embedding_backward(dout, tokens, ntokens, vocab, hidden, dweight, scratch
 def gc_dropout(x, counts, p, seed, y, offset=0, step=None, residual=None, dtype=None, stream=None):
     """y = residual + dropout(x) of each rank's counts[r] elements; y may be x or residual.  The mask follows from
     (seed, offset + step, rank, element) alone, so the gradient is the same call on y's gradient without residual.
-    step: an int64 device tensor of one value that a replayed graph may count up, or None."""
+    step: an int64 device tensor of one value that a replayed graph may count up, or None.  Dropouts with the same sum of
+    offset and step share a mask: give the l-th one of a step the offset l << 40 where steps count by one."""
     N, t = len(counts), _infer_dtype(x, dtype)
     nb = _rows_of(counts, _ES.get(t, 0))
     _check(_c_dropout(_bufs(x, N, nb, "x", t), _bufs(residual, N, nb, "residual", t), _i64_array(counts), N, float(p),

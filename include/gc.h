@@ -526,8 +526,11 @@ gc_status gc_embedding_backward(const void* const* dout, const int32_t* const* t
  * 2011), key (seed's low, high word) and counter (b's low word, b's high word +
  * 256 * rank, s's low, high word), b = i / 8, s = offset + *step, element i takes
  * half word i % 8 of the four result words (low halves first) and is kept where
- * that is at least d.  Ranks have masks of their own; calls that shall differ
- * (layers, steps) take different offsets or steps.
+ * that is at least d.  Ranks have masks of their own.  Of offset and *step only
+ * the sum counts: calls with the same seed share a mask exactly where their sums (modulo 2^64)
+ * are equal, as offset 0 at step 1 and offset 1 at step 0 do.  Dropouts that shall all
+ * differ need sums that never meet: offset l * 2^40 for the l-th dropout of a step
+ * where steps count by one, or offsets 0 .. n - 1 where *step counts by n.
  *   step      DEVICE pointer to one uint64 read when the kernel runs, or NULL for
  *             0: a replayed graph gets new masks by adding to it in between.
  *   y[r]      may be x[r] or residual[r] itself; no other overlap.
