@@ -55,11 +55,11 @@ extern "C" gc_status gc_embedding(const void* const* weight, const int32_t* cons
   return gci::launch_embedding({weight, tokens, ntokens, nranks, vocab, hidden, scale, t, out, stream});
 }
 
-// Ranks of at most 2048 tokens are sorted by one workgroup each, in one launch (a gradient of 2048 x 256 takes 25 us so,
-// 29 in pieces; 4096 x 256 35 and 30); longer ones by a workgroup per 1024 tokens (two of each lane), more where a rank
+// Ranks of at most 2048 tokens are sorted by one workgroup each, in one launch (a gradient of 2048 x 256 takes 26 us so,
+// 28 in pieces; 4096 x 256 35 and 31); longer ones by a workgroup per 1024 tokens (two of each lane), more where a rank
 // would make over 256 pieces: every piece reads the counts of all the others.  A group of lanes sums a run of 8 sorted
 // tokens where they are few, for more groups (517 x 1000 fp32: 16 us, 28 with 64), and of up to 64 where those are a
-// thousand, for fewer partial sums (8 x 16384 x 4096 bf16, frequent tokens: 587 us, 604 with 8; none frequent: 635, 608).
+// thousand, for fewer partial sums (8 x 16384 x 4096 bf16, frequent tokens: 584 us, 599 with 8; none frequent: 642, 604).
 gci::EmbeddingGeom gci::embedding_geom(const int64_t* tokens, int nranks, uint64_t vocab, uint64_t hidden) {
   gci::EmbeddingGeom g;
   int64_t most = 0;
@@ -174,7 +174,8 @@ gc_status logprob_check(const gci::LogprobCall& c, Buffers& b) {
 namespace {
 
 // A workgroup per row leaves most of the chip idle where there are few rows.  Few long ones are cut into parts of 8192
-// logits or more, 256 parts in all, for a second launch to join; one row of 32000 takes as long whole.
+// logits or more, 256 parts in all, for a second launch to join; one row of 32000 with 20 alternatives takes 12 us
+// whole and 14 in four parts, 64 rows of 131072 33 in parts and 32 whole.
 int logprob_parts(const int64_t* ntokens, int nranks, size_t vocab) {
   int64_t rows = 0;
   for (int r = 0; r < nranks; ++r) rows += ntokens[r];

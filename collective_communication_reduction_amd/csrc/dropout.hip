@@ -53,8 +53,8 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
 // A lane takes one unit, a whole generator block of bf16 elements or half of one of
 // fp32: with both halves in one lane each of its stores would leave every other 16
 // bytes to the next store (2.4 TB/s instead of 6).  A workgroup takes kThreads units.
-// HBM bounds it: 8 x 16384 x 4096 bf16 with residual 496 us, 6.5 TB/s, as the library's
-// copies; 4 ranks of as many fp32 values 500 us.
+// HBM bounds it: 8 x 16384 x 4096 bf16 with residual 500 us, 6.4 TB/s, near the library's
+// copies; 4 ranks of as many fp32 values 506 us.
 template <class In, bool RES, int P>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs<P> a) {
   typedef AnyUnit<In> U;

@@ -6,9 +6,9 @@
 // digits of the id), so that each row's terms are added in token order whatever
 // the timing: results repeat bit for bit, and no atomic touches a gradient.
 //
-// HBM bytes bound both.  8 x 16384 rows of 4096 bf16 from a vocabulary of 32000: the lookup takes 256 us (1.07 GB written,
-// of the weight only what occurs read: 5.1 TB/s), the gradient 591: sums and cleared rows 551 (3.17 GB read and written,
-// 5.8 TB/s), sort 23, long rows 10.
+// HBM bytes bound both.  8 x 16384 rows of 4096 bf16 from a vocabulary of 32000: the lookup takes 242 us (1.07 GB written,
+// of the weight only what occurs read: 5.5 TB/s; 227 to 261 by the card and by where the frequent rows lie), the gradient 566 (561 to
+// 596): sums and cleared rows 537 to 558 (3.17 GB read and written, 5.7 to 5.9 TB/s), sort 23, long rows 10.
 
 #include <algorithm>
 #include <type_traits>
@@ -21,9 +21,9 @@ using namespace gcdev;
 
 // ------------------------------------------------------------- lookup
 //
-// Up to a wavefront of lanes share a row's slice, each with up to four units in flight: rows of 4096 bf16 take 336 us so
-// and 375 with one unit a lane and eight slices (8 x 16384 distinct rows), 267 and 298 with eight units a lane (rows that
-// repeat).  The weight may stay in the caches, frequent tokens being read again: 267 us, 291 with streaming loads.
+// Up to a wavefront of lanes share a row's slice, each with up to four units in flight: 8 x 16384 rows of 4096 bf16
+// that repeat take 227 us so, 337 with one unit a lane and eight slices, 279 with eight units a lane (distinct rows 385, 388
+// and 401).  The weight may stay in the caches, frequent tokens being read again: 227 us, 271 with streaming loads.
 
 template <int P>
 struct EmbeddingArgs {
@@ -619,8 +619,8 @@ gc_status row_sums(RowSumArgs<P>& r, bool long_rows, hipStream_t stream) {
   r.slices = static_cast<uint32_t>((r.units + per - 1) / per);
   r.sum_blocks = ((runs * r.slices << r.lanes_log2) + kThreads - 1) / kThreads;
   const uint64_t row = r.H * OutT::ES, rows = static_cast<uint64_t>(r.N) * r.vocab;
-  // about 64 bytes per lane of a clearing group: 131072 rows of 4096 bf16 of which 4096 tokens use some take 193 us,
-  // 228 with 16 or 256 bytes; a million rows of 64 62 us, 70 and 69
+  // about 64 bytes per lane of a clearing group: 131072 rows of 4096 bf16 of which 4096 tokens use some take 180 us,
+  // 224 with 16 or 256 bytes; a million rows of 64 54 us, 62 and 60
   const uint64_t lane_bytes = row >> r.lanes_log2;
   r.clear_rows = static_cast<uint32_t>(std::max<uint64_t>(1, 64 / std::max<uint64_t>(1, lane_bytes)));
   const uint64_t groups = (rows + r.clear_rows - 1) / r.clear_rows;
@@ -699,8 +699,8 @@ gc_status embedding_backward_typed(const gci::EmbeddingBackwardCall& c) {
   r.accumulate = c.accumulate;
   r.lanes_log2 = 3;
   while (r.lanes_log2 < 8 && (uint64_t(1) << r.lanes_log2) < r.units) ++r.lanes_log2;
-  // Two units per lane where that makes no more idle lanes than one: rows of 4096 bf16 244 us against 257, of 8192 478
-  // against 493; where it does, one: of 4608 285 us against 331, of 6144 371 against 379 (4 x 8192 rows).
+  // Two units per lane where that makes no more idle lanes than one: rows of 4096 bf16 245 us against 258, of 8192 480
+  // against 490; where it does, one: of 4608 287 us against 326, of 6144 372 against 380 (4 x 8192 rows).
   const uint64_t slices = (r.units + kThreads - 1) / kThreads;
   return slices % 2 ? row_sums<In, OutT, 1, P>(r, long_rows, c.stream) : row_sums<In, OutT, 2, P>(r, long_rows, c.stream);
 }

@@ -10,9 +10,12 @@
 // sums are joined at the end.  Longer rows go through the registers in tiles, and
 // only their gradient reads them again.  HBM bytes bound it, with about ten vector
 // operations a value, four of them the exponential's quarter rate, close behind:
-// 8 x 4096 rows of 32000 bf16 take 360 us for the sums (5.8 TB/s), 721 with the
-// gradient (5.8 TB/s, read and written); 4 x 2048 rows with five alternatives 110
-// (4.8 TB/s); the gradient from a saved lse of 2 x 1024 x 131072 180 (6.0 TB/s).
+// 8 x 4096 rows of 32000 bf16 take 316 us for the sums (6.6 TB/s), 729 with the
+// gradient (5.8 TB/s, read and written); 4 x 2048 rows with five alternatives 108
+// (4.9 TB/s); the gradient from a saved lse of 2 x 1024 x 131072 178 (6.0 TB/s).
+// All times here are of calls queued one after the other on one card (short ones
+// replayed from a graph); others differ by up to 5 %, and kernels that a profiler
+// runs one at a time take up to a quarter longer.
 
 #include <type_traits>
 
@@ -672,8 +675,8 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(const LogprobArg
 }
 
 // The gradient from the saved lse and entropy, kSlice units of a row per lane group: workgroups that run side by side
-// then read and write memory side by side (sums, then gradient of 2 x 1024 x 131072 bf16: 281 us,
-// 327 with a workgroup per row).
+// then read and write memory side by side (2 x 1024 x 131072 bf16: 178 us, 212 with a workgroup per row; 8 x 4096 x 32000
+// 786 and 803).
 constexpr int kSlice = 4;   // units per lane
 
 template <class In, int LANES, int P>
@@ -712,14 +715,17 @@ gc_status launch_rows(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   return launch_blocks(logprob_kernel<In, LANES, NV, MODE, false, P>, a, a.tile0[c.nranks], threads, c.stream);
 }
 
-// Lanes of a row and their units.  A wavefront holds a short row: 8 x 16384 rows of 1000 bf16 take 70 us for the sums
-// and 122 with the gradient so, 185 and 275 with 256 lanes (of 2000, the longest: 103 and 215, 187 and 326).  A longer
-// row's gradient wants all of it in registers, in few lanes: of 32000 815 us with 512 lanes of 8 units, 830 with 256 of
-// 16, 865 with 1024 of 4 (8 x 4096 rows); beyond what registers hold tiles of 4 units cost less at the row's end than
-// those of 8: of 69632 266 us and 300, of 131072 273 and 277 (7 x 550 and 2 x 1024 rows), 300 and 296 with 512 of 4 and
-// 256 of 4.  Sums alone stream: 365 us with 256 lanes of 4 where 512 of 8 take 404 and 1024 of 4 496; with alternatives
-// 256 of 8 take 151 us, 512 of 4 183 (4 x 2048 rows).  Where rows are too few to fill the chip, more lanes finish one
-// sooner: 64 rows of 32003 fp32 20 us with 1024 lanes, 26 with 256.
+// Lanes of a row and their units.  A wavefront holds a short row: 8 x 16384 rows of 1000 bf16 take 73 us for the sums
+// and 121 with the gradient so, 192 and 277 with 256 lanes (of 2000, the longest: 108 and 218, 196 and 332).  A longer
+// row's gradient wants all of it in registers, in few lanes: of 8192 183 us with 256 lanes of 4 units, 215 with 512; of
+// 16384 368 with 512 of 4, 398 of 8; of 32000 728 with 512 of 8, 759 with 256 of 16, 775 with 1024 of 4 (8 x 4096 rows).
+// Beyond what registers hold tiles of 4 units cost less at the row's end than those of 8: of 69632 264 us and 299, of
+// 131072 273 and 274 (7 x 550 and 2 x 1024 rows), 300 and 292 with 512 of 4, 314 and 297 with 256 of 4.  Sums alone
+// stream: 316 us with 256 lanes of 4, 314 of 8, 335 with 512 of 8, 366 with 1024 of 4; with five alternatives 256 of 8
+// take 108 us, of 4 126, 512 of 4 144 (4 x 2048 rows).  Where rows are too few to fill the chip, more lanes finish one
+// sooner: 64 rows of 32003 fp32 5.3 us with 1024 lanes, 9.7 with 256, with five alternatives 12.7 and 19.3.
+// More than 8 ranks have one form, chosen for the size of the library and not by time: 64 x 2048 rows of 1000 take 906
+// us and with the gradient 1075, as 8 x 16384 76 and 127; 64 x 512 of 32000 387 and 777, as 8 x 4096 325 and 729.
 template <class In, int MODE, int P>
 gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   if constexpr (P > 8) {
@@ -741,7 +747,7 @@ gc_status launch_mode(LogprobArgs<P>& a, const gci::LogprobCall& c) {
   }
 }
 
-// Few rows: a workgroup per part, and one per row that joins them (one row of 131072 bf16 with 20 alternatives: 21 us, 36
+// Few rows: a workgroup per part, and one per row that joins them (one row of 131072 bf16 with 20 alternatives: 13 us, 25
 // by one workgroup).
 template <class In, int P>
 gc_status launch_parts(LogprobArgs<P>& a, const gci::LogprobCall& c) {

@@ -46,9 +46,9 @@ struct AnyUnit {
   }
   // VE elements from s on, or all of a shorter row.  through: to memory, past the L2; for rows that all start on a
   // line of memory (kLine).  Others share lines with their neighbours and are left to meet there.  Rows of 4092 fp32,
-  // whole units but not lines, take less time so (lookup 397 us against 437, its gradient 765 against 872, 8 x 16384 rows).
-  // Rows of whole lines take less through: the lookup of 8 x 16384 x 4096 bf16 from distinct rows 330 us against 368, its
-  // gradient 582 against 646, dropout 499 against 515.  And a line that is written both ways takes a multiple (rows of
+  // whole units but not lines, take less time so (lookup 619 us against 711, its gradient 1406 against 1668, 8 x 16384 rows).
+  // Rows of whole lines take less through: the lookup of 8 x 16384 x 4096 bf16 from distinct rows 383 us against 410, its
+  // gradient 584 against 650, dropout 501 against 520.  And a line that is written both ways takes a multiple (rows of
   // 4095 bf16: 0.8 TB/s where the units on a 16-byte boundary went through, 5.4 where none did).
   __device__ static __forceinline__ void store(char* row, uint32_t n, uint32_t s, T v, bool through) {
     char* p = row + static_cast<uint64_t>(s) * In::ES;
